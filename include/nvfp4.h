@@ -73,7 +73,7 @@ typedef enum {
     NVFP4_ERR_ARCH = -5,      /* current device is not compute capability 10.0 (B200) */
     NVFP4_ERR_LAUNCH = -6,    /* the CUDA launch failed (cudaGetLastError) */
     NVFP4_ERR_WORKSPACE = -7, /* workspace NULL, misaligned or smaller than required */
-    NVFP4_ERR_ALIAS = -8      /* a prologue's residual output overlaps what the call reads or y */
+    NVFP4_ERR_ALIAS = -8      /* an output overlaps what the call reads or another output */
 } nvfp4_status;
 
 #define NVFP4_MAX_ROWS 128 /* rows of x (and y) per call */
@@ -382,6 +382,130 @@ int nvfp4_gemv_chain_owner_wait(const nvfp4_chain_op_t* ops, int count, int m, v
  * and the prologue's x' (M x K bf16).  Zero-filled before first use, like any workspace.
  * NVFP4_ERR_NULL, NVFP4_ERR_SHAPE (as nvfp4_gemv), NVFP4_ERR_ROWS, NVFP4_ERR_ARCH. */
 int nvfp4_workspace_bytes_wide(int64_t n, int64_t k, int m, size_t* bytes);
+
+/* ---- Paged key/value cache, attention and adapters --------------------------------------------
+ * The operators of a decode step that stand between the projections: block tables and slot maps
+ * for a batch of requests, new key and value rows into the paged cache, the attention that reads
+ * it, and low-rank adapters beside a projection.  The decode plan launches the middle two as
+ * reshape_and_cache and paged_decode_attn ("Blueprint - circuit executor" page for
+ * qwen3.8-27b-nvfp4 on GB10, table "Kernels the plan launches"); the formulas are the standard
+ * ones.  Lengths, tables and indexes are device memory, so a captured call serves later values.
+ * They are taken within bounds: an index outside its range is skipped as each call says, never
+ * followed.  Results are the same in every run.
+ */
+#define NVFP4_MAX_REQUESTS 8192
+
+#define NVFP4_KV_BF16 0
+#define NVFP4_KV_E4M3 1 /* e4m3 (FN) codes; the value is code * k_scale (v_scale) */
+
+/* A paged cache: `blocks` pages of block_size slots, each a row of `dim` values per kv head.
+ * Element (page, slot, head, i) of K lies at k + (page * block_stride + slot * slot_stride +
+ * head * head_stride + i) elements, and V likewise from v, so [page][slot][head][dim] and
+ * [page][head][slot][dim], K and V apart or page by page in one buffer, all fit.
+ *   type: NVFP4_KV_BF16 or NVFP4_KV_E4M3;  dim: 64, 128 or 256;  heads: 1..1024
+ *   block_size: a multiple of 16, at most 2^20;  blocks * block_size < 2^31
+ *   k, v 16-byte aligned;  every stride >= dim and a multiple of 16 bytes
+ *   k_scale, v_scale: > 0 and finite (NVFP4_KV_E4M3; ignored otherwise) */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t type;
+    int32_t heads;
+    int32_t dim;
+    int32_t block_size;
+    int64_t blocks;
+    int64_t block_stride, slot_stride, head_stride; /* elements */
+    float k_scale, v_scale;
+} nvfp4_kv_cache_t;
+
+/* Block tables and slot maps from request lengths.  For request r with lens[r] tokens in the
+ * cache and new_tokens[r] to come (negative counts as 0), b = block_size:
+ *   starts[r]   = new_tokens[0] + ... + new_tokens[r-1], starts[requests] the total
+ *   lens_out[r] = lens[r] + new_tokens[r]
+ *   pages       = table columns [ceil(lens/b), min(ceil(lens_out/b), table_columns)) are filled
+ *                 from the free list: free_pages[head], free_pages[head + 1], ... in request
+ *                 order; -1 where the list is spent.  Other entries stay as they were.
+ * and for token t, starts[r] <= t < starts[r+1], at pos = lens[r] + t - starts[r]:
+ *   slots[t] = table[r][pos / b] * b + pos % b, or -1 if there is no such page;
+ *   request[t] = r;  positions[t] = pos
+ * Entries t >= starts[requests] are -1, -1 and 0, so rows padded to `tokens` are inert in
+ * nvfp4_kv_append and nvfp4_lora_add.  A batch of more than `tokens` tokens gets the first ones.
+ *   head_out[0] = head[0] + the pages taken;  missing[0] = pages wanted and not there (the list
+ *   spent, or beyond table_columns).
+ * Sums are formed in 64 bits and stored saturated at 2^31 - 1; a slot of 2^31 or more is -1. */
+typedef struct {
+    const int32_t* lens;       /* [requests] */
+    const int32_t* new_tokens; /* [requests] */
+    int32_t requests;          /* 0..NVFP4_MAX_REQUESTS */
+    int32_t block_size;        /* >= 1 */
+    int32_t* table;            /* [requests][ld_table], filled in place */
+    int64_t ld_table;          /* >= table_columns */
+    int64_t table_columns;
+    const int32_t* free_pages; /* [free_count] */
+    int64_t free_count;
+    const int32_t* head;       /* [1]: how many of free_pages are taken already */
+    int64_t tokens;            /* length of slots, request and positions */
+    int32_t* starts;           /* [requests + 1] */
+    int32_t* lens_out;         /* [requests] */
+    int32_t* slots;            /* [tokens] */
+    int32_t* request;          /* [tokens], or NULL */
+    int32_t* positions;        /* [tokens], or NULL */
+    int32_t* head_out;         /* [1] */
+    int32_t* missing;          /* [1] */
+} nvfp4_paged_plan_t;
+
+/* Errors: NVFP4_ERR_NULL, NVFP4_ERR_SHAPE, NVFP4_ERR_ALIGN (4 bytes), NVFP4_ERR_ALIAS (an output
+ * overlaps an input or another output: lens_out and head_out are not written in place),
+ * NVFP4_ERR_ARCH, NVFP4_ERR_LAUNCH; all checked before anything is enqueued. */
+int nvfp4_paged_plan(const nvfp4_paged_plan_t* plan, cudaStream_t stream);
+
+/* New key and value rows into the cache: row t of k and v (bf16, head h at k + t*ldk +
+ * h*k_head_stride) goes to slot slots[t], i.e. page slots[t] / block_size; rows whose slot is
+ * negative or past the last page are skipped.  An e4m3 cache stores e4m3_rn(x / scale) of the
+ * fp32 quotient, saturated at +-448 (NaN stays NaN).  Slots that occur twice leave, value by
+ * value, one of their rows.
+ *   k, v 16-byte aligned;  strides >= dim and multiples of 8;  the cache overlaps no input.
+ * Errors: NVFP4_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARCH, _LAUNCH. */
+int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const void* v, int64_t ldv,
+                    int64_t v_head_stride, int64_t tokens, const int32_t* slots,
+                    const nvfp4_kv_cache_t* cache, cudaStream_t stream);
+
+/* Attention of each request's newest tokens over its paged cache, in which they already lie.
+ * Tokens starts[r] .. starts[r+1]-1 are the last n of request r's lens[r]; token i of them is at
+ * position p = lens[r] - n + i and sees the keys j <= p of its request:
+ *   o[t][h] = bf16( sum_j w_j v_j / sum_j w_j ),  w_j = exp(scale * (q[t][h] . k_j))
+ * with kv head h / (heads / cache->heads), key j at slot j % block_size of page
+ * table[r][j / block_size].  Keys whose page is not in 0..blocks-1, or lies beyond table_columns,
+ * are not there; a token that sees no key gives zeros.  Rows of o behind the last token stay as
+ * they were.  What cache slots hold that no token sees has no effect, whatever it is.
+ *   q, o: bf16, head h of token t at q + t*ldq + h*q_head_stride; 16-byte aligned, strides
+ *   multiples of 8 and >= dim; o may not overlap q.   heads % cache->heads == 0
+ *   scale: > 0 (scale * k_scale a normal fp32 number) */
+typedef struct {
+    const void* q;
+    int64_t ldq, q_head_stride;
+    void* o;
+    int64_t ldo, o_head_stride;
+    int64_t tokens;           /* rows of q and o */
+    int32_t heads;
+    int32_t requests;         /* 0..NVFP4_MAX_REQUESTS */
+    const int32_t* table;     /* [requests][ld_table] */
+    int64_t ld_table, table_columns;
+    const int32_t* starts;    /* [requests + 1], ascending; cut to 0..tokens */
+    const int32_t* lens;      /* [requests] */
+    float scale;
+} nvfp4_paged_attn_t;
+
+/* Workspace bytes of nvfp4_paged_attn for this head dim on the current device (parts of the rows
+ * that its split of the keys cuts: 39 MB at dim 256 on a 148-SM B200). */
+int nvfp4_paged_attn_workspace_bytes(int dim, size_t* bytes);
+
+/* workspace: 16-byte aligned, the above bytes, zero-filled before first use (its first word is
+ * the error word of nvfp4_workspace_error: 5..9, a bounded wait gave up and the results are
+ * invalid).  Calls that may run at the same time need different workspaces.
+ * Errors: NVFP4_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _WORKSPACE, _ARCH, _LAUNCH. */
+int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cache,
+                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* The workspace's error word after the work enqueued so far has run (synchronises the
  * stream): 0 if no kernel hit a bounded wait's limit, else a nonzero code -- 2 or 3: a wait on

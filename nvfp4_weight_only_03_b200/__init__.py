@@ -24,6 +24,9 @@ import os
 import torch
 
 from . import build as _build
+from . import serving as _serving
+from .serving import (KV_BF16, KV_E4M3, MAX_REQUESTS, PagedPlan, kv_append, paged_attention,
+                      paged_attention_workspace_bytes, paged_plan)
 
 _LIB_PATH = _build.LIB
 _lib = None
@@ -189,6 +192,7 @@ def lib():
                   L.nvfp4_chain_workspace_bytes, L.nvfp4_gemv_chain,
                   L.nvfp4_gemv_chain_unsignalled, L.nvfp4_gemv_chain_owner_wait):
             f.restype = c_int
+        _serving.declare(L)
         _lib = L
     return _lib
 

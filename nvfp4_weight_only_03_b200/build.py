@@ -6,9 +6,11 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", "nvfp4_gemv.cu"), os.path.join(HERE, "csrc", "nvfp4_gemv_tc.cu")]
-HDRS = [os.path.join(ROOT, "include", "nvfp4.h"), os.path.join(HERE, "csrc", "nvfp4_tc.h"),
-        os.path.join(HERE, "csrc", "nvfp4_prologue.h")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in
+        ("nvfp4_gemv.cu", "nvfp4_gemv_tc.cu", "nvfp4_paged.cu", "nvfp4_attn.cu")]
+HDRS = [os.path.join(ROOT, "include", "nvfp4.h")] + \
+       [os.path.join(HERE, "csrc", f) for f in
+        ("nvfp4_tc.h", "nvfp4_prologue.h", "nvfp4_host.h", "nvfp4_ptx.h")]
 LIB = os.path.join(HERE, "libnvfp4gemv.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

@@ -1,0 +1,991 @@
+// Attention of each request's newest tokens over its paged key/value cache (nvfp4_paged_attn):
+// one token of a decode step, the rows of a verify round, a prefill chunk.  The decode plan
+// launches it as paged_decode_attn ("Blueprint - circuit executor" page for qwen3.8-27b-nvfp4 on
+// GB10, table "Kernels the plan launches").
+//
+//   token i of request r's n new ones: p = len - n + i
+//   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j),  over the keys j <= p that have a page
+//
+// * Rows: the query heads that share a kv head are rows of one matrix product, row g of a request
+//   being (token g / G, head g % G); 128 rows are a tile (the MMA's M), so a key or value row
+//   leaves HBM once per tile and kv head.  A decode step fills 6 of the 128 rows: the tensor
+//   cores have the time (512 cycles of MMA against some 2500 of HBM per 64 KB of cache), and one
+//   kernel serves every row count.
+// * Work: units of TK keys of one (request, kv head, row tile).  All units in order are cut into
+//   equal ranges, one per CTA (one CTA per SM), from the lengths in device memory: the host knows
+//   none of them, so a captured call serves every later length.  A tile that a range boundary
+//   cuts leaves (max, sum, O) in the workspace, and a second kernel joins the parts in order.
+//   No atomics: results are the same in every run.
+// * One pass over the cache: S = Q K^T in tensor memory, one thread per row keeps the running
+//   maximum and sum, P goes back to tensor memory as the A operand of O += P V.  O stays in tensor
+//   memory; it is rescaled only when a row's maximum rose by more than 2^8 (P is then at most
+//   2^8 and the sums are fp32, so nothing overflows).  S and P have two buffers each, so the MMAs
+//   of one unit run under the softmax of another.
+// * Roles: 4 softmax warps, 1 MMA warp, 1 TMA warp, 2 warps that gather Q, and 4 that widen an
+//   e4m3 cache to f16 (exact); the bf16 cache goes to the MMA as it lies in memory.
+// * P is rounded to the MMA's 16-bit type (bf16, or f16 with the e4m3 cache): half a step, 2^-9
+//   (2^-12) of each weight.  With the e4m3 cache q is carried as f16 times a power of two per row.
+//   S, O, maxima and sums are fp32.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "nvfp4.h"
+#include "nvfp4_host.h"
+#include "nvfp4_ptx.h"
+
+namespace nvfp4_host {
+int check_cache(const nvfp4_kv_cache_t* c);
+}
+
+namespace {
+
+using namespace nvfp4_ptx;
+using nvfp4_host::misaligned;
+using nvfp4_host::overlaps;
+
+constexpr int kRows = 128;  // rows of a tile: the MMA's M and tensor memory's lanes
+constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kTmaWarp = 5, kQWarp = 6, kQWarps = 2;
+constexpr int kWidenWarp = 8, kWidenWarps = 4;
+constexpr int kTmemCols = 512;
+constexpr size_t kSmemBudget = 229376;  // of 232448: the rest holds barriers and 1 KB alignment
+
+template <int D, bool F8>
+struct Cfg {
+    static constexpr int TK = D == 256 ? 64 : 128;          // keys per unit
+    static constexpr int kPanels = D / 64;                  // 128-byte panels of a row
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kTile = TK * D * 2;                // one K or V tile, 16-bit
+    static constexpr int kRaw = F8 ? TK * D : 0;            // the same in e4m3
+    static constexpr int kThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kQWarp + kQWarps);
+    static constexpr int kStages =
+        F8 ? (D == 64 ? 4 : 3) : (int)((kSmemBudget - kQBytes) / kTile);
+    static constexpr int kRawStages =
+        F8 ? (int)((kSmemBudget - kQBytes - kStages * kTile) / (F8 ? kRaw : 1)) : 1;
+    static constexpr size_t kSmem =
+        1024 + kQBytes + (size_t)kStages * kTile + (F8 ? (size_t)kRawStages * kRaw : 0);
+    // tensor memory columns: O, then two S, then two P (two 16-bit values per column)
+    static constexpr int kS = D, kP = D + 2 * TK, kEnd = D + 2 * TK + TK;
+    static_assert(kEnd <= kTmemCols, "tensor memory");
+    static_assert(kSmem <= kSmemBudget + 1024, "shared memory");
+};
+
+// A row tile that was cut: its parts lie with the CTAs `owner` (which holds its first unit) to
+// owner + parts - 1.
+struct Cut {
+    int32_t parts;  // 0: this CTA owns none
+    int32_t token0, row0, rows, head;
+    int32_t pad[3];
+};
+
+struct Params {
+    const uint16_t* q;
+    int64_t ldq, q_head_stride;
+    uint16_t* o;
+    int64_t ldo, o_head_stride;
+    const int32_t* table;
+    int64_t ld_table;
+    const int32_t *starts, *lens;
+    int requests, tokens, kv_heads, group, block, blocks, box;
+    int outside;       // a page index past the tensor: its boxes arrive as zeros
+    int capacity;      // keys that a table row can hold
+    int min_units;     // fewest units worth a CTA of their own
+    float c;           // scale * k_scale * log2(e)
+    float v_scale;
+    int32_t* error;
+    Cut* cuts;         // [grid]
+    float2* part_ml;   // [grid][2][128]: maximum (log2 domain) and sum
+    float* part_o;     // [grid][2][128][D]
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
+    uint32_t r;
+    if (f16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---- the order of the work ---------------------------------------------------------------
+
+struct Request {
+    int token0, n, len;  // first token, new tokens, tokens in the cache (the new ones included)
+};
+
+// Device data is taken as it is, within bounds: a request outside [0, tokens] is cut to it.
+__device__ __forceinline__ Request request_of(const Params& p, int r) {
+    Request q;
+    q.token0 = min(max(p.starts[r], 0), p.tokens);
+    q.n = min(max(p.starts[r + 1], q.token0), p.tokens) - q.token0;
+    q.len = max(p.lens[r], 0);
+    return q;
+}
+
+__device__ __forceinline__ int row_tiles(const Params& p, const Request& q) {
+    return (int)(((int64_t)q.n * p.group + kRows - 1) / kRows);
+}
+
+// Keys below this are loaded for a row tile: the last row's own position, within the table.
+__device__ __forceinline__ int key_end(const Params& p, const Request& q, int tile) {
+    const int64_t rows = min((int64_t)(tile + 1) * kRows, (int64_t)q.n * p.group);
+    const int last = (int)((rows - 1) / p.group);
+    return min(max(q.len - q.n + last + 1, 0), p.capacity);
+}
+
+template <int TK>
+__device__ __forceinline__ int units_of(const Params& p, const Request& q, int tile) {
+    return max(1, (key_end(p, q, tile) + TK - 1) / TK);  // 1: rows without keys are written too
+}
+
+template <int TK>
+struct Cursor {
+    int r, h, tile, tiles, u, n;  // unit u of the row tile's n
+    Request q;
+    __device__ __forceinline__ void enter(const Params& p) {
+        tiles = row_tiles(p, q);
+        n = units_of<TK>(p, q, tile);
+    }
+    __device__ __forceinline__ void next(const Params& p) {  // the next row tile
+        u = 0;
+        if (++tile == tiles) {
+            tile = 0;
+            if (++h == p.kv_heads) {
+                h = 0;
+                do {
+                    if (++r >= p.requests) return;  // the last one: nothing is left to do
+                    q = request_of(p, r);
+                } while (q.n == 0);
+                tiles = row_tiles(p, q);
+            }
+        }
+        n = units_of<TK>(p, q, tile);
+    }
+};
+
+struct Range {
+    int64_t begin, end, total;
+    int ctas;
+};
+
+__device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int c) {
+    return total * c / ctas;
+}
+
+// This CTA's units and the row tile they start in.  Every thread sums the units of a run of
+// requests; the thread that holds the first one walks to it.
+template <int TK, int THREADS>
+__device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, int64_t* sums) {
+    const int tid = threadIdx.x;
+    const int per = (p.requests + THREADS - 1) / THREADS;
+    const int r0 = min(tid * per, p.requests), r1 = min(r0 + per, p.requests);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Request q = request_of(p, r);
+        const int tiles = row_tiles(p, q);
+        int64_t s = 0;
+        for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t);
+        mine += s * p.kv_heads;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t a = __shfl_up_sync(~0u, incl, d);
+        if ((tid & 31) >= d) incl += a;
+    }
+    if ((tid & 31) == 31) sums[tid >> 5] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < (tid >> 5)) before += sums[w];
+        total += sums[w];
+    }
+    before += incl - mine;
+    Range g;
+    g.total = total;
+    const int64_t most = (total + p.min_units - 1) / p.min_units;
+    g.ctas = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
+    g.begin = g.end = 0;
+    if ((int)blockIdx.x < g.ctas) {
+        g.begin = range_begin(total, g.ctas, blockIdx.x);
+        g.end = range_begin(total, g.ctas, blockIdx.x + 1);
+    }
+    if (g.end > g.begin && before <= g.begin && g.begin < before + mine) {
+        int64_t at = g.begin - before;
+        for (int r = r0; r < r1; ++r) {
+            const Request q = request_of(p, r);
+            const int tiles = row_tiles(p, q);
+            int64_t s = 0;
+            for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t);
+            if (at >= s * p.kv_heads) {
+                at -= s * p.kv_heads;
+                continue;
+            }
+            Cursor<TK> c;
+            c.r = r;
+            c.q = q;
+            c.h = (int)(at / s);
+            at -= c.h * s;
+            c.tile = 0;
+            while (at >= units_of<TK>(p, q, c.tile)) at -= units_of<TK>(p, q, c.tile++);
+            c.u = (int)at;
+            c.enter(p);
+            *start = c;
+            break;
+        }
+    }
+    __syncthreads();
+    return g;
+}
+
+// ---- the kernel --------------------------------------------------------------------------
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
+    nvfp4_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v) {
+    using C = Cfg<D, F8>;
+    constexpr int TK = C::TK, NS = C::kStages, NR = C::kRawStages;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* const base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* const q_tile = base;
+    uint8_t* const ring = base + C::kQBytes;
+    uint8_t* const raw = ring + NS * C::kTile;
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[NR], q_full,
+        q_free, s_full[2], p_full[2], pv_done, o_full, o_free, drained;
+    __shared__ uint32_t tmem_base;
+    __shared__ int stop;
+    __shared__ int64_t sums[C::kThreads / 32];
+    __shared__ Cursor<TK> start;
+    __shared__ float q_scale[2][kRows];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_base)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], F8 ? kWidenWarps * 32 : 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], kWidenWarps * 32);
+        }
+        mbar_init(&q_full, kQWarps * 32);
+        mbar_init(&q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], kSoftmaxWarps * 32);
+        }
+        mbar_init(&pv_done, 1);
+        mbar_init(&o_full, 1);
+        mbar_init(&drained, 1);
+        mbar_init(&o_free, kSoftmaxWarps * 32);
+        stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+    }
+    tc_before_sync();
+    const Range range = find_range<TK, C::kThreads>(p, &start, sums);  // two __syncthreads
+    tc_after_sync();
+    const uint32_t tmem = tmem_base;
+    volatile int* const stop_v = &stop;
+    int64_t left = range.end - range.begin;
+    Cursor<TK> cur = start;
+    bool ok = true;
+    int code = 0;
+
+    if (left == 0) {
+        if (tid == 0) p.cuts[blockIdx.x].parts = 0;
+    } else if (warp == kTmaWarp) {
+        // ---- K and V tiles, in the order of the MMAs: K0 K1 V0 K2 V1 ... V(n-1).  Lane i copies
+        // box i of a tile: `box` keys of one page (and 64 values of them); keys past the end, and
+        // pages that do not exist, are boxes outside the tensor, which arrive as zeros.
+        const int groups = TK / p.box;
+        constexpr int kInner = F8 ? 1 : C::kPanels;
+        const int boxes = groups * kInner;
+        const int g_of = lane % groups, panel = lane / groups;
+        int it = 0;
+        while (left > 0 && ok) {
+            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+            const int end = key_end(p, cur.q, cur.tile);
+            const int32_t* const row = p.table + cur.r * p.ld_table;
+            auto page_at = [&](int j) {  // page of this lane's keys in unit j of the range
+                const int key = (cur.u + j) * TK + g_of * p.box;
+                if (j >= cnt || key >= end) return -1;
+                const int page = row[key / p.block];
+                return (unsigned)page < (unsigned)p.blocks ? page : -1;
+            };
+            auto load = [&](const CUtensorMap* map, int j, int page) {
+                constexpr int N = F8 ? NR : NS;
+                const int slot = it % N;
+                uint64_t* const fb = F8 ? &raw_full[slot] : &full[slot];
+                uint64_t* const eb = F8 ? &raw_empty[slot] : &empty[slot];
+                if (it >= N && !mbar_wait(eb, (it / N - 1) & 1, stop_v)) {
+                    ok = false;
+                    return;
+                }
+                if (lane == 0) mbar_expect_tx(fb, F8 ? C::kRaw : C::kTile);
+                __syncwarp();
+                const int key = (cur.u + j) * TK + g_of * p.box;
+                const int w = page < 0 ? p.outside : page;
+                uint8_t* const dst = F8 ? raw + slot * C::kRaw : ring + slot * C::kTile;
+                for (int b = lane, pn = panel; b < boxes; b += 32, pn += 32 / groups) {
+                    if (F8)
+                        tma_load_4d(dst + g_of * p.box * D, map, 0, key % p.block, cur.h, w, fb);
+                    else
+                        tma_load_4d(dst + pn * (TK * 128) + g_of * p.box * 128, map, pn * 64,
+                                    key % p.block, cur.h, w, fb);
+                }
+                ++it;
+            };
+            int page = page_at(0), ahead = page_at(1);
+            load(&map_k, 0, page);
+            for (int j = 0; j < cnt && ok; ++j) {
+                const int later = page_at(j + 2);
+                if (j + 1 < cnt) load(&map_k, j + 1, ahead);
+                if (ok) load(&map_v, j, page);
+                page = ahead;
+                ahead = later;
+            }
+            left -= cnt;
+            cur.next(p);
+        }
+        if (!ok) code = 5;
+        // a CTA that gives up leaves no copy in flight behind it
+        if (!ok) {
+            constexpr int N = F8 ? NR : NS;
+            for (int k = max(0, it - N); k < it; ++k) {
+                uint64_t* const fb = F8 ? &raw_full[k % N] : &full[k % N];
+                volatile int none = 0;
+                mbar_wait(fb, (k / N) & 1, &none, 10000000ull);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- MMAs, from one thread
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_16(!F8, TK, false), id_o = idesc_16(!F8, D, true);
+            const uint32_t q0 = smem_u32(q_tile);
+            int it = 0, g = 0, item = 0;
+            auto ready = [&](uint64_t* b, uint32_t parity) {
+                if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
+                return ok;
+            };
+            auto scores = [&](int at) {  // S = Q K^T of tile `at`
+                const int slot = it % NS;
+                if (!ready(&full[slot], (it / NS) & 1)) return;
+                tc_after_sync();
+                const uint32_t k0 = smem_u32(ring + slot * C::kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(tmem + C::kS + (at & 1) * TK,
+                           desc_k_major(q0 + (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
+                           desc_k_major(k0 + (kk >> 2) * (TK * 128) + (kk & 3) * 32), id_s,
+                           kk > 0);
+                mma_commit(&empty[slot]);
+                mma_commit(&s_full[at & 1]);
+                ++it;
+            };
+            while (left > 0 && ok) {
+                const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+                if (!ready(&q_full, item & 1)) break;
+                scores(g);
+                if (cnt == 1) mma_commit(&q_free);
+                for (int j = 0; j < cnt && ok; ++j) {
+                    if (j + 1 < cnt) {
+                        scores(g + 1);
+                        if (j + 2 == cnt) mma_commit(&q_free);
+                    }
+                    const int slot = it % NS;
+                    if (!ready(&full[slot], (it / NS) & 1)) break;
+                    if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
+                    if (j == 0 && item > 0 && !ready(&o_free, (item - 1) & 1)) break;
+                    tc_after_sync();
+                    const uint32_t v0 = smem_u32(ring + slot * C::kTile);
+#pragma unroll
+                    for (int kk = 0; kk < TK / 16; ++kk)
+                        mma_ts(tmem, tmem + C::kP + (g & 1) * (TK / 2) + kk * 8,
+                               desc_mn_major(v0 + kk * 2048, TK * 128), id_o,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(&empty[slot]);
+                    mma_commit(&pv_done);
+                    if (j + 1 == cnt) mma_commit(&o_full);
+                    ++it;
+                    ++g;
+                }
+                ++item;
+                left -= cnt;
+                cur.next(p);
+            }
+            if (!ok) {  // let the MMAs that were issued end before tensor memory is freed
+                code = 6;
+                volatile int none = 0;
+                mma_commit(&drained);
+                mbar_wait(&drained, 0, &none, 10000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kQWarp && warp < kQWarp + kQWarps) {
+        // ---- Q rows into the MMA's layout (K-major, 128-byte swizzle)
+        const int t = tid - kQWarp * 32;
+        int item = 0;
+        while (left > 0) {
+            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+            if (item > 0 && !mbar_wait(&q_free, (item - 1) & 1, stop_v)) {
+                ok = false;
+                break;
+            }
+            const int row0 = cur.tile * kRows;
+            const int rows = (int)min((int64_t)kRows, (int64_t)cur.q.n * p.group - row0);
+            auto src_of = [&](int r) {
+                const int tok = (row0 + r) / p.group, h = (row0 + r) - tok * p.group;
+                return p.q + (int64_t)(cur.q.token0 + tok) * p.ldq +
+                       (int64_t)(cur.h * p.group + h) * p.q_head_stride;
+            };
+            if (!F8) {
+                for (int i = t; i < rows * (D / 8); i += kQWarps * 32) {
+                    const int r = i / (D / 8), c = i % (D / 8);
+                    const uint32_t dst = smem_u32(q_tile) + (c >> 3) * (kRows * 128) + r * 128 +
+                                         (((c & 7) ^ (r & 7)) << 4);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                                 "l"(src_of(r) + c * 8)
+                                 : "memory");
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            } else {
+                // a warp per row: x 2^e with the largest magnitude in [2^14, 2^15), as f16
+                for (int r = warp - kQWarp; r < rows; r += kQWarps) {
+                    const uint16_t* const src = src_of(r);
+                    constexpr int kPer = D / 32;  // 2, 4 or 8 consecutive values per lane
+                    uint32_t w[kPer / 2];
+#pragma unroll
+                    for (int i = 0; i < kPer / 2; ++i)
+                        w[i] = *reinterpret_cast<const uint32_t*>(src + lane * kPer + 2 * i);
+                    uint32_t big = 0;  // largest magnitude's bits; NaN and infinity are the largest
+#pragma unroll
+                    for (int i = 0; i < kPer / 2; ++i)
+                        big = max(big, max((w[i] & 0x7fffu), (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) big = max(big, __shfl_xor_sync(~0u, big, d));
+                    // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value is
+                    // below 2^-50 has scores of zero to fp32 either way
+                    const int up = min(127 + 14 + 127 - (int)(big >> 7), 127 + 64);
+                    const float mul = __uint_as_float((uint32_t)up << 23);
+                    const float back = __uint_as_float((uint32_t)(254 - up) << 23);
+                    if (lane == 0) q_scale[item & 1][r] = back;
+                    uint8_t* const row = q_tile + r * 128;
+#pragma unroll
+                    for (int i = 0; i < kPer / 2; ++i) {
+                        const int el = lane * kPer + 2 * i;
+                        const uint32_t h =
+                            pack16(true, __uint_as_float(w[i] << 16) * mul,
+                                   __uint_as_float(w[i] & 0xffff0000u) * mul);
+                        *reinterpret_cast<uint32_t*>(
+                            row + (el >> 6) * (kRows * 128) +
+                            ((((el & 63) >> 3) ^ (r & 7)) << 4) + (el & 7) * 2) = h;
+                    }
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(&q_full);
+            ++item;
+            left -= cnt;
+            cur.next(p);
+        }
+        if (!ok) code = 7;
+    } else if (F8 && warp >= kWidenWarp) {
+        // ---- e4m3 tiles to f16 in the MMA's layout.  A lane takes 16 codes of a key: two 16-byte
+        // pieces of its row; lanes 4..7 of 8 store theirs in the other order, so that 8 lanes
+        // always cover a panel's 128 bytes.
+        const int t = tid - kWidenWarp * 32;
+        int it = 0;
+        auto widen = [&](bool value, int key0, int end) {
+            const int rs = it % NR, ts = it % NS;
+            if (!mbar_wait(&raw_full[rs], (it / NR) & 1, stop_v) ||
+                (it >= NS && !mbar_wait(&empty[ts], (it / NS - 1) & 1, stop_v))) {
+                ok = false;
+                return;
+            }
+            const uint8_t* const src = raw + rs * C::kRaw;
+            uint8_t* const dst = ring + ts * C::kTile;
+            constexpr int kPer = D / 16;  // pieces per key
+#pragma unroll 4
+            for (int i = t; i < TK * kPer; i += kWidenWarps * 32) {
+                const int key = i / kPer, c = i % kPer;
+                uint4 w = *reinterpret_cast<const uint4*>(src + (size_t)i * 16);
+                // a value past the end must not meet a weight of zero as NaN or infinity
+                if (value && key0 + key >= end) w = make_uint4(0, 0, 0, 0);
+                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                uint32_t out[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                        : "=r"(out[2 * j]), "=r"(out[2 * j + 1])
+                        : "r"(in[j]));
+                uint8_t* const row = dst + (c >> 2) * (TK * 128) + key * 128;
+                const int u0 = (c & 3) * 2, swap = (lane >> 2) & 1, x = key & 7;
+                const uint4 a = make_uint4(out[0], out[1], out[2], out[3]);
+                const uint4 b = make_uint4(out[4], out[5], out[6], out[7]);
+                *reinterpret_cast<uint4*>(row + (((u0 + swap) ^ x) << 4)) = swap ? b : a;
+                *reinterpret_cast<uint4*>(row + (((u0 + 1 - swap) ^ x) << 4)) = swap ? a : b;
+            }
+            fence_async_smem();
+            mbar_arrive(&full[ts]);
+            mbar_arrive(&raw_empty[rs]);
+            ++it;
+        };
+        while (left > 0 && ok) {
+            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+            const int end = key_end(p, cur.q, cur.tile), k0 = cur.u * TK;
+            widen(false, k0, end);
+            for (int j = 0; j < cnt && ok; ++j) {
+                if (j + 1 < cnt) widen(false, k0, end);
+                if (ok) widen(true, k0 + j * TK, end);
+            }
+            left -= cnt;
+            cur.next(p);
+        }
+        if (!ok) code = 8;
+    } else if (warp < kSoftmaxWarps) {
+        // ---- softmax: thread = row = tensor memory lane
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        int g = 0, item = 0, ring_at = 0;
+        while (left > 0 && ok) {
+            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+            const int row0 = cur.tile * kRows;
+            const int rows = (int)min((int64_t)kRows, (int64_t)cur.q.n * p.group - row0);
+            const bool busy = warp * 32 < rows;  // this warp has rows
+            const int tok = (row0 + tid) / p.group;
+            const int end = key_end(p, cur.q, cur.tile);
+            // the last key this row sees
+            const int last = tid < rows ? min(cur.q.len - cur.q.n + tok, end - 1) : -1;
+            const int32_t* const table = p.table + cur.r * p.ld_table;
+            auto holes_at = [&](int j) {  // lane i: whether 16 keys of the unit have no page
+                const int key = (cur.u + j) * TK + lane * 16;
+                if (j >= cnt || lane >= TK / 16 || key >= end) return false;
+                return (unsigned)table[key / p.block] >= (unsigned)p.blocks;
+            };
+            float m = -INFINITY, l = 0.f, c = p.c;
+            bool hole = holes_at(0);
+            for (int j = 0; j < cnt; ++j, ++g) {
+                const bool hole_next = holes_at(j + 1);
+                const int key0 = (cur.u + j) * TK;
+                if (!mbar_wait(&s_full[g & 1], (g >> 1) & 1, stop_v)) {
+                    ok = false;
+                    break;
+                }
+                tc_after_sync();
+                if (!F8 && key0 + TK > end) {
+                    // values past the end are whatever the page held: zeros, so that their weights
+                    // of zero add nothing
+                    const int vi = ring_at + 2 * cnt - 1, slot = vi % NS;
+                    if (!mbar_wait(&full[slot], (vi / NS) & 1, stop_v)) {
+                        ok = false;
+                        break;
+                    }
+                    const int from = max(end - key0, 0);
+                    uint8_t* const v = ring + slot * C::kTile;
+                    for (int i = tid; i < (TK - from) * (D / 8); i += kSoftmaxWarps * 32) {
+                        const int key = from + i / (D / 8), x = i % (D / 8);
+                        *reinterpret_cast<uint4*>(v + (x >> 3) * (TK * 128) + key * 128 +
+                                                  (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                }
+                __syncwarp();
+                // the scores are there, so the rows' scales are (q_full itself may be a phase on)
+                if (F8 && j == 0 && tid < rows) c *= q_scale[item & 1][tid];
+                if (busy) {
+                    uint32_t s[TK / 32][32];
+#pragma unroll
+                    for (int i = 0; i < TK / 32; ++i)
+                        tmem_ld32(tmem + lanes + C::kS + (g & 1) * TK + i * 32, s[i]);
+#pragma unroll
+                    for (int i = 0; i < TK / 32; ++i) tmem_wait_ld(s[i]);
+                    const uint32_t holes = __ballot_sync(~0u, hole);
+                    const int see = last - key0;  // keys 0..see of the unit
+                    if (holes || __any_sync(~0u, see < TK - 1)) {
+#pragma unroll
+                        for (int i = 0; i < TK; ++i)
+                            if (i > see || ((holes >> (i / 16)) & 1))
+                                s[i / 32][i % 32] = 0xff800000u;  // -inf
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < TK; ++i)
+                        mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i / 32][i % 32]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (j == 0) {
+                        m = top;
+                    } else {
+                        const bool rise = (top - m) * c > 8.f;
+                        if (__any_sync(~0u, rise)) {
+                            const float f = rise ? exp2_approx((m - top) * c) : 1.f;
+                            if (rise) m = top;
+                            l *= f;
+                            // these scores came after PV of unit g - 2, and that of unit g waits
+                            // for this warp: the phase is g - 1 or its completion, no other
+                            if (!mbar_wait(&pv_done, (g - 1) & 1, stop_v)) {
+                                ok = false;
+                                break;
+                            }
+                            __syncwarp();
+                            tc_after_sync();
+#pragma unroll 1
+                            for (int i = 0; i < D / 32; ++i) {
+                                uint32_t o[32];
+                                tmem_ld32(tmem + lanes + i * 32, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(tmem + lanes + i * 32, o);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < TK / 64; ++i) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int k = i * 64 + 2 * e;
+                            const float a = exp2_approx(
+                                fmaf(__uint_as_float(s[k / 32][k % 32]), c, -mc));
+                            const float b = exp2_approx(
+                                fmaf(__uint_as_float(s[(k + 1) / 32][(k + 1) % 32]), c, -mc));
+                            sum[(2 * e) & 3] += a;
+                            sum[(2 * e + 1) & 3] += b;
+                            w[e] = pack16(F8, a, b);
+                        }
+                        tmem_st32(tmem + lanes + C::kP + (g & 1) * (TK / 2) + i * 32, w);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                tc_before_sync();
+                mbar_arrive(&p_full[g & 1]);
+                hole = hole_next;
+            }
+            if (!ok || !mbar_wait(&o_full, item & 1, stop_v)) {
+                ok = false;
+                break;
+            }
+            __syncwarp();
+            tc_after_sync();
+            const bool whole = cur.u == 0 && cnt == cur.n;
+            const int which = cur.u == 0 ? 1 : 0;  // this CTA's cut at its end, or at its start
+            const int64_t part = ((int64_t)blockIdx.x * 2 + which) * kRows + tid;
+            if (busy) {
+                const int head = cur.h * p.group + (row0 + tid) - tok * p.group;
+                uint16_t* const out = p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +
+                                      (int64_t)head * p.o_head_stride;
+                const float inv = l == 0.f ? 0.f : p.v_scale / l;
+                if (!whole && tid < rows)
+                    p.part_ml[part] = make_float2(m == -INFINITY ? m : m * c, l);
+#pragma unroll 1
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + lanes + i * 32, o);
+                    tmem_wait_ld(o);
+                    if (tid < rows) {
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint4 w;
+                                uint32_t* const ww = &w.x;
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    ww[x] = pack16(false,
+                                                   __uint_as_float(o[e * 8 + 2 * x]) * inv,
+                                                   __uint_as_float(o[e * 8 + 2 * x + 1]) * inv);
+                                *reinterpret_cast<uint4*>(out + i * 32 + e * 8) = w;
+                            }
+                        } else {
+                            float* const dst = p.part_o + part * D + i * 32;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(dst + e * 4) = make_uint4(
+                                    o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+                        }
+                    }
+                }
+            }
+            tc_before_sync();
+            mbar_arrive(&o_free);
+            ring_at += 2 * cnt;
+            left -= cnt;
+            ++item;
+            if (tid == 0 && left == 0) {
+                Cut cut;
+                memset(&cut, 0, sizeof(cut));
+                if (cur.u == 0 && !whole) {  // the last row tile goes on in later CTAs
+                    const int64_t x = range.end - cnt + cur.n - 1;  // its last unit
+                    const int64_t e =
+                        ((x + 1) * range.ctas + range.total - 1) / range.total - 1;
+                    cut.parts = (int)(e - blockIdx.x) + 1;
+                    cut.token0 = cur.q.token0;
+                    cut.row0 = row0;
+                    cut.rows = rows;
+                    cut.head = cur.h;
+                }
+                p.cuts[blockIdx.x] = cut;
+            }
+            cur.next(p);
+        }
+        if (!ok) code = 9;
+    }
+
+    if (code) {
+        *stop_v = 1;
+        if (lane == 0 || code == 9) atomicCAS(p.error, 0, code);
+        if (code == 9 && tid == 0) p.cuts[blockIdx.x].parts = 0;
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols));
+    }
+}
+
+// ---- joining the parts of cut row tiles: a warp per row, the parts in order ----------------
+constexpr int kJoinWarps = 8, kJoinSplit = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_attn_join_kernel(const Params p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int owner = blockIdx.x / kJoinSplit;
+    const Cut cut = p.cuts[owner];
+    if (cut.parts == 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kPer = D / 32;
+    for (int row = (blockIdx.x % kJoinSplit) * kJoinWarps + warp; row < cut.rows;
+         row += kJoinSplit * kJoinWarps) {
+        // part 0 lies with its CTA's cut at the end, the others with their cuts at the start
+        auto at = [&](int i) { return ((int64_t)(owner + i) * 2 + (i == 0)) * kRows + row; };
+        float top = -INFINITY;
+        for (int i = lane; i < cut.parts; i += 32) top = fmaxf(top, p.part_ml[at(i)].x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        float acc[kPer], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+        if (top > -INFINITY) {
+#pragma unroll 4
+            for (int i = 0; i < cut.parts; ++i) {
+                const int64_t a = at(i);
+                const float2 ml = p.part_ml[a];
+                const float w = exp2_approx(ml.x - top);
+                const float* const src = p.part_o + a * D + lane * kPer;
+                sum = fmaf(w, ml.y, sum);
+                // a part that saw no key has a weight of zero and zeros to weigh
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+            }
+        }
+        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+        const int grow = cut.row0 + row, tok = grow / p.group;
+        uint16_t* const out = p.o + (int64_t)(cut.token0 + tok) * p.ldo +
+                              (int64_t)(cut.head * p.group + grow - tok * p.group) * p.o_head_stride +
+                              lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2)
+            *reinterpret_cast<uint32_t*>(out + e) = pack16(false, acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+// ---- host --------------------------------------------------------------------------------
+
+struct Layout {
+    size_t cuts, ml, o, total;
+};
+
+Layout workspace_layout(int sms, int dim) {
+    Layout w;
+    w.cuts = 512;
+    w.ml = w.cuts + (size_t)sms * sizeof(Cut);
+    w.ml = (w.ml + 255) / 256 * 256;
+    w.o = w.ml + (size_t)sms * 2 * kRows * sizeof(float2);
+    w.total = w.o + (size_t)sms * 2 * kRows * dim * 4;
+    return w;
+}
+
+int gcd(int a, int b) {
+    while (b) {
+        const int t = a % b;
+        a = b;
+        b = t;
+    }
+    return a;
+}
+
+template <int D, bool F8>
+int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int grid,
+           cudaStream_t stream) {
+    using C = Cfg<D, F8>;
+    static bool ready[64];
+    if (!ready[dev]) {
+        if (cudaFuncSetAttribute(nvfp4_attn_kernel<D, F8>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)C::kSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return NVFP4_ERR_LAUNCH;
+        }
+        ready[dev] = true;
+    }
+    p.min_units = 1;
+    nvfp4_attn_kernel<D, F8><<<grid, C::kThreads, C::kSmem, stream>>>(p, mk, mv);
+    if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(grid * kJoinSplit);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, nvfp4_attn_join_kernel<D>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return NVFP4_ERR_LAUNCH;
+    }
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int nvfp4_paged_attn_workspace_bytes(int dim, size_t* bytes) {
+    if (!bytes) return NVFP4_ERR_NULL;
+    if (dim != 64 && dim != 128 && dim != 256) return NVFP4_ERR_SHAPE;
+    int dev, sms;
+    nvfp4_host::EncodeFn encode;
+    const int st = nvfp4_host::device(&dev, &sms, &encode);
+    if (st != NVFP4_OK) return st;
+    *bytes = workspace_layout(sms, dim).total;
+    return NVFP4_OK;
+}
+
+int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cache,
+                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!attn) return NVFP4_ERR_NULL;
+    int st = nvfp4_host::check_cache(cache);
+    if (st != NVFP4_OK) return st;
+    const nvfp4_paged_attn_t& a = *attn;
+    const nvfp4_kv_cache_t& kv = *cache;
+    if (a.heads < 1 || a.heads % kv.heads || a.heads > 16384 || a.tokens < 0 ||
+        a.tokens > (1 << 30) / (a.heads / kv.heads) || a.requests < 0 ||
+        a.requests > NVFP4_MAX_REQUESTS || a.table_columns < 0 || a.table_columns > INT32_MAX ||
+        a.ld_table < a.table_columns || !(a.scale > 0) || isinf(a.scale) || a.ldq < kv.dim ||
+        a.q_head_stride < kv.dim || a.ldo < kv.dim || a.o_head_stride < kv.dim)
+        return NVFP4_ERR_SHAPE;
+    if (a.tokens == 0 || a.requests == 0) return NVFP4_OK;
+    if (!a.q || !a.o || !a.starts || !a.lens || (a.table_columns && !a.table))
+        return NVFP4_ERR_NULL;
+    if (misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.starts, 4) ||
+        misaligned(a.lens, 4) || misaligned(a.table, 4) || a.ldq % 8 || a.q_head_stride % 8 ||
+        a.ldo % 8 || a.o_head_stride % 8)
+        return NVFP4_ERR_ALIGN;
+    const uint64_t qb = 2ull * ((a.tokens - 1) * a.ldq + (a.heads - 1) * a.q_head_stride + kv.dim);
+    const uint64_t ob = 2ull * ((a.tokens - 1) * a.ldo + (a.heads - 1) * a.o_head_stride + kv.dim);
+    if (overlaps(a.o, ob, a.q, qb)) return NVFP4_ERR_ALIAS;
+    if (!workspace || misaligned(workspace, 16)) return NVFP4_ERR_WORKSPACE;
+    int dev, sms;
+    nvfp4_host::EncodeFn encode;
+    st = nvfp4_host::device(&dev, &sms, &encode);
+    if (st != NVFP4_OK) return st;
+    const Layout w = workspace_layout(sms, kv.dim);
+    if (workspace_bytes < w.total) return NVFP4_ERR_WORKSPACE;
+
+    const bool f8 = kv.type == NVFP4_KV_E4M3;
+    const int tk = kv.dim == 256 ? 64 : 128;
+    const int box = gcd(kv.block_size, tk);
+    const int size = f8 ? 1 : 2;
+    CUtensorMap maps[2];
+    memset(maps, 0, sizeof(maps));
+    const void* tensors[2] = {kv.k, kv.v};
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[4] = {(cuuint64_t)kv.dim, (cuuint64_t)kv.block_size,
+                                    (cuuint64_t)kv.heads, (cuuint64_t)(kv.blocks ? kv.blocks : 1)};
+        const cuuint64_t strides[3] = {(cuuint64_t)kv.slot_stride * size,
+                                       (cuuint64_t)kv.head_stride * size,
+                                       (cuuint64_t)kv.block_stride * size};
+        const cuuint32_t boxes[4] = {(cuuint32_t)(f8 ? kv.dim : 64), (cuuint32_t)box, 1, 1};
+        const cuuint32_t one[4] = {1, 1, 1, 1};
+        // without pages nothing is read: every box then lies outside, on any valid address
+        void* const at = const_cast<void*>(kv.blocks ? tensors[i] : workspace);
+        if (encode(&maps[i], f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   4, at, dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return NVFP4_ERR_LAUNCH;
+    }
+    Params p;
+    memset(&p, 0, sizeof(p));
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.ldq = a.ldq;
+    p.q_head_stride = a.q_head_stride;
+    p.o = static_cast<uint16_t*>(a.o);
+    p.ldo = a.ldo;
+    p.o_head_stride = a.o_head_stride;
+    p.table = a.table;
+    p.ld_table = a.ld_table;
+    p.starts = a.starts;
+    p.lens = a.lens;
+    p.requests = a.requests;
+    p.tokens = (int)a.tokens;
+    p.kv_heads = kv.heads;
+    p.group = a.heads / kv.heads;
+    p.block = kv.block_size;
+    p.blocks = (int)kv.blocks;
+    p.outside = kv.blocks ? (int)kv.blocks : 1;
+    p.box = box;
+    const int64_t cap = a.table_columns * kv.block_size;
+    p.capacity = (int)(cap > INT32_MAX - 1024 ? INT32_MAX - 1024 : cap);
+    p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;
+    p.v_scale = f8 ? kv.v_scale : 1.f;
+    // a factor that left fp32's normal range would turn a masked score of -infinity into NaN
+    if (!(p.c >= 1.1754944e-38f) || isinf(p.c)) return NVFP4_ERR_SHAPE;
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    p.error = reinterpret_cast<int32_t*>(ws);
+    p.cuts = reinterpret_cast<Cut*>(ws + w.cuts);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    switch (kv.dim) {
+        case 64:
+            return f8 ? launch<64, true>(p, maps[0], maps[1], dev, sms, stream)
+                      : launch<64, false>(p, maps[0], maps[1], dev, sms, stream);
+        case 128:
+            return f8 ? launch<128, true>(p, maps[0], maps[1], dev, sms, stream)
+                      : launch<128, false>(p, maps[0], maps[1], dev, sms, stream);
+        default:
+            return f8 ? launch<256, true>(p, maps[0], maps[1], dev, sms, stream)
+                      : launch<256, false>(p, maps[0], maps[1], dev, sms, stream);
+    }
+}
+
+}  // extern "C"

@@ -1,0 +1,385 @@
+// The paged key/value cache around the attention: block tables and slot maps from request
+// lengths (nvfp4_paged_plan), and new rows into the cache (nvfp4_kv_append).  The decode plan
+// launches the latter as reshape_and_cache ("Blueprint - circuit executor" page for
+// qwen3.8-27b-nvfp4 on GB10, table "Kernels the plan launches").
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "nvfp4.h"
+#include "nvfp4_host.h"
+
+namespace {
+
+using nvfp4_host::launched;
+using nvfp4_host::misaligned;
+using nvfp4_host::overlaps;
+
+// ------------------------------------------------------------------------------------------
+// Plan.  With b = block_size, old = ceil(len / b), want = max(old, min(ceil((len + new) / b),
+// columns)), need = want - old:
+//   starts = exclusive sums of new;  first = exclusive sums of need
+//   table[r][c] = free[head + first[r] + c - old[r]] for old <= c < want, -1 past the list's end
+//   slot of token t = page * b + pos % b, pos = len[r] + t - starts[r], page = table[r][pos / b]
+//
+// The two sums are the only step that needs every request; a few thousand integers from L2 cost
+// less than a second launch or a grid-wide wait, so every CTA forms them itself in shared memory
+// and then takes its share of the tokens and of the new pages, finding a token's (a page's)
+// request by binary search.  Nothing is read that another CTA writes: an entry that this call
+// fills is taken from the free list again instead of from the table.  Latency bound: the chain
+// is lengths -> sums -> search -> table -> slot.
+constexpr int kPlanThreads = 512;
+
+struct PlanParams {
+    const int32_t* lens;
+    const int32_t* fresh;  // new tokens
+    int32_t* table;
+    int64_t ld_table, columns;
+    const int32_t* free_pages;
+    int64_t n_free;
+    const int32_t* head;
+    int64_t tokens;  // capacity of the per-token outputs
+    int32_t *starts, *lens_out, *slots, *request, *positions, *head_out, *missing;
+    int requests, block;
+};
+
+__device__ __forceinline__ int32_t saturate(int64_t v) {
+    return v > INT32_MAX ? INT32_MAX : (int32_t)v;
+}
+
+struct Pages {
+    int64_t old, need, lost;  // pages held, to take, and wanted beyond the table's columns
+};
+
+__device__ __forceinline__ Pages pages_of(const PlanParams& p, int64_t len, int64_t fresh) {
+    const int64_t old = (len + p.block - 1) / p.block;
+    const int64_t all = (len + fresh + p.block - 1) / p.block;
+    const int64_t held = all < p.columns ? all : p.columns;
+    Pages g;
+    g.old = old;
+    g.need = held > old ? held - old : 0;
+    g.lost = all - old - g.need;
+    return g;
+}
+
+// Index of the last i in [0, n) with a[i] <= v, for ascending a with a[0] <= v.
+__device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanParams p) {
+    extern __shared__ int64_t sums[];  // starts[requests], first[requests]
+    int64_t* const starts = sums;
+    int64_t* const first = sums + p.requests;
+    __shared__ int64_t warp_sum[3][kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t carry_tok = 0, carry_page = 0, lost = 0;
+    for (int base = 0; base < p.requests; base += kPlanThreads) {
+        const int r = base + tid;
+        int64_t tok = 0, need = 0;
+        if (r < p.requests) {
+            const int64_t len = max(p.lens[r], 0);
+            tok = max(p.fresh[r], 0);
+            const Pages g = pages_of(p, len, tok);
+            need = g.need;
+            lost += g.lost;
+        }
+        int64_t st = tok, sp = need;  // inclusive sums over the warp
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t a = __shfl_up_sync(~0u, st, d), b = __shfl_up_sync(~0u, sp, d);
+            if (lane >= d) st += a, sp += b;
+        }
+        if (lane == 31) warp_sum[0][warp] = st, warp_sum[1][warp] = sp;
+        __syncthreads();
+        int64_t bt = carry_tok, bp = carry_page;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            const int64_t a = warp_sum[0][w], b = warp_sum[1][w];
+            if (w < warp) bt += a, bp += b;
+            carry_tok += a, carry_page += b;
+        }
+        if (r < p.requests) {
+            starts[r] = bt + st - tok;
+            first[r] = bp + sp - need;
+            if (blockIdx.x == 0) {
+                p.starts[r] = saturate(bt + st - tok);
+                p.lens_out[r] = saturate((int64_t)max(p.lens[r], 0) + tok);
+            }
+        }
+        __syncthreads();  // starts, first; and warp_sum may be written again
+    }
+    const int64_t total = carry_tok, wanted = carry_page;
+    const int64_t head = max(p.head[0], 0);
+    const int64_t left = p.n_free > head ? p.n_free - head : 0;
+    const int64_t got = wanted < left ? wanted : left;
+    if (blockIdx.x == 0) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) lost += __shfl_down_sync(~0u, lost, d);
+        if (lane == 0) warp_sum[2][warp] = lost;
+        __syncthreads();
+        if (tid == 0) {
+            int64_t all = wanted - got;
+            for (int w = 0; w < kPlanThreads / 32; ++w) all += warp_sum[2][w];
+            p.starts[p.requests] = saturate(total);
+            p.head_out[0] = saturate(head + got);
+            p.missing[0] = saturate(all);
+        }
+    }
+    const int64_t stride = (int64_t)gridDim.x * kPlanThreads;
+    const int64_t me = (int64_t)blockIdx.x * kPlanThreads + tid;
+    for (int64_t i = me; i < wanted; i += stride) {
+        const int r = last_at_most(first, p.requests, i);  // the last one: need > 0
+        const int64_t old = ((int64_t)max(p.lens[r], 0) + p.block - 1) / p.block;
+        p.table[r * p.ld_table + old + i - first[r]] =
+            i < left ? p.free_pages[head + i] : -1;
+    }
+    for (int64_t t = me; t < p.tokens; t += stride) {
+        int32_t slot = -1, req = -1, at = 0;
+        if (t < total) {
+            const int r = last_at_most(starts, p.requests, t);
+            const int64_t len = max(p.lens[r], 0);
+            const int64_t pos = len + t - starts[r];
+            const int64_t c = pos / p.block, old = (len + p.block - 1) / p.block;
+            int64_t page = -1;
+            if (c < p.columns) {
+                const int64_t i = first[r] + c - old;
+                if (c < old) page = p.table[r * p.ld_table + c];
+                else if (i < left) page = p.free_pages[head + i];
+            }
+            const int64_t s = page * p.block + pos % p.block;
+            if (page >= 0 && s <= INT32_MAX) slot = (int32_t)s;
+            req = r;
+            at = saturate(pos);
+        }
+        p.slots[t] = slot;
+        if (p.request) p.request[t] = req;
+        if (p.positions) p.positions[t] = at;
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// Append.  One 16-byte vector of 8 elements per thread and step, K and V in one launch; a
+// warp's lanes hold consecutive vectors of a token's row, so loads and stores are whole
+// sectors.  HBM bound, 4 bytes of traffic per element (3 with an 8-bit cache).  An e4m3
+// element is e4m3_rn(x / scale), saturated at 448: a true division, so the code is that of the
+// rounded quotient whatever the scale.
+constexpr int kAppendThreads = 256;
+
+struct AppendParams {
+    const uint16_t* src[2];
+    int64_t ld[2], head_stride[2];
+    uint8_t* cache[2];
+    float scale[2];
+    const int32_t* slots;
+    int64_t tokens, blocks, block_stride, slot_stride, cache_head_stride;
+    int heads, dim, block;
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, float scale) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(r)
+        : "f"(__fdiv_rn(bf16_hi(w), scale)), "f"(__fdiv_rn(bf16_lo(w), scale)));
+    return r;
+}
+
+template <bool F8>
+__global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const AppendParams p) {
+    const int vecs = p.dim / 8, row = p.heads * vecs;  // vectors of a token's K (or V)
+    const int64_t all = p.tokens * row * 2;
+    const int64_t stride = (int64_t)gridDim.x * kAppendThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x; i < all; i += stride) {
+        const int64_t t = i / (2 * row);
+        const int in = (int)(i - t * 2 * row), which = in >= row;
+        const int j = in - which * row, h = j / vecs, c = j - h * vecs;
+        const int32_t slot = p.slots[t];
+        const int64_t page = slot / p.block;
+        if (slot < 0 || page >= p.blocks) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            p.src[which] + t * p.ld[which] + h * p.head_stride[which] + c * 8);
+        const int64_t at = page * p.block_stride + (int64_t)(slot - (int32_t)page * p.block) * p.slot_stride +
+                           h * p.cache_head_stride + c * 8;
+        if (F8) {
+            const float s = p.scale[which];
+            uint2 o;
+            o.x = e4m3_pair(v.x, s) | e4m3_pair(v.y, s) << 16;
+            o.y = e4m3_pair(v.z, s) | e4m3_pair(v.w, s) << 16;
+            *reinterpret_cast<uint2*>(p.cache[which] + at) = o;
+        } else {
+            *reinterpret_cast<uint4*>(p.cache[which] + 2 * at) = v;
+        }
+    }
+}
+
+}  // namespace
+
+namespace nvfp4_host {
+
+int check_cache(const nvfp4_kv_cache_t* c) {
+    if (!c) return NVFP4_ERR_NULL;
+    if (c->type != NVFP4_KV_BF16 && c->type != NVFP4_KV_E4M3) return NVFP4_ERR_SHAPE;
+    if (c->heads < 1 || c->heads > 1024 || (c->dim != 64 && c->dim != 128 && c->dim != 256) ||
+        c->block_size < 16 || c->block_size % 16 || c->block_size > (1 << 20) || c->blocks < 0 ||
+        c->blocks > INT32_MAX || c->blocks * c->block_size > INT32_MAX)
+        return NVFP4_ERR_SHAPE;
+    if (c->type == NVFP4_KV_E4M3 &&
+        (!(c->k_scale > 0) || !(c->v_scale > 0) || isinf(c->k_scale) || isinf(c->v_scale)))
+        return NVFP4_ERR_SHAPE;
+    const int size = c->type == NVFP4_KV_E4M3 ? 1 : 2;
+    const int64_t most = (int64_t)1 << 39;  // a tensor map's strides are below 2^40 bytes
+    const int64_t strides[3] = {c->block_stride, c->slot_stride, c->head_stride};
+    for (int64_t s : strides) {
+        if (s < c->dim || s * size >= most) return NVFP4_ERR_SHAPE;
+        if (s * size % 16) return NVFP4_ERR_ALIGN;
+    }
+    if (c->blocks > 0) {
+        if (!c->k || !c->v) return NVFP4_ERR_NULL;
+        if (misaligned(c->k, 16) || misaligned(c->v, 16)) return NVFP4_ERR_ALIGN;
+    }
+    return NVFP4_OK;
+}
+
+}  // namespace nvfp4_host
+
+extern "C" {
+
+int nvfp4_paged_plan(const nvfp4_paged_plan_t* plan, cudaStream_t stream) {
+    if (!plan) return NVFP4_ERR_NULL;
+    const nvfp4_paged_plan_t& a = *plan;
+    if (a.requests < 0 || a.requests > NVFP4_MAX_REQUESTS || a.table_columns < 0 ||
+        a.ld_table < a.table_columns || a.block_size < 1 || a.free_count < 0 || a.tokens < 0 ||
+        a.tokens > INT32_MAX || a.free_count > INT32_MAX || a.table_columns > INT32_MAX)
+        return NVFP4_ERR_SHAPE;
+    if (!a.head || !a.starts || !a.head_out || !a.missing || (a.free_count && !a.free_pages) ||
+        (a.tokens && !a.slots) || (a.requests && (!a.lens || !a.new_tokens || !a.lens_out)) ||
+        (a.requests && a.table_columns && !a.table))
+        return NVFP4_ERR_NULL;
+    const void* all[] = {a.lens, a.new_tokens, a.table, a.free_pages, a.head, a.starts, a.lens_out,
+                         a.slots, a.request, a.positions, a.head_out, a.missing};
+    for (const void* q : all)
+        if (misaligned(q, 4)) return NVFP4_ERR_ALIGN;
+    // nothing that is written may overlap anything else: every CTA reads the inputs
+    const uint64_t rb = 4ull * a.requests, tb = 4ull * a.tokens;
+    const uint64_t bytes[] = {
+        rb, rb,
+        a.requests ? 4ull * ((uint64_t)(a.requests - 1) * a.ld_table + a.table_columns) : 0,
+        4ull * a.free_count, 4, rb + 4, rb, tb, a.request ? tb : 0, a.positions ? tb : 0, 4, 4};
+    const int inputs[] = {0, 1, 3, 4}, outputs[] = {2, 5, 6, 7, 8, 9, 10, 11};
+    for (int i = 0; i < 8; ++i) {
+        for (int j : inputs)
+            if (overlaps(all[outputs[i]], bytes[outputs[i]], all[j], bytes[j]))
+                return NVFP4_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(all[outputs[i]], bytes[outputs[i]], all[outputs[j]], bytes[outputs[j]]))
+                return NVFP4_ERR_ALIAS;
+    }
+    int dev, sms;
+    nvfp4_host::EncodeFn encode;
+    int st = nvfp4_host::device(&dev, &sms, &encode);
+    if (st != NVFP4_OK) return st;
+    PlanParams p;
+    memset(&p, 0, sizeof(p));
+    p.lens = a.lens;
+    p.fresh = a.new_tokens;
+    p.table = a.table;
+    p.ld_table = a.ld_table;
+    p.columns = a.table_columns;
+    p.free_pages = a.free_pages;
+    p.n_free = a.free_count;
+    p.head = a.head;
+    p.tokens = a.tokens;
+    p.starts = a.starts;
+    p.lens_out = a.lens_out;
+    p.slots = a.slots;
+    p.request = a.request;
+    p.positions = a.positions;
+    p.head_out = a.head_out;
+    p.missing = a.missing;
+    p.requests = a.requests;
+    p.block = a.block_size;
+    const size_t smem = 16ull * a.requests;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(nvfp4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             16 * NVFP4_MAX_REQUESTS) != cudaSuccess) {
+        cudaGetLastError();
+        return NVFP4_ERR_LAUNCH;
+    }
+    const int64_t want = (a.tokens + a.requests + kPlanThreads - 1) / kPlanThreads;
+    const int grid = (int)(want < 1 ? 1 : want > sms ? sms : want);
+    nvfp4_plan_kernel<<<grid, kPlanThreads, smem, stream>>>(p);
+    return launched();
+}
+
+int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const void* v, int64_t ldv,
+                    int64_t v_head_stride, int64_t tokens, const int32_t* slots,
+                    const nvfp4_kv_cache_t* cache, cudaStream_t stream) {
+    int st = nvfp4_host::check_cache(cache);
+    if (st != NVFP4_OK) return st;
+    const nvfp4_kv_cache_t& c = *cache;
+    if (tokens < 0 || tokens > INT32_MAX || ldk < c.dim || ldv < c.dim || k_head_stride < c.dim ||
+        v_head_stride < c.dim)
+        return NVFP4_ERR_SHAPE;
+    if (tokens == 0 || c.blocks == 0) return NVFP4_OK;
+    if (!k || !v || !slots) return NVFP4_ERR_NULL;
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 4) || ldk % 8 || ldv % 8 ||
+        k_head_stride % 8 || v_head_stride % 8)
+        return NVFP4_ERR_ALIGN;
+    const int size = c.type == NVFP4_KV_E4M3 ? 1 : 2;
+    const uint64_t cache_bytes = (uint64_t)size * ((c.blocks - 1) * c.block_stride +
+                                                   (c.block_size - 1) * c.slot_stride +
+                                                   (c.heads - 1) * c.head_stride + c.dim);
+    const uint64_t kb = 2ull * ((tokens - 1) * ldk + (c.heads - 1) * k_head_stride + c.dim);
+    const uint64_t vb = 2ull * ((tokens - 1) * ldv + (c.heads - 1) * v_head_stride + c.dim);
+    const void* caches[2] = {c.k, c.v};
+    for (const void* dst : caches)
+        if (overlaps(dst, cache_bytes, k, kb) || overlaps(dst, cache_bytes, v, vb) ||
+            overlaps(dst, cache_bytes, slots, 4ull * tokens))
+            return NVFP4_ERR_ALIAS;
+    int dev, sms;
+    nvfp4_host::EncodeFn encode;
+    st = nvfp4_host::device(&dev, &sms, &encode);
+    if (st != NVFP4_OK) return st;
+    AppendParams p;
+    memset(&p, 0, sizeof(p));
+    p.src[0] = static_cast<const uint16_t*>(k);
+    p.src[1] = static_cast<const uint16_t*>(v);
+    p.ld[0] = ldk;
+    p.ld[1] = ldv;
+    p.head_stride[0] = k_head_stride;
+    p.head_stride[1] = v_head_stride;
+    p.cache[0] = static_cast<uint8_t*>(c.k);
+    p.cache[1] = static_cast<uint8_t*>(c.v);
+    p.scale[0] = c.k_scale;
+    p.scale[1] = c.v_scale;
+    p.slots = slots;
+    p.tokens = tokens;
+    p.blocks = c.blocks;
+    p.block_stride = c.block_stride;
+    p.slot_stride = c.slot_stride;
+    p.cache_head_stride = c.head_stride;
+    p.heads = c.heads;
+    p.dim = c.dim;
+    p.block = c.block_size;
+    const int64_t want = (tokens * c.heads * (c.dim / 8) * 2 + kAppendThreads - 1) / kAppendThreads;
+    const int grid = (int)(want > 8 * sms ? 8 * sms : want);
+    if (c.type == NVFP4_KV_E4M3)
+        nvfp4_append_kernel<true><<<grid, kAppendThreads, 0, stream>>>(p);
+    else
+        nvfp4_append_kernel<false><<<grid, kAppendThreads, 0, stream>>>(p);
+    return launched();
+}
+
+}  // extern "C"

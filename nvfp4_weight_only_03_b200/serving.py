@@ -1,0 +1,290 @@
+"""Binding of the operators between the projections of a decode step: block tables and slot maps
+(paged_plan), new rows into the paged cache (kv_append), attention over it (paged_attention).
+
+    plan = paged_plan(lens, new, table, free, head, block_size, tokens=T)
+    kv_append(k, v, k_cache, v_cache, plan.slots)
+    o = paged_attention(q, k_cache, v_cache, table, plan.starts, plan.lens)
+
+Lengths, tables and indexes stay on the device: no call copies anything to the host or waits, and
+a captured call serves later lengths.  Every tensor of a call lies on one device, which need not
+be the current one; the call runs on that device's current stream unless `stream` names another,
+on which the inputs must then be ready.  Outputs that a call makes are allocated for the stream
+it runs on.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+KV_BF16, KV_E4M3 = 0, 1
+MAX_REQUESTS = 8192
+
+_p, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class KvCacheStruct(ctypes.Structure):
+    """nvfp4_kv_cache_t."""
+    _fields_ = [("k", _p), ("v", _p), ("type", _i32), ("heads", _i32), ("dim", _i32),
+                ("block_size", _i32), ("blocks", _i64), ("block_stride", _i64),
+                ("slot_stride", _i64), ("head_stride", _i64), ("k_scale", _f32),
+                ("v_scale", _f32)]
+
+
+class PlanStruct(ctypes.Structure):
+    """nvfp4_paged_plan_t."""
+    _fields_ = [("lens", _p), ("new_tokens", _p), ("requests", _i32), ("block_size", _i32),
+                ("table", _p), ("ld_table", _i64), ("table_columns", _i64), ("free_pages", _p),
+                ("free_count", _i64), ("head", _p), ("tokens", _i64), ("starts", _p),
+                ("lens_out", _p), ("slots", _p), ("request", _p), ("positions", _p),
+                ("head_out", _p), ("missing", _p)]
+
+
+class AttnStruct(ctypes.Structure):
+    """nvfp4_paged_attn_t."""
+    _fields_ = [("q", _p), ("ldq", _i64), ("q_head_stride", _i64), ("o", _p), ("ldo", _i64),
+                ("o_head_stride", _i64), ("tokens", _i64), ("heads", _i32), ("requests", _i32),
+                ("table", _p), ("ld_table", _i64), ("table_columns", _i64), ("starts", _p),
+                ("lens", _p), ("scale", _f32)]
+
+
+def declare(L) -> None:
+    """Argument types of the entry points bound here."""
+    sz = ctypes.c_size_t
+    kv = ctypes.POINTER(KvCacheStruct)
+    L.nvfp4_paged_plan.argtypes = [ctypes.POINTER(PlanStruct), _p]
+    L.nvfp4_kv_append.argtypes = [_p, _i64, _i64, _p, _i64, _i64, _i64, _p, kv, _p]
+    L.nvfp4_paged_attn_workspace_bytes.argtypes = [ctypes.c_int, ctypes.POINTER(sz)]
+    L.nvfp4_paged_attn.argtypes = [ctypes.POINTER(AttnStruct), kv, _p, sz, _p]
+    for f in (L.nvfp4_paged_plan, L.nvfp4_kv_append, L.nvfp4_paged_attn_workspace_bytes,
+              L.nvfp4_paged_attn):
+        f.restype = ctypes.c_int
+
+
+def _nv():
+    import nvfp4_weight_only_03_b200 as nv
+    return nv
+
+
+def _device(first: torch.Tensor, **others) -> torch.device:
+    """The one CUDA device of a call's tensors."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    return first.device
+
+
+@contextlib.contextmanager
+def _running(dev: torch.device, stream):
+    """Makes the call's device and stream current; yields the stream's handle."""
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            yield torch.cuda.current_stream(dev).cuda_stream
+        else:
+            with torch.cuda.device(dev):
+                yield torch.cuda.current_stream(dev).cuda_stream
+        return
+    st = _nv()._stream_obj(stream, dev)
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        yield st.cuda_stream
+
+
+def _ints(t: torch.Tensor, name: str, shape) -> torch.Tensor:
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _table_args(table: torch.Tensor, rows: int):
+    if table.dtype != torch.int32:
+        raise TypeError("table must be int32")
+    if table.dim() != 2 or table.shape[0] != rows or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be [{rows}][columns] with unit inner stride")
+    cols = table.shape[1]
+    return cols, table.stride(0) if rows > 1 else cols
+
+
+def _heads(t: torch.Tensor, name: str):
+    """(token stride, head stride) of a bf16 [tokens][heads][dim] view."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens][heads][dim] with unit inner stride")
+    n, h, d = t.shape
+    head = t.stride(1) if h > 1 else d
+    return t.stride(0) if n > 1 else max(h * head, d), head
+
+
+def _cache_args(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float,
+                v_scale: float) -> KvCacheStruct:
+    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or \
+            v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be [blocks][block_size][heads][dim]")
+    blocks, block, heads, dim = k_cache.shape
+
+    def strides(c):
+        slot, head = c.stride(1), c.stride(2) if heads > 1 else dim
+        return c.stride(0) if blocks > 1 else block * slot, slot, head
+
+    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1 or strides(k_cache) != strides(v_cache):
+        raise ValueError("k_cache and v_cache must have the same strides, the inner one 1")
+    bs, ss, hs = strides(k_cache)
+    return KvCacheStruct(
+        k=k_cache.data_ptr(), v=v_cache.data_ptr(),
+        type=KV_BF16 if k_cache.dtype == torch.bfloat16 else KV_E4M3, heads=heads, dim=dim,
+        block_size=block, blocks=blocks, block_stride=bs, slot_stride=ss, head_stride=hs,
+        k_scale=float(k_scale), v_scale=float(v_scale))
+
+
+def _workspace(kind: str, need: int, dev: torch.device) -> torch.Tensor:
+    """The cached workspace of (device, current stream), or, while a graph is captured, one of
+    the graph's own: two graphs never share one."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws[:512].zero_()
+        return ws
+    return _nv()._cached_workspace(kind, need, dev, torch.cuda.current_stream(dev))
+
+
+class PagedPlan(NamedTuple):
+    """What paged_plan computes, all int32 on the device."""
+    starts: torch.Tensor     # [requests + 1]: first token of each request, and the total
+    lens: torch.Tensor       # [requests]: tokens in the cache once the new ones are there
+    slots: torch.Tensor      # [tokens]: cache slot of each token, -1 for none
+    request: torch.Tensor    # [tokens]: its request, -1 behind the last token
+    positions: torch.Tensor  # [tokens]: its position in the request, 0 behind the last token
+    head: torch.Tensor       # [1]: how many of the free list are taken now
+    missing: torch.Tensor    # [1]: pages that were wanted and not there
+
+
+def paged_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: torch.Tensor,
+               head: torch.Tensor, block_size: int, tokens: int,
+               out: Optional[PagedPlan] = None, stream=None) -> PagedPlan:
+    """Block tables and slot maps of a batch from its requests' lengths (nvfp4_paged_plan).
+
+    lens, new: int32 [requests], tokens in the cache and tokens to come.  table: int32
+    [requests][columns], page of each block_size tokens of a request; the pages that the new
+    tokens need are taken from free[head:] in request order and written into it (-1 where the
+    list is spent).  tokens: length of the per-token outputs; those behind the last token are
+    inert (slot -1, request -1, position 0).  out: the outputs to fill, as an earlier call
+    returned them (none of them may be one of the inputs); by default new ones."""
+    n = lens.shape[0]
+    dev = _device(lens, new=new, table=table, free=free, head=head)
+    _ints(lens, "lens", (n,))
+    _ints(new, "new", (n,))
+    _ints(free, "free", (free.numel(),))
+    _ints(head, "head", (1,))
+    cols, ld = _table_args(table, n)
+    sizes = (n + 1, n, tokens, tokens, tokens, 1, 1)
+    with _running(dev, stream) as st:
+        if out is None:
+            out = PagedPlan(*(torch.empty(s, dtype=torch.int32, device=dev) for s in sizes))
+        for name, t, s in zip(PagedPlan._fields, out, sizes):
+            _ints(t, "out." + name, (s,))
+        _device(lens, **{"out." + k: t for k, t in out._asdict().items()})
+        a = PlanStruct(
+            lens=lens.data_ptr(), new_tokens=new.data_ptr(), requests=n,
+            block_size=int(block_size), table=table.data_ptr(), ld_table=ld, table_columns=cols,
+            free_pages=free.data_ptr(), free_count=free.numel(), head=head.data_ptr(),
+            tokens=int(tokens), starts=out.starts.data_ptr(), lens_out=out.lens.data_ptr(),
+            slots=out.slots.data_ptr(), request=out.request.data_ptr(),
+            positions=out.positions.data_ptr(), head_out=out.head.data_ptr(),
+            missing=out.missing.data_ptr())
+        nv = _nv()
+        nv._check(nv.lib().nvfp4_paged_plan(ctypes.byref(a), st), "nvfp4_paged_plan")
+    return out
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              slots: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
+              stream=None) -> None:
+    """Writes the rows of k and v into their slots of the paged cache (nvfp4_kv_append).
+
+    k, v: bfloat16 [tokens][heads][dim], views into a fused projection's rows included.
+    k_cache, v_cache: bfloat16 or float8_e4m3fn [blocks][block_size][heads][dim] (any strides
+    with an inner one of 1, the same for both); a float8 cache holds e4m3(x / scale).  slots:
+    int32 [tokens], page * block_size + place; rows with a negative slot, or one past the last
+    page, are skipped."""
+    dev = _device(k, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots)
+    c = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    ldk, hk = _heads(k, "k")
+    ldv, hv = _heads(v, "v")
+    n = k.shape[0]
+    if k.shape != v.shape or tuple(k.shape[1:]) != (c.heads, c.dim):
+        raise ValueError(f"k and v must be [tokens][{c.heads}][{c.dim}]")
+    _ints(slots, "slots", (n,))
+    nv = _nv()
+    with _running(dev, stream) as st:
+        nv._check(nv.lib().nvfp4_kv_append(k.data_ptr(), ldk, hk, v.data_ptr(), ldv, hv, n,
+                                           slots.data_ptr(), ctypes.byref(c), st),
+                  "nvfp4_kv_append")
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    table: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+                    scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                    out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                    stream=None, check: bool = False) -> torch.Tensor:
+    """Causal attention of each request's newest tokens over its paged cache (nvfp4_paged_attn).
+
+    q: bfloat16 [tokens][heads][dim]; tokens starts[r] .. starts[r+1]-1 are the last ones of
+    request r's lens[r], already in the cache.  Query head h reads kv head h // (heads //
+    kv_heads).  scale: of the scores, dim ** -0.5 by default.  out: bfloat16 like q (by default a
+    new one); its rows behind the last token are not written.  ws: a workspace of
+    paged_attention_workspace_bytes(dim) bytes, zero-filled before its first use; by default
+    the cached one of (device, stream), or the graph's own during a capture.  check: synchronise
+    and raise if a bounded wait in the kernel gave up."""
+    dev = _device(q, k_cache=k_cache, v_cache=v_cache, table=table, starts=starts, lens=lens,
+                  out=out, ws=ws)
+    c = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    ldq, hq = _heads(q, "q")
+    tokens, heads, dim = q.shape
+    if dim != c.dim or heads % max(c.heads, 1):
+        raise ValueError(f"q must be [tokens][heads][{c.dim}], heads a multiple of {c.heads}")
+    n = lens.shape[0]
+    _ints(lens, "lens", (n,))
+    _ints(starts, "starts", (n + 1,))
+    cols, ld = _table_args(table, n)
+    nv = _nv()
+    with _running(dev, stream) as st:
+        if out is None:
+            out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {list(q.shape)}")
+        ldo, ho = _heads(out, "out")
+        if ws is None:
+            ws = _workspace("attn", paged_attention_workspace_bytes(dim), dev)
+        a = AttnStruct(
+            q=q.data_ptr(), ldq=ldq, q_head_stride=hq, o=out.data_ptr(), ldo=ldo,
+            o_head_stride=ho, tokens=tokens, heads=heads, requests=n, table=table.data_ptr(),
+            ld_table=ld, table_columns=cols, starts=starts.data_ptr(), lens=lens.data_ptr(),
+            scale=float(dim ** -0.5 if scale is None else scale))
+        nv._check(nv.lib().nvfp4_paged_attn(ctypes.byref(a), ctypes.byref(c), ws.data_ptr(),
+                                            ws.numel() * ws.element_size(), st),
+                  "nvfp4_paged_attn")
+        if check:
+            nv._check_error(ws, st, "nvfp4_paged_attn")
+    return out
+
+
+_attn_bytes: dict = {}
+
+
+def paged_attention_workspace_bytes(dim: int) -> int:
+    """Bytes of a paged_attention workspace for this head dim on the current device."""
+    key = (torch.cuda.current_device(), dim)
+    if key not in _attn_bytes:
+        b = ctypes.c_size_t()
+        nv = _nv()
+        nv._check(nv.lib().nvfp4_paged_attn_workspace_bytes(dim, ctypes.byref(b)),
+                  "nvfp4_paged_attn_workspace_bytes")
+        _attn_bytes[key] = int(b.value)
+    return _attn_bytes[key]

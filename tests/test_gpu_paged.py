@@ -1,0 +1,417 @@
+"""Paged cache and attention through the binding: block tables and slot maps, cache rows, and the
+attention, each against a plain implementation in 64 bits (whole numbers and copies: exactly).
+
+Tolerance of the attention, per element, with A = sum_j w_j |v_j| / sum_j w_j over the keys a row
+sees, h the half step of a rounding (bf16 2^-8, f16 2^-11, fp32 2^-24):
+  output rounding              2^-8 |o|
+  weights rounded for the MMA  (2^-8 bf16 cache, 2^-11 e4m3 cache) A, and for f16 half its
+                               smallest step, 2^-25, per key: n 2^-25 max|v| (a row's largest
+                               weight is at least 1, so the sum of weights is, too)
+  scores                       a sum of D products off by at most D 2^-23 sum|q k| (twice the
+                               rounding of every partial sum) moves a weight by as much,
+                               relatively, in the numerator and in the sum: 2 delta A
+  exponent and sums            2^-20 (argument, ex2 and the rescaling), and 2^-23 per step of a
+                               chain of n / 16 MMA steps and 128 additions, in both: times 2 A
+"""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_weight_only_03_b200 as nv
+
+pytestmark = pytest.mark.gpu
+
+F8 = torch.float8_e4m3fn
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def make_cache(g, blocks, block, heads, dim, f8, layout="nhd"):
+    """K and V caches full of NaN in one of the layouts a program may keep."""
+    dt = F8 if f8 else torch.bfloat16
+    if layout == "hnd":  # [blocks][heads][block][dim]
+        make = lambda: torch.empty((blocks, heads, block, dim), device="cuda", dtype=dt) \
+            .transpose(1, 2)
+        k, v = make(), make()
+    elif layout == "joint":  # [blocks][2][block][heads][dim]
+        both = torch.empty((blocks, 2, block, heads, dim), device="cuda", dtype=dt)
+        k, v = both[:, 0], both[:, 1]
+    else:
+        k, v = (torch.empty((blocks, block, heads, dim), device="cuda", dtype=dt)
+                for _ in range(2))
+    for c in (k, v):
+        if f8:
+            c.view(torch.uint8).fill_(0x7F)
+        else:
+            c.fill_(float("nan"))
+    return k, v
+
+
+def put(cache, page, place, rows):
+    if cache.dtype == F8:
+        cache.view(torch.uint8)[page, place] = rows.to(F8).view(torch.uint8)
+    else:
+        cache[page, place] = rows.to(cache.dtype)
+
+
+class Batch:
+    """Requests with their keys and values scattered over random pages; every slot that no
+    request owns holds NaN."""
+
+    def __init__(self, seed, lens, new, heads, kv_heads, dim, block, f8=False, layout="nhd",
+                 q_scale=1.5, pad=0, spare_columns=1, holes=()):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        self.lens, self.new, self.f8, self.dim = lens, new, f8, dim
+        self.heads, self.kv_heads = heads, kv_heads
+        pages = [-(-n // block) for n in lens]
+        total = sum(pages) + 3
+        order = rng.permutation(total)
+        cols = max(pages + [0]) + spare_columns
+        table = np.full((len(lens), cols), -1, np.int32)
+        at = 0
+        for r, n in enumerate(pages):
+            table[r, :n] = order[at:at + n]
+            at += n
+        self.kc, self.vc = make_cache(g, total, block, kv_heads, dim, f8, layout)
+        self.k_scale, self.v_scale = (0.25, 0.125) if f8 else (1.0, 1.0)
+        spread = 4.0 if f8 else 1.0
+        for r, n in enumerate(lens):
+            if n == 0:
+                continue
+            pos = torch.arange(n, device="cuda")
+            page = torch.from_numpy(table[r]).cuda().long()[pos // block]
+            for c in (self.kc, self.vc):
+                rows = torch.randn((n, kv_heads, dim), generator=g, device="cuda") * spread
+                put(c, page, pos % block, rows)
+        for r, c, page in holes:  # entries that name no page
+            table[r, c] = page
+        self.table = torch.from_numpy(table).cuda()
+        t = sum(new)
+        self.tokens = t
+        self.q = torch.randn((t + pad, heads, dim), generator=g, device="cuda")\
+            .mul_(q_scale).to(torch.bfloat16)
+        self.starts = ints([0] + list(np.cumsum(new)))
+        self.block, self.blocks, self.cols = block, total, cols
+        self.scale = dim ** -0.5
+
+    def call(self, **kw):
+        kw.setdefault("q", self.q)
+        q = kw.pop("q")
+        return nv.paged_attention(q, self.kc, self.vc, self.table, self.starts, ints(self.lens),
+                                  k_scale=self.k_scale, v_scale=self.v_scale, scale=self.scale,
+                                  check=kw.pop("check", True), **kw)
+
+    def reference(self):
+        """(o, tolerance) in 64 bits."""
+        t, G = self.tokens, self.heads // self.kv_heads
+        o = torch.zeros((t, self.heads, self.dim), dtype=torch.float64, device="cuda")
+        tol = torch.zeros_like(o)
+        first = 0
+        for r, (n, m) in enumerate(zip(self.lens, self.new)):
+            if m == 0:
+                continue
+            cap = min(n, self.cols * self.block)
+            pos = torch.arange(cap, device="cuda")
+            page = self.table[r].long()[pos // self.block]
+            there = (page >= 0) & (page < self.blocks)
+            pg = torch.where(there, page, 0)
+            p = n - m + torch.arange(m, device="cuda")
+            for h in range(self.kv_heads):
+                k, v = (c[pg, pos % self.block, h].double() if not self.f8 else
+                        c.view(torch.uint8)[pg, pos % self.block, h].view(F8).double()
+                        for c in (self.kc, self.vc))
+                k, v = k * self.k_scale, v * self.v_scale
+                q = self.q[first:first + m, h * G:(h + 1) * G].double()
+                s = torch.einsum("mgd,nd->mgn", q, k) * self.scale
+                mag = torch.einsum("mgd,nd->mgn", q.abs(), k.abs()) * self.scale
+                see = (there & (pos <= p[:, None]))[:, None, :]
+                s = torch.where(see, s, -torch.inf)
+                delta = torch.where(see, mag, 0.0).amax(-1) if cap else q.new_zeros(m, G)
+                delta = delta * self.dim * 2.0 ** -23
+                w = torch.exp(s - s.amax(-1, keepdim=True).clamp(min=-1e300)) if cap else s
+                tot = w.sum(-1, keepdim=True)
+                w = torch.where(tot > 0, w / tot.clamp(min=1e-300), 0.0)
+                v = torch.where(torch.isnan(v) & ~there[:, None], 0.0, v)
+                vis = see.expand(w.shape).any(1).any(0)
+                v = torch.where(vis[:, None], v, 0.0)
+                out = torch.einsum("mgn,nd->mgd", w, v)
+                A = torch.einsum("mgn,nd->mgd", w, v.abs())
+                n_vis = max(cap, 1)
+                rel = (2.0 ** -11 if self.f8 else 2.0 ** -8) + 2 * delta[..., None] + \
+                    2 * (2.0 ** -20 + (n_vis / 16 + 128) * 2.0 ** -23)
+                sl = (slice(first, first + m), slice(h * G, (h + 1) * G))
+                o[sl] = out
+                tol[sl] = 2.0 ** -8 * out.abs() + rel * A + 1e-30
+                if self.f8 and cap:
+                    tol[sl] += n_vis * 2.0 ** -25 * v.abs().max()
+            first += m
+        return o, tol
+
+
+def check_attention(b, **kw):
+    out = b.call(**kw)
+    ref, tol = b.reference()
+    got = out[:b.tokens].double()
+    assert torch.isfinite(got).all(), "a masked or unowned value reached a result"
+    err = (got - ref).abs()
+    worst = (err / tol.clamp(min=1e-30)).max().item() if err.numel() else 0.0
+    assert worst <= 1.0, f"error {worst:.3f} of the tolerance"
+    return out
+
+
+GEOMETRY = [(24, 4, 256), (8, 8, 128), (7, 1, 64), (32, 8, 128)]
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim", GEOMETRY)
+def test_decode_lengths(heads, kv_heads, dim, f8):
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300]
+    check_attention(Batch(1, lens, [1] * len(lens), heads, kv_heads, dim, 16, f8))
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim", GEOMETRY)
+def test_chunks(heads, kv_heads, dim, f8):
+    # whole prompts, chunks at the end of longer ones, one token, idle requests
+    lens, new = [45, 200, 70, 9, 130, 33], [45, 31, 1, 0, 130, 8]
+    check_attention(Batch(2, lens, new, heads, kv_heads, dim, 32, f8, pad=3))
+
+
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "joint"])
+@pytest.mark.parametrize("block", [16, 48, 64, 256])
+def test_layouts_and_pages(layout, block):
+    for f8 in (False, True):
+        check_attention(Batch(3, [517, 1, 95, 256], [3, 1, 20, 1], 12, 2, 128, block, f8, layout))
+
+
+def test_empty_requests_and_rows_without_keys():
+    # no keys at all; more new tokens than keys (the first ones see none); idle requests around
+    b = Batch(4, [0, 5, 0, 20], [2, 0, 0, 30], 6, 2, 64, 16)
+    out = check_attention(b)
+    assert (out[:2] == 0).all() and (out[2:12] == 0).all()
+
+
+def test_pages_that_do_not_exist():
+    # entries of -1, past the cache and far past it; a table that ends before the length does
+    for f8 in (False, True):
+        holes = [(0, 0, -1), (0, 3, 10 ** 6), (1, 1, -(2 ** 31)), (1, 2, 2 ** 31 - 1)]
+        check_attention(Batch(5, [100, 60], [9, 4], 12, 2, 128, 16, f8, holes=holes))
+        b = Batch(6, [100, 60], [9, 4], 12, 2, 128, 16, f8)
+        b.lens = [100, 600]  # 600 tokens claimed, the table holds at most 128
+        ref, tol = b.reference()
+        got = b.call()[:b.tokens].double()
+        # request 0 as ever; request 1's rows see everything that its table holds: the last
+        # page's four unowned slots, which hold NaN, among it
+        assert ((got - ref).abs() <= tol)[:9].all()
+        assert torch.isnan(ref[9:]).all() and torch.isnan(got[9:]).all()
+        b = Batch(6, [100, 64], [9, 4], 12, 2, 128, 16, f8)
+        b.lens = [100, 600]  # the pages that are there are full
+        check_attention(b)
+
+
+def test_large_scores_and_rising_maxima():
+    # scores that rise along the context, so that running maxima move again and again
+    b = Batch(7, [900, 700], [5, 1], 12, 2, 128, 16, q_scale=8.0)
+    check_attention(b)
+    b = Batch(8, [900], [40], 6, 1, 256, 16, q_scale=8.0)
+    ramp = torch.linspace(0.1, 3.0, 900, device="cuda")
+    pos = torch.arange(900, device="cuda")
+    page = b.table[0].long()[pos // 16]
+    b.kc[page, pos % 16] = (b.kc[page, pos % 16].float() * ramp[:, None, None]).bfloat16()
+    check_attention(b)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_many_requests_and_long_context(f8):
+    rng = np.random.default_rng(9)
+    lens = [int(x) for x in rng.integers(1, 400, 300)]
+    check_attention(Batch(9, lens, [1] * 300, 8, 2, 64, 16, f8))
+    check_attention(Batch(10, [20011], [8], 24, 4, 256, 64, f8))
+    check_attention(Batch(11, [3001, 2500], [500, 333], 12, 2, 128, 16, f8))
+
+
+def test_rows_behind_the_last_token_stay():
+    b = Batch(12, [40, 50], [3, 1], 8, 2, 128, 16, pad=5)
+    out = torch.full_like(b.q, 7.0)
+    check_attention(b, out=out)
+    assert (out[4:] == 7.0).all()
+
+
+def test_strided_rows():
+    b = Batch(13, [90, 33], [4, 2], 6, 2, 128, 16)
+    fused = torch.zeros((6, 3, 6, 2, 128), dtype=torch.bfloat16, device="cuda")
+    fused[:, 1, :, 0] = b.q
+    out = torch.zeros((6, 9, 200), dtype=torch.bfloat16, device="cuda")
+    want = b.call()
+    got = b.call(q=fused[:, 1, :, 0], out=out[:, 1:7, 8:136])
+    assert torch.equal(got, want)
+    assert (out[:, 7:] == 0).all() and (out[:, :, :8] == 0).all() and (out[:, :, 136:] == 0).all()
+
+
+def test_same_result_every_time_and_on_another_stream():
+    b = Batch(14, [3000, 5, 1200], [1, 5, 70], 24, 4, 256, 16)
+    want = b.call()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = [b.call(stream=other) for _ in range(3)] + [b.call()]
+    for o in got:
+        assert torch.equal(o, want)
+
+
+def test_captured_call_serves_later_lengths():
+    b = Batch(15, [200, 300], [1, 1], 8, 2, 128, 16)
+    lens, out = ints([200, 300]), torch.empty_like(b.q)
+    call = lambda: nv.paged_attention(b.q, b.kc, b.vc, b.table, b.starts, lens, out=out)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for now in ([200, 300], [17, 299], [1, 64]):
+        lens.copy_(ints(now))
+        out.zero_()
+        graph.replay()
+        b.lens = now
+        ref, tol = b.reference()
+        assert ((out.double() - ref).abs() <= tol).all()
+
+
+# ---------------------------------------------------------------- the cache's rows
+
+
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "joint"])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("tokens,heads,dim,block", [(1, 1, 64, 16), (37, 4, 256, 16),
+                                                    (1000, 3, 128, 48)])
+def test_append(tokens, heads, dim, block, f8, layout):
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    blocks = -(-tokens // block) + 2
+    kc, vc = make_cache(g, blocks, block, heads, dim, f8, layout)
+    rows = torch.randn((tokens, 3 * heads * dim + 8), generator=g, device="cuda").mul_(40)
+    rows[0, :4] = torch.tensor([float("inf"), -float("inf"), 1e30, 0.0], device="cuda")
+    rows = rows.to(torch.bfloat16)
+    k = rows[:, :heads * dim].view(tokens, heads, dim)
+    v = rows[:, 2 * heads * dim + 8:].view(tokens, heads, dim)
+    slots = torch.randperm(blocks * block, generator=g, device="cuda")[:tokens].to(torch.int32)
+    if tokens > 8:
+        slots[3], slots[5], slots[7] = -1, blocks * block, -2 ** 31  # skipped
+    before = [c.clone().view(torch.uint8) for c in (kc, vc)]
+    nv.kv_append(k, v, kc, vc, slots, 0.3, 0.7)
+    keep = (slots >= 0) & (slots < blocks * block)
+    at = slots[keep].long()
+    for cache, rows_, scale, old in ((kc, k, 0.3, before[0]), (vc, v, 0.7, before[1])):
+        want = old.view(cache.dtype)
+        new = rows_[keep]
+        if f8:
+            scale = torch.tensor(scale, dtype=torch.float32, device="cuda")
+            new = (new.float() / scale).clamp(-448, 448).to(F8)
+        w = want.view(torch.uint8).view(blocks, block, heads, -1)
+        w[at // block, at % block] = new.contiguous().view(torch.uint8).view(len(at), heads, -1)
+        got = cache.contiguous().view(torch.uint8).view(blocks, block, heads, -1)
+        assert torch.equal(got, w)
+
+
+# ---------------------------------------------------------------- the plan
+
+
+def plan_reference(lens, new, table, free, head, block, tokens):
+    """The definition, one request and token after another."""
+    lens, new = [max(x, 0) for x in lens], [max(x, 0) for x in new]
+    table, cols = table.copy(), table.shape[1]
+    starts, slots, request, positions, missing = [0], [], [], [], 0
+    for r, (n, m) in enumerate(zip(lens, new)):
+        for c in range(-(-n // block), -(-(n + m) // block)):
+            if c >= cols:
+                missing += 1
+                continue
+            if head < len(free):
+                table[r, c] = free[head]
+                head += 1
+            else:
+                table[r, c] = -1
+                missing += 1
+        for pos in range(n, n + m):
+            page = table[r, pos // block] if pos // block < cols else -1
+            slots.append(page * block + pos % block if page >= 0 else -1)
+            request.append(r)
+            positions.append(pos)
+        starts.append(starts[-1] + m)
+    more = tokens - len(slots)
+    return dict(table=table, starts=starts, lens=[a + b for a, b in zip(lens, new)],
+                slots=(slots + [-1] * more)[:tokens], request=(request + [-1] * more)[:tokens],
+                positions=(positions + [0] * more)[:tokens], head=[head], missing=[missing])
+
+
+def check_plan(lens, new, block, cols, n_free, head, tokens, ld=None):
+    rng = np.random.default_rng(len(lens) + block)
+    table = rng.integers(0, 10 ** 6, (len(lens), ld or cols)).astype(np.int32)
+    free = rng.permutation(n_free).astype(np.int32)
+    want = plan_reference(lens, new, table[:, :cols], free, head, block, tokens)
+    tab = torch.from_numpy(table).cuda()
+    p = nv.paged_plan(ints(lens), ints(new), tab[:, :cols], torch.from_numpy(free).cuda(),
+                      ints([head]), block, tokens)
+    full = table.copy()
+    full[:, :cols] = want.pop("table")
+    assert np.array_equal(tab.cpu().numpy(), full)
+    for name, w in want.items():
+        assert getattr(p, name).tolist() == list(w), name
+
+
+@pytest.mark.parametrize("block", [1, 16, 48, 128])
+@pytest.mark.parametrize("requests", [1, 2, 33, 700, 2000])
+def test_plan(requests, block):
+    rng = np.random.default_rng(requests)
+    lens = [int(x) for x in rng.integers(0, 500, requests)]
+    new = [int(x) for x in rng.choice([0, 1, 1, 8, 40], requests)]
+    pages = sum(-(-(a + b) // block) - -(-a // block) for a, b in zip(lens, new))
+    check_plan(lens, new, block, 541, pages + 9, 4, sum(new) + 7)
+
+
+def test_plan_runs_out():
+    check_plan([10, 0, 30, 16], [10, 50, 3, 1], 16, 3, 4, 2, 70)   # list spent, table too short
+    check_plan([10, 0, 30, 16], [10, 50, 3, 1], 16, 9, 2, 2, 64)   # nothing left
+    check_plan([10, 0, 30, 16], [10, 50, 3, 1], 16, 9, 2, 9, 64)   # a head past the list
+    check_plan([10, 0, 30, 16], [10, 50, 3, 1], 16, 9, 20, 0, 20)  # fewer outputs than tokens
+    check_plan([5, -3, 7], [-1, 4, 0], 16, 4, 20, 0, 9, ld=11)     # negative counts as zero
+    check_plan([5, 6], [0, 0], 16, 4, 20, 3, 5)                    # nothing new
+
+
+def test_plan_without_requests():
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    p = nv.paged_plan(e, e, e.view(0, 0), ints([3, 4]), ints([1]), 16, 3)
+    assert p.starts.tolist() == [0] and p.slots.tolist() == [-1] * 3
+    assert p.head.tolist() == [1] and p.missing.tolist() == [0]
+
+
+# ---------------------------------------------------------------- together
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_steps_of_a_batch_from_empty_tables(f8):
+    """Plan, append and attend over several steps, as a serving loop does: a prefill, single
+    tokens, verify rounds; the cache grows page by page."""
+    heads, kv_heads, dim, block = 12, 2, 128, 16
+    g = torch.Generator(device="cuda").manual_seed(21)
+    n, blocks = 3, 40
+    kc, vc = make_cache(g, blocks, block, kv_heads, dim, f8)
+    table = torch.full((n, 12), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(blocks, generator=g, device="cuda").to(torch.int32)
+    lens, head = ints([0] * n), ints([0])
+    scale = 0.02 if f8 else 1.0
+    for new in ([20, 1, 70], [1, 1, 1], [8, 0, 8], [1, 30, 1]):
+        t = sum(new)
+        plan = nv.paged_plan(lens, ints(new), table, free, head, block, tokens=t + 2)
+        qkv = torch.randn((t + 2, heads + 2 * kv_heads, dim), generator=g, device="cuda").bfloat16()
+        nv.kv_append(qkv[:, heads:heads + kv_heads], qkv[:, heads + kv_heads:], kc, vc,
+                     plan.slots, scale, scale)
+        b = Batch.__new__(Batch)
+        b.lens, b.new, b.f8, b.dim, b.heads, b.kv_heads = plan.lens.tolist(), new, f8, dim, \
+            heads, kv_heads
+        b.kc, b.vc, b.k_scale, b.v_scale, b.table = kc, vc, scale, scale, table
+        b.q, b.tokens, b.starts, b.scale = qkv[:, :heads], t, plan.starts, dim ** -0.5
+        b.block, b.blocks, b.cols = block, blocks, table.shape[1]
+        check_attention(b)
+        lens, head = plan.lens, plan.head
+        assert plan.missing.item() == 0
