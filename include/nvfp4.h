@@ -507,6 +507,40 @@ int nvfp4_paged_attn_workspace_bytes(int dim, size_t* bytes);
 int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cache,
                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Low-rank adapters of many requests beside a shared projection (nvfp4_gemv's y of the same x):
+ *   out[m] = bf16( y[m] + scales[a] * B_a (A_a x[m]) ),  a = index[m],  rows 0..ranks[a]-1 of A_a
+ * summed in fp32 (A x kept in fp32 and multiplied as two bf16 values, to 2^-17).  A row whose
+ * index is not in 0..adapters-1 keeps y[m].  Rows that share an adapter read it once.
+ *   a: bf16, row r of adapter s at a + s*a_stride + r*a_ld (K values);  b: bf16, output n of
+ *   adapter s at b + s*b_stride + n*b_ld (rank values).  Rows of a, and columns of b, at or past an
+ *   adapter's own rank are not used, whatever they hold.
+ *   rank: the most of any adapter, a multiple of 8, at most NVFP4_LORA_MAX_RANK.
+ *   x, y, out, a, b 16-byte aligned, their strides multiples of 8;  n % 8 == 0, k % 8 == 0. */
+#define NVFP4_LORA_MAX_RANK 128
+
+typedef struct {
+    const void* a;
+    int64_t a_stride, a_ld;
+    const void* b;
+    int64_t b_stride, b_ld;
+    const float* scales;   /* [adapters], device */
+    const int32_t* ranks;  /* [adapters], device, each cut to 0..rank; NULL: all are rank */
+    const int32_t* index;  /* [M], device */
+    int32_t adapters;      /* 0..32767 */
+    int32_t rank;
+} nvfp4_lora_t;
+
+/* Workspace bytes of nvfp4_lora_add (sums of A x over the ranges K is split into). */
+int nvfp4_lora_workspace_bytes(int m, int adapters, int rank, int64_t k, size_t* bytes);
+
+/* M = 0..NVFP4_MAX_ROWS rows.  out may be y itself (same leading dimension); otherwise it overlaps
+ * neither y nor x.  workspace: 16-byte aligned, the above bytes, of any content; it holds no error
+ * word (nothing in the call waits).  Calls that may run at the same time need different ones.
+ * Errors: NVFP4_ERR_NULL, _SHAPE, _ROWS, _ALIGN, _ALIAS, _WORKSPACE, _ARCH, _LAUNCH. */
+int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const void* y,
+                   int64_t ldy, void* out, int64_t ldo, int m, int64_t n, int64_t k,
+                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* The workspace's error word after the work enqueued so far has run (synchronises the
  * stream): 0 if no kernel hit a bounded wait's limit, else a nonzero code -- 2 or 3: a wait on
  * the shared-memory ring (a weight copy that never landed), 4: a chain's dependency wait --

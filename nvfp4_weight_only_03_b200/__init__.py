@@ -25,8 +25,9 @@ import torch
 
 from . import build as _build
 from . import serving as _serving
-from .serving import (KV_BF16, KV_E4M3, MAX_REQUESTS, PagedPlan, kv_append, paged_attention,
-                      paged_attention_workspace_bytes, paged_plan)
+from .serving import (KV_BF16, KV_E4M3, MAX_REQUESTS, PagedPlan, kv_append, lora_add,
+                      lora_workspace_bytes, paged_attention, paged_attention_workspace_bytes,
+                      paged_plan)
 
 _LIB_PATH = _build.LIB
 _lib = None
@@ -135,6 +136,24 @@ class SigmoidGate:
     def struct(self, m: int, k: int) -> Prologue:
         t, ldt = _rows_arg(self.gate, m, k, "gate")
         return Prologue(kind=PROLOGUE_SIGMOID_GATE, gate=t.data_ptr(), ld_gate=ldt)
+
+
+class Lora:
+    """Adapters of a projection's rows (lora_add): a [adapters][rank][K], b [adapters][N][rank],
+    index [M] (-1: none), scales [adapters], ranks [adapters] or None."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
+                 scales: torch.Tensor, ranks: torch.Tensor = None):
+        self.a, self.b, self.index, self.scales, self.ranks = a, b, index, scales, ranks
+
+    def add(self, y: torch.Tensor, x: torch.Tensor, stream=None) -> torch.Tensor:
+        return lora_add(y, x, self.a, self.b, self.index, self.scales, ranks=self.ranks, out=y,
+                        stream=stream)
+
+
+def _check_lora(lora, prologue):
+    if prologue is not None and lora is not None:
+        raise ValueError("lora and prologue cannot be combined: the adapters read x as given")
 
 
 class PackInfo(ctypes.Structure):
@@ -322,7 +341,8 @@ def _check_error(ws: torch.Tensor, stream, where: str):
 
 def gemv(w: torch.Tensor, s: torch.Tensor, g: float, x: torch.Tensor, y: torch.Tensor = None,
          ws: torch.Tensor = None, stream=None, prefetch_weights: bool = False,
-         wide_tensor: bool = False, prologue=None, check: bool = False) -> torch.Tensor:
+         wide_tensor: bool = False, prologue=None, check: bool = False,
+         lora: Lora = None) -> torch.Tensor:
     """y[m][n] = bf16(g * sum_k e2m1(w[n][k]) * e4m3(s[n][k/16]) * x[m][k]) on the GPU.
 
     prefetch_weights: stream w and s before earlier work on the stream has finished
@@ -332,7 +352,10 @@ def gemv(w: torch.Tensor, s: torch.Tensor, g: float, x: torch.Tensor, y: torch.T
     prologue: AddRmsNorm or SigmoidGate, applied to x inside the call (its x' lives in the
     workspace, so a caller's ws must hold workspace_bytes_wide(n, k, m)).
     ws: the workspace; by default the cached one of (x's device, stream).
-    check: synchronise after the call and raise if a bounded wait in its kernels gave up."""
+    check: synchronise after the call and raise if a bounded wait in its kernels gave up.
+    lora: adapters of the rows, added to y (lora_add in place: y is rounded before and after);
+    not with a prologue."""
+    _check_lora(lora, prologue)
     n, k = _weight_args(w, s)
     x, m, ldx = _x_args(x, k, getattr(prologue, "x_dtype", torch.bfloat16))
     pro = None if prologue is None else prologue.struct(m, k)
@@ -351,6 +374,8 @@ def gemv(w: torch.Tensor, s: torch.Tensor, g: float, x: torch.Tensor, y: torch.T
     _check(st, "nvfp4_gemv")
     if check:
         _check_error(ws, stream, "nvfp4_gemv")
+    if lora is not None:
+        lora.add(y, x, stream)
     return y
 
 
@@ -402,14 +427,18 @@ def gemv_dual(wg: torch.Tensor, sg: torch.Tensor, gg: float, wu: torch.Tensor, s
 
 def gemv_multi(weights, x: torch.Tensor, ys=None, ws: torch.Tensor = None, stream=None,
                prefetch_weights: bool = False, prologue=None, wide_tensor: bool = False,
-               check: bool = False) -> list:
+               check: bool = False, lora=None) -> list:
     """Several GEMVs sharing x in one pass (nvfp4_gemv_multi): weights is a list of up to
     MAX_OUTPUTS (w, s, g) triples with the same K; returns [y_0, y_1, ...], y_o the GEMV of
     weight o as gemv computes it.  ys: optional preallocated outputs, one per weight.
     prologue: as for gemv, applied once to the shared x.  wide_tensor: 9..128 rows on the
     tensor-core tier, each output bitwise as gemv(..., wide_tensor=True) computes it.
-    ws, check: as for gemv."""
+    ws, check: as for gemv.  lora: one Lora (or None) per weight, as for gemv."""
     weights = list(weights)
+    lora = None if lora is None else list(lora)
+    _check_lora(lora, prologue)
+    if lora is not None and len(lora) != len(weights):
+        raise ValueError("one lora (or None) per weight")
     if not 1 <= len(weights) <= MAX_OUTPUTS:
         raise ValueError(f"1..{MAX_OUTPUTS} weights, got {len(weights)}")
     shapes = [_weight_args(w, s) for w, s, _ in weights]
@@ -445,6 +474,9 @@ def gemv_multi(weights, x: torch.Tensor, ys=None, ws: torch.Tensor = None, strea
     _check(st, "nvfp4_gemv_multi")
     if check:
         _check_error(ws, stream, "nvfp4_gemv_multi")
+    for y, l in zip(result, lora or ()):
+        if l is not None:
+            l.add(y, x, stream)
     return result
 
 

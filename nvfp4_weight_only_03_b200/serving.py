@@ -1,9 +1,11 @@
 """Binding of the operators between the projections of a decode step: block tables and slot maps
-(paged_plan), new rows into the paged cache (kv_append), attention over it (paged_attention).
+(paged_plan), new rows into the paged cache (kv_append), attention over it (paged_attention), and
+adapters beside a projection (lora_add).
 
     plan = paged_plan(lens, new, table, free, head, block_size, tokens=T)
     kv_append(k, v, k_cache, v_cache, plan.slots)
     o = paged_attention(q, k_cache, v_cache, table, plan.starts, plan.lens)
+    y = lora_add(y, x, a, b, index, scales)  # y += scales[i] * B_i (A_i x), i = index[row]
 
 Lengths, tables and indexes stay on the device: no call copies anything to the host or waits, and
 a captured call serves later lengths.  Every tensor of a call lies on one device, which need not
@@ -50,6 +52,13 @@ class AttnStruct(ctypes.Structure):
                 ("lens", _p), ("scale", _f32)]
 
 
+class LoraStruct(ctypes.Structure):
+    """nvfp4_lora_t."""
+    _fields_ = [("a", _p), ("a_stride", _i64), ("a_ld", _i64), ("b", _p), ("b_stride", _i64),
+                ("b_ld", _i64), ("scales", _p), ("ranks", _p), ("index", _p), ("adapters", _i32),
+                ("rank", _i32)]
+
+
 def declare(L) -> None:
     """Argument types of the entry points bound here."""
     sz = ctypes.c_size_t
@@ -58,8 +67,12 @@ def declare(L) -> None:
     L.nvfp4_kv_append.argtypes = [_p, _i64, _i64, _p, _i64, _i64, _i64, _p, kv, _p]
     L.nvfp4_paged_attn_workspace_bytes.argtypes = [ctypes.c_int, ctypes.POINTER(sz)]
     L.nvfp4_paged_attn.argtypes = [ctypes.POINTER(AttnStruct), kv, _p, sz, _p]
+    L.nvfp4_lora_workspace_bytes.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64,
+                                             ctypes.POINTER(sz)]
+    L.nvfp4_lora_add.argtypes = [ctypes.POINTER(LoraStruct), _p, _i64, _p, _i64, _p, _i64,
+                                 ctypes.c_int, _i64, _i64, _p, sz, _p]
     for f in (L.nvfp4_paged_plan, L.nvfp4_kv_append, L.nvfp4_paged_attn_workspace_bytes,
-              L.nvfp4_paged_attn):
+              L.nvfp4_paged_attn, L.nvfp4_lora_workspace_bytes, L.nvfp4_lora_add):
         f.restype = ctypes.c_int
 
 
@@ -288,3 +301,79 @@ def paged_attention_workspace_bytes(dim: int) -> int:
                   "nvfp4_paged_attn_workspace_bytes")
         _attn_bytes[key] = int(b.value)
     return _attn_bytes[key]
+
+
+def _rows(t: torch.Tensor, name: str, m: int, n: int) -> int:
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 2 or tuple(t.shape) != (m, n) or (n > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{m}][{n}] with unit inner stride, got {list(t.shape)}")
+    return t.stride(0) if m > 1 else n
+
+
+_lora_bytes: dict = {}
+
+
+def lora_workspace_bytes(m: int, adapters: int, rank: int, k: int) -> int:
+    """Bytes of a lora_add workspace on the current device."""
+    key = (torch.cuda.current_device(), m, adapters, rank, k)
+    if key not in _lora_bytes:
+        b = ctypes.c_size_t()
+        nv = _nv()
+        nv._check(nv.lib().nvfp4_lora_workspace_bytes(m, adapters, rank, k, ctypes.byref(b)),
+                  "nvfp4_lora_workspace_bytes")
+        _lora_bytes[key] = int(b.value)
+    return _lora_bytes[key]
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+             index: torch.Tensor, scales: torch.Tensor, ranks: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+             stream=None) -> torch.Tensor:
+    """out[m] = bf16(y[m] + scales[i] * B_i (A_i x[m])), i = index[m] (nvfp4_lora_add).
+
+    y: bfloat16 [M][N], a projection of x: bfloat16 [M][K] (M up to 128).  a: bfloat16
+    [adapters][rank][K]; b: bfloat16 [adapters][N][rank]; scales: float32 [adapters]; ranks:
+    int32 [adapters], how many of `rank` each adapter uses (all by default).  index: int32 [M];
+    a row whose index names no adapter (-1) keeps y.  out: y itself for an update in place, or
+    a tensor apart from y and x; by default a new one.  ws: lora_workspace_bytes(M, adapters,
+    rank, K) bytes of any content, by default the cached workspace of (device, stream)."""
+    if x.dim() == 1:
+        x = x.unsqueeze(0)
+    dev = _device(y, x=x, a=a, b=b, index=index, scales=scales, ranks=ranks, out=out, ws=ws)
+    for name, t in (("a", a), ("b", b)):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16")
+        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name} must be 3-D with unit inner stride")
+    s, rank, k = a.shape
+    n = b.shape[1]
+    if b.shape[0] != s or b.shape[2] != rank:
+        raise ValueError(f"b must be [{s}][N][{rank}], got {list(b.shape)}")
+    m = y.shape[0]
+    ldy, ldx = _rows(y, "y", m, n), _rows(x, "x", m, k)
+    _ints(index, "index", (m,))
+    if ranks is not None:
+        _ints(ranks, "ranks", (s,))
+    if scales.dtype != torch.float32:
+        raise TypeError("scales must be float32")
+    if tuple(scales.shape) != (s,) or not scales.is_contiguous():
+        raise ValueError(f"scales must be contiguous [{s}]")
+    nv = _nv()
+    with _running(dev, stream) as st:
+        if out is None:
+            out = torch.empty((m, n), dtype=y.dtype, device=dev)
+        ldo = _rows(out, "out", m, n)
+        need = lora_workspace_bytes(m, s, rank, k)
+        if ws is None:
+            ws = _workspace("lora", need, dev)
+        l = LoraStruct(
+            a=a.data_ptr(), a_stride=a.stride(0) if s > 1 else rank * k,
+            a_ld=a.stride(1) if rank > 1 else k, b=b.data_ptr(),
+            b_stride=b.stride(0) if s > 1 else n * rank, b_ld=b.stride(1) if n > 1 else rank,
+            scales=scales.data_ptr(), ranks=None if ranks is None else ranks.data_ptr(),
+            index=index.data_ptr(), adapters=s, rank=rank)
+        nv._check(nv.lib().nvfp4_lora_add(ctypes.byref(l), x.data_ptr(), ldx, y.data_ptr(), ldy,
+                                          out.data_ptr(), ldo, m, n, k, ws.data_ptr(),
+                                          ws.numel() * ws.element_size(), st), "nvfp4_lora_add")
+    return out
