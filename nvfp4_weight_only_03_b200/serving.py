@@ -24,6 +24,8 @@ import torch
 KV_BF16, KV_E4M3 = 0, 1
 MAX_REQUESTS = 8192
 
+_lib = None  # the loaded library, set by declare
+
 _p, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 
@@ -74,6 +76,12 @@ def declare(L) -> None:
     for f in (L.nvfp4_paged_plan, L.nvfp4_kv_append, L.nvfp4_paged_attn_workspace_bytes,
               L.nvfp4_paged_attn, L.nvfp4_lora_workspace_bytes, L.nvfp4_lora_add):
         f.restype = ctypes.c_int
+    global _lib
+    _lib = L
+
+
+def _load():
+    return _nv().lib()
 
 
 def _nv():
@@ -81,90 +89,117 @@ def _nv():
     return nv
 
 
-def _device(first: torch.Tensor, **others) -> torch.device:
-    """The one CUDA device of a call's tensors."""
+# A call takes tens of microseconds on the device at most, so what it does on the host counts:
+# the usual case (the tensors' device is current, no stream given) asks torch for plain numbers
+# only; any other enters the device and the stream and starts again.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(first: torch.Tensor, stream) -> bool:
+    """Whether the call has to enter another device or stream first."""
     if not first.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-    return first.device
+    return stream is not None or first.get_device() != torch.cuda.current_device()
 
 
 @contextlib.contextmanager
-def _running(dev: torch.device, stream):
-    """Makes the call's device and stream current; yields the stream's handle."""
-    if stream is None:
-        if torch.cuda.current_device() == dev.index:
-            yield torch.cuda.current_stream(dev).cuda_stream
+def _entered(first: torch.Tensor, stream):
+    dev = first.device
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
         else:
-            with torch.cuda.device(dev):
-                yield torch.cuda.current_stream(dev).cuda_stream
-        return
-    st = _nv()._stream_obj(stream, dev)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        yield st.cuda_stream
+            with torch.cuda.stream(_nv()._stream_obj(stream, dev)):
+                yield
 
 
-def _ints(t: torch.Tensor, name: str, shape) -> torch.Tensor:
+def _same_device(index: int, name: str, t: torch.Tensor) -> None:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _ints(t: torch.Tensor, name: str, n: int, index: int) -> int:
+    """Address of a contiguous int32 [n] on the call's device."""
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
-    return t
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{n}], got {list(t.shape)}")
+    if t.get_device() != index:
+        _same_device(index, name, t)
+    return t.data_ptr()
 
 
-def _table_args(table: torch.Tensor, rows: int):
+def _table_args(table: torch.Tensor, rows: int, index: int):
     if table.dtype != torch.int32:
         raise TypeError("table must be int32")
-    if table.dim() != 2 or table.shape[0] != rows or (table.shape[1] > 1 and table.stride(1) != 1):
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != rows or (shape[1] > 1 and table.stride(1) != 1):
         raise ValueError(f"table must be [{rows}][columns] with unit inner stride")
-    cols = table.shape[1]
+    _same_device(index, "table", table)
+    cols = shape[1]
     return cols, table.stride(0) if rows > 1 else cols
 
 
-def _heads(t: torch.Tensor, name: str):
+def _heads(t: torch.Tensor, name: str, index: int):
     """(token stride, head stride) of a bf16 [tokens][heads][dim] view."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 3 or t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1:
         raise ValueError(f"{name} must be [tokens][heads][dim] with unit inner stride")
-    n, h, d = t.shape
-    head = t.stride(1) if h > 1 else d
-    return t.stride(0) if n > 1 else max(h * head, d), head
+    _same_device(index, name, t)
+    head = stride[1] if shape[1] > 1 else shape[2]
+    return stride[0] if shape[0] > 1 else max(shape[1] * head, shape[2]), head
 
 
-def _cache_args(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float,
-                v_scale: float) -> KvCacheStruct:
-    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or \
-            v_cache.dtype != k_cache.dtype:
+def _cache_args(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float, v_scale: float,
+                index: int) -> KvCacheStruct:
+    dtype = k_cache.dtype
+    if (dtype != torch.bfloat16 and dtype != torch.float8_e4m3fn) or v_cache.dtype != dtype:
         raise TypeError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must be [blocks][block_size][heads][dim]")
-    blocks, block, heads, dim = k_cache.shape
-
-    def strides(c):
-        slot, head = c.stride(1), c.stride(2) if heads > 1 else dim
-        return c.stride(0) if blocks > 1 else block * slot, slot, head
-
-    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1 or strides(k_cache) != strides(v_cache):
+    blocks, block, heads, dim = shape
+    stride = k_cache.stride()
+    same = stride == v_cache.stride()
+    page, slot, head, one = stride
+    if heads == 1 or blocks <= 1 or not same:  # the stride of a single head or page says nothing
+        def used(st):
+            return (st[0] if blocks > 1 else block * st[1], st[1], st[2] if heads > 1 else dim,
+                    st[3])
+        page, slot, head, one = used(stride)
+        same = used(v_cache.stride()) == (page, slot, head, one)
+    if one != 1 or not same:
         raise ValueError("k_cache and v_cache must have the same strides, the inner one 1")
-    bs, ss, hs = strides(k_cache)
-    return KvCacheStruct(
-        k=k_cache.data_ptr(), v=v_cache.data_ptr(),
-        type=KV_BF16 if k_cache.dtype == torch.bfloat16 else KV_E4M3, heads=heads, dim=dim,
-        block_size=block, blocks=blocks, block_stride=bs, slot_stride=ss, head_stride=hs,
-        k_scale=float(k_scale), v_scale=float(v_scale))
+    _same_device(index, "k_cache", k_cache)
+    _same_device(index, "v_cache", v_cache)
+    return KvCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(),
+                         KV_BF16 if dtype == torch.bfloat16 else KV_E4M3, heads, dim, block,
+                         blocks, page, slot, head, k_scale, v_scale)
 
 
-def _workspace(kind: str, need: int, dev: torch.device) -> torch.Tensor:
+def _workspace(kind: str, need: int, index: int, st: int) -> torch.Tensor:
     """The cached workspace of (device, current stream), or, while a graph is captured, one of
     the graph's own: two graphs never share one."""
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
         ws[:512].zero_()
         return ws
-    return _nv()._cached_workspace(kind, need, dev, torch.cuda.current_stream(dev))
+    ws = _workspaces.get((kind, index, st))
+    if ws is None or ws.numel() < need:
+        dev = torch.device("cuda", index)
+        # this cache holds the stream, so that its handle stays its own
+        ws = _nv()._cached_workspace(kind, need, dev, torch.cuda.current_stream(dev))
+        _workspaces[(kind, index, st)] = ws
+    return ws
+
+
+_workspaces: dict = {}
+
+
+def _fail(status: int, where: str):
+    raise _nv().Nvfp4Error(status, where)
 
 
 class PagedPlan(NamedTuple):
@@ -189,30 +224,28 @@ def paged_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free:
     list is spent).  tokens: length of the per-token outputs; those behind the last token are
     inert (slot -1, request -1, position 0).  out: the outputs to fill, as an earlier call
     returned them (none of them may be one of the inputs); by default new ones."""
+    if _elsewhere(lens, stream):
+        with _entered(lens, stream):
+            return paged_plan(lens, new, table, free, head, block_size, tokens, out)
+    index = lens.get_device()
     n = lens.shape[0]
-    dev = _device(lens, new=new, table=table, free=free, head=head)
-    _ints(lens, "lens", (n,))
-    _ints(new, "new", (n,))
-    _ints(free, "free", (free.numel(),))
-    _ints(head, "head", (1,))
-    cols, ld = _table_args(table, n)
+    cols, ld = _table_args(table, n, index)
     sizes = (n + 1, n, tokens, tokens, tokens, 1, 1)
-    with _running(dev, stream) as st:
-        if out is None:
-            out = PagedPlan(*(torch.empty(s, dtype=torch.int32, device=dev) for s in sizes))
-        for name, t, s in zip(PagedPlan._fields, out, sizes):
-            _ints(t, "out." + name, (s,))
-        _device(lens, **{"out." + k: t for k, t in out._asdict().items()})
-        a = PlanStruct(
-            lens=lens.data_ptr(), new_tokens=new.data_ptr(), requests=n,
-            block_size=int(block_size), table=table.data_ptr(), ld_table=ld, table_columns=cols,
-            free_pages=free.data_ptr(), free_count=free.numel(), head=head.data_ptr(),
-            tokens=int(tokens), starts=out.starts.data_ptr(), lens_out=out.lens.data_ptr(),
-            slots=out.slots.data_ptr(), request=out.request.data_ptr(),
-            positions=out.positions.data_ptr(), head_out=out.head.data_ptr(),
-            missing=out.missing.data_ptr())
-        nv = _nv()
-        nv._check(nv.lib().nvfp4_paged_plan(ctypes.byref(a), st), "nvfp4_paged_plan")
+    if out is None:
+        if tokens < 0:
+            raise ValueError("tokens must not be negative")
+        out = PagedPlan._make(lens.new_empty(2 * n + 3 + 3 * tokens).split_with_sizes(sizes))
+        o = [t.data_ptr() for t in out]
+    else:
+        o = [_ints(t, "out." + name, size, index)
+             for name, t, size in zip(PagedPlan._fields, out, sizes)]
+    a = PlanStruct(_ints(lens, "lens", n, index), _ints(new, "new", n, index), n, block_size,
+                   table.data_ptr(), ld, cols, _ints(free, "free", free.numel(), index),
+                   free.numel(), _ints(head, "head", 1, index), tokens, o[0], o[1], o[2], o[3],
+                   o[4], o[5], o[6])
+    status = (_lib or _load()).nvfp4_paged_plan(a, _raw_stream(index))
+    if status:
+        _fail(status, "nvfp4_paged_plan")
     return out
 
 
@@ -226,19 +259,22 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     with an inner one of 1, the same for both); a float8 cache holds e4m3(x / scale).  slots:
     int32 [tokens], page * block_size + place; rows with a negative slot, or one past the last
     page, are skipped."""
-    dev = _device(k, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots)
-    c = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    ldk, hk = _heads(k, "k")
-    ldv, hv = _heads(v, "v")
-    n = k.shape[0]
-    if k.shape != v.shape or tuple(k.shape[1:]) != (c.heads, c.dim):
+    if _elsewhere(k, stream):
+        with _entered(k, stream):
+            return kv_append(k, v, k_cache, v_cache, slots, k_scale, v_scale)
+    index = k.get_device()
+    c = _cache_args(k_cache, v_cache, k_scale, v_scale, index)
+    ldk, hk = _heads(k, "k", index)
+    ldv, hv = _heads(v, "v", index)
+    shape = k.shape
+    n = shape[0]
+    if shape != v.shape or shape[1] != c.heads or shape[2] != c.dim:
         raise ValueError(f"k and v must be [tokens][{c.heads}][{c.dim}]")
-    _ints(slots, "slots", (n,))
-    nv = _nv()
-    with _running(dev, stream) as st:
-        nv._check(nv.lib().nvfp4_kv_append(k.data_ptr(), ldk, hk, v.data_ptr(), ldv, hv, n,
-                                           slots.data_ptr(), ctypes.byref(c), st),
-                  "nvfp4_kv_append")
+    status = (_lib or _load()).nvfp4_kv_append(
+        k.data_ptr(), ldk, hk, v.data_ptr(), ldv, hv, n, _ints(slots, "slots", n, index), c,
+        _raw_stream(index))
+    if status:
+        _fail(status, "nvfp4_kv_append")
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -255,36 +291,40 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     paged_attention_workspace_bytes(dim) bytes, zero-filled before its first use; by default
     the cached one of (device, stream), or the graph's own during a capture.  check: synchronise
     and raise if a bounded wait in the kernel gave up."""
-    dev = _device(q, k_cache=k_cache, v_cache=v_cache, table=table, starts=starts, lens=lens,
-                  out=out, ws=ws)
-    c = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    ldq, hq = _heads(q, "q")
-    tokens, heads, dim = q.shape
+    if _elsewhere(q, stream):
+        with _entered(q, stream):
+            return paged_attention(q, k_cache, v_cache, table, starts, lens, scale, k_scale,
+                                   v_scale, out, ws, None, check)
+    index = q.get_device()
+    c = _cache_args(k_cache, v_cache, k_scale, v_scale, index)
+    ldq, hq = _heads(q, "q", index)
+    shape = q.shape
+    tokens, heads, dim = shape
     if dim != c.dim or heads % max(c.heads, 1):
         raise ValueError(f"q must be [tokens][heads][{c.dim}], heads a multiple of {c.heads}")
     n = lens.shape[0]
-    _ints(lens, "lens", (n,))
-    _ints(starts, "starts", (n + 1,))
-    cols, ld = _table_args(table, n)
-    nv = _nv()
-    with _running(dev, stream) as st:
-        if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
-        if out.shape != q.shape:
-            raise ValueError(f"out must be {list(q.shape)}")
-        ldo, ho = _heads(out, "out")
-        if ws is None:
-            ws = _workspace("attn", paged_attention_workspace_bytes(dim), dev)
-        a = AttnStruct(
-            q=q.data_ptr(), ldq=ldq, q_head_stride=hq, o=out.data_ptr(), ldo=ldo,
-            o_head_stride=ho, tokens=tokens, heads=heads, requests=n, table=table.data_ptr(),
-            ld_table=ld, table_columns=cols, starts=starts.data_ptr(), lens=lens.data_ptr(),
-            scale=float(dim ** -0.5 if scale is None else scale))
-        nv._check(nv.lib().nvfp4_paged_attn(ctypes.byref(a), ctypes.byref(c), ws.data_ptr(),
-                                            ws.numel() * ws.element_size(), st),
-                  "nvfp4_paged_attn")
-        if check:
-            nv._check_error(ws, st, "nvfp4_paged_attn")
+    cols, ld = _table_args(table, n, index)
+    if out is None:
+        out = q.new_empty(shape)
+        ldo, ho = heads * dim, dim
+    else:
+        if out.shape != shape:
+            raise ValueError(f"out must be {list(shape)}")
+        ldo, ho = _heads(out, "out", index)
+    st = _raw_stream(index)
+    if ws is None:
+        ws = _workspace("attn", paged_attention_workspace_bytes(dim), index, st)
+    else:
+        _same_device(index, "ws", ws)
+    a = AttnStruct(q.data_ptr(), ldq, hq, out.data_ptr(), ldo, ho, tokens, heads, n,
+                   table.data_ptr(), ld, cols, _ints(starts, "starts", n + 1, index),
+                   _ints(lens, "lens", n, index), dim ** -0.5 if scale is None else scale)
+    status = (_lib or _load()).nvfp4_paged_attn(a, c, ws.data_ptr(),
+                                                ws.numel() * ws.element_size(), st)
+    if status:
+        _fail(status, "nvfp4_paged_attn")
+    if check:
+        _nv()._check_error(ws, st, "nvfp4_paged_attn")
     return out
 
 
@@ -303,11 +343,12 @@ def paged_attention_workspace_bytes(dim: int) -> int:
     return _attn_bytes[key]
 
 
-def _rows(t: torch.Tensor, name: str, m: int, n: int) -> int:
+def _rows(t: torch.Tensor, name: str, m: int, n: int, index: int) -> int:
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 2 or tuple(t.shape) != (m, n) or (n > 1 and t.stride(1) != 1):
+    if t.shape != (m, n) or (n > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [{m}][{n}] with unit inner stride, got {list(t.shape)}")
+    _same_device(index, name, t)
     return t.stride(0) if m > 1 else n
 
 
@@ -338,42 +379,47 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     a row whose index names no adapter (-1) keeps y.  out: y itself for an update in place, or
     a tensor apart from y and x; by default a new one.  ws: lora_workspace_bytes(M, adapters,
     rank, K) bytes of any content, by default the cached workspace of (device, stream)."""
+    if _elsewhere(y, stream):
+        with _entered(y, stream):
+            return lora_add(y, x, a, b, index, scales, ranks, out, ws)
     if x.dim() == 1:
         x = x.unsqueeze(0)
-    dev = _device(y, x=x, a=a, b=b, index=index, scales=scales, ranks=ranks, out=out, ws=ws)
+    dev = y.get_device()
     for name, t in (("a", a), ("b", b)):
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be bfloat16")
         if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
             raise ValueError(f"{name} must be 3-D with unit inner stride")
+        _same_device(dev, name, t)
     s, rank, k = a.shape
     n = b.shape[1]
-    if b.shape[0] != s or b.shape[2] != rank:
+    if b.shape != (s, n, rank):
         raise ValueError(f"b must be [{s}][N][{rank}], got {list(b.shape)}")
     m = y.shape[0]
-    ldy, ldx = _rows(y, "y", m, n), _rows(x, "x", m, k)
-    _ints(index, "index", (m,))
-    if ranks is not None:
-        _ints(ranks, "ranks", (s,))
+    ldy, ldx = _rows(y, "y", m, n, dev), _rows(x, "x", m, k, dev)
     if scales.dtype != torch.float32:
         raise TypeError("scales must be float32")
-    if tuple(scales.shape) != (s,) or not scales.is_contiguous():
+    if scales.shape != (s,) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous [{s}]")
-    nv = _nv()
-    with _running(dev, stream) as st:
-        if out is None:
-            out = torch.empty((m, n), dtype=y.dtype, device=dev)
-        ldo = _rows(out, "out", m, n)
-        need = lora_workspace_bytes(m, s, rank, k)
-        if ws is None:
-            ws = _workspace("lora", need, dev)
-        l = LoraStruct(
-            a=a.data_ptr(), a_stride=a.stride(0) if s > 1 else rank * k,
-            a_ld=a.stride(1) if rank > 1 else k, b=b.data_ptr(),
-            b_stride=b.stride(0) if s > 1 else n * rank, b_ld=b.stride(1) if n > 1 else rank,
-            scales=scales.data_ptr(), ranks=None if ranks is None else ranks.data_ptr(),
-            index=index.data_ptr(), adapters=s, rank=rank)
-        nv._check(nv.lib().nvfp4_lora_add(ctypes.byref(l), x.data_ptr(), ldx, y.data_ptr(), ldy,
-                                          out.data_ptr(), ldo, m, n, k, ws.data_ptr(),
-                                          ws.numel() * ws.element_size(), st), "nvfp4_lora_add")
+    _same_device(dev, "scales", scales)
+    if out is None:
+        out = y.new_empty((m, n))
+        ldo = n
+    else:
+        ldo = _rows(out, "out", m, n, dev)
+    st = _raw_stream(dev)
+    if ws is None:
+        ws = _workspace("lora", lora_workspace_bytes(m, s, rank, k), dev, st)
+    else:
+        _same_device(dev, "ws", ws)
+    sa, sb = a.stride(), b.stride()
+    l = LoraStruct(a.data_ptr(), sa[0] if s > 1 else rank * k, sa[1] if rank > 1 else k,
+                   b.data_ptr(), sb[0] if s > 1 else n * rank, sb[1] if n > 1 else rank,
+                   scales.data_ptr(), None if ranks is None else _ints(ranks, "ranks", s, dev),
+                   _ints(index, "index", m, dev), s, rank)
+    status = (_lib or _load()).nvfp4_lora_add(l, x.data_ptr(), ldx, y.data_ptr(), ldy,
+                                              out.data_ptr(), ldo, m, n, k, ws.data_ptr(),
+                                              ws.numel() * ws.element_size(), st)
+    if status:
+        _fail(status, "nvfp4_lora_add")
     return out
