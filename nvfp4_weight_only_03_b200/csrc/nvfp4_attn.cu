@@ -187,6 +187,7 @@ __device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int c) {
 template <int TK, int THREADS>
 __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, int64_t* sums) {
     const int tid = threadIdx.x;
+    if (tid == 0) start->r = -1;  // behind the first __syncthreads at the latest
     const int per = (p.requests + THREADS - 1) / THREADS;
     const int r0 = min(tid * per, p.requests), r1 = min(r0 + per, p.requests);
     int64_t mine = 0;
@@ -246,6 +247,9 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
         }
     }
     __syncthreads();
+    // lengths that change while the call runs (another stream writes them) may leave no row tile
+    // to start in: the results are then whatever they are, but nothing is read out of bounds
+    if (g.end > g.begin && start->r < 0) g.end = g.begin;
     return g;
 }
 
@@ -315,133 +319,160 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     if (left == 0) {
         if (tid == 0) p.cuts[blockIdx.x].parts = 0;
     } else if (warp == kTmaWarp) {
-        // ---- K and V tiles, in the order of the MMAs: K0 K1 V0 K2 V1 ... V(n-1).  Lane i copies
-        // box i of a tile: `box` keys of one page (and 64 values of them); keys past the end, and
-        // pages that do not exist, are boxes outside the tensor, which arrive as zeros.
+        // ---- K and V tiles, in the order of the MMAs: K0 K1 V0 K2 V1 ... V(n-1).  A tile is
+        // TK / box groups of `box` keys of one page each (lane i knows group i's page and place),
+        // and a group is a box per 64 values.  Keys past the end, and pages that do not exist, are
+        // boxes outside the tensor, which arrive as zeros.  One elected lane issues all of a tile's
+        // boxes: a divergent issue, a lane per box, took 95 cycles a box.
+        constexpr int N = F8 ? NR : NS, kMost = TK / 16;
         const int groups = TK / p.box;
-        constexpr int kInner = F8 ? 1 : C::kPanels;
-        const int boxes = groups * kInner;
-        const int g_of = lane % groups, panel = lane / groups;
-        int it = 0;
+        uint64_t* const fulls = F8 ? raw_full : full;
+        uint64_t* const empties = F8 ? raw_empty : empty;
+        uint8_t* const tiles = F8 ? raw : ring;
+        int slot = 0, it = 0;
+        uint32_t phase = 1;  // of `empties`: the first lap finds them free
         while (left > 0 && ok) {
             const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
             const int end = key_end(p, cur.q, cur.tile);
             const int32_t* const row = p.table + cur.r * p.ld_table;
-            auto page_at = [&](int j) {  // page of this lane's keys in unit j of the range
-                const int key = (cur.u + j) * TK + g_of * p.box;
-                if (j >= cnt || key >= end) return -1;
-                const int page = row[key / p.block];
-                return (unsigned)page < (unsigned)p.blocks ? page : -1;
+            // this lane's page and place in unit j of the range
+            auto page_at = [&](int j, int& place) {
+                const int key = (cur.u + j) * TK + lane * p.box;
+                place = 0;
+                if (j >= cnt || lane >= groups || key >= end) return p.outside;
+                const int col = key / p.block;
+                place = key - col * p.block;
+                return row[col];
             };
-            auto load = [&](const CUtensorMap* map, int j, int page) {
-                constexpr int N = F8 ? NR : NS;
-                const int slot = it % N;
-                uint64_t* const fb = F8 ? &raw_full[slot] : &full[slot];
-                uint64_t* const eb = F8 ? &raw_empty[slot] : &empty[slot];
-                if (it >= N && !mbar_wait(eb, (it / N - 1) & 1, stop_v)) {
+            auto load = [&](const CUtensorMap* map, int page, int place) {
+                if (!mbar_wait(&empties[slot], phase, stop_v)) {
                     ok = false;
                     return;
                 }
-                if (lane == 0) mbar_expect_tx(fb, F8 ? C::kRaw : C::kTile);
-                __syncwarp();
-                const int key = (cur.u + j) * TK + g_of * p.box;
-                const int w = page < 0 ? p.outside : page;
-                uint8_t* const dst = F8 ? raw + slot * C::kRaw : ring + slot * C::kTile;
-                for (int b = lane, pn = panel; b < boxes; b += 32, pn += 32 / groups) {
-                    if (F8)
-                        tma_load_4d(dst + g_of * p.box * D, map, 0, key % p.block, cur.h, w, fb);
-                    else
-                        tma_load_4d(dst + pn * (TK * 128) + g_of * p.box * 128, map, pn * 64,
-                                    key % p.block, cur.h, w, fb);
+                const int at = (unsigned)page < (unsigned)p.blocks ? page : p.outside;
+                int w[kMost], y[kMost];
+#pragma unroll
+                for (int i = 0; i < kMost; ++i) {
+                    w[i] = __shfl_sync(~0u, at, i);
+                    y[i] = __shfl_sync(~0u, place, i);
                 }
+                if (elect_one()) {
+                    uint64_t* const fb = &fulls[slot];
+                    uint8_t* const dst = tiles + slot * (F8 ? C::kRaw : C::kTile);
+                    mbar_expect_tx(fb, F8 ? C::kRaw : C::kTile);
+#pragma unroll
+                    for (int i = 0; i < kMost; ++i) {
+                        if (i >= groups) break;
+                        if (F8) {
+                            tma_load_4d(dst + i * p.box * D, map, 0, y[i], cur.h, w[i], fb);
+                        } else {
+#pragma unroll
+                            for (int pn = 0; pn < C::kPanels; ++pn)
+                                tma_load_4d(dst + pn * (TK * 128) + i * p.box * 128, map, pn * 64,
+                                            y[i], cur.h, w[i], fb);
+                        }
+                    }
+                }
+                __syncwarp();
                 ++it;
+                if (++slot == N) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             };
-            int page = page_at(0), ahead = page_at(1);
-            load(&map_k, 0, page);
+            // pages are read two units ahead
+            int place, place1, place2;
+            int page = page_at(0, place), page1 = page_at(1, place1);
+            load(&map_k, page, place);
             for (int j = 0; j < cnt && ok; ++j) {
-                const int later = page_at(j + 2);
-                if (j + 1 < cnt) load(&map_k, j + 1, ahead);
-                if (ok) load(&map_v, j, page);
-                page = ahead;
-                ahead = later;
+                const int page2 = page_at(j + 2, place2);
+                if (j + 1 < cnt) load(&map_k, page1, place1);
+                if (ok) load(&map_v, page, place);
+                page = page1;
+                place = place1;
+                page1 = page2;
+                place1 = place2;
             }
             left -= cnt;
             cur.next(p);
         }
         if (!ok) code = 5;
-        // a CTA that gives up leaves no copy in flight behind it
-        if (!ok) {
-            constexpr int N = F8 ? NR : NS;
-            for (int k = max(0, it - N); k < it; ++k) {
-                uint64_t* const fb = F8 ? &raw_full[k % N] : &full[k % N];
-                volatile int none = 0;
-                mbar_wait(fb, (k / N) & 1, &none, 10000000ull);
-            }
+        if (!ok) {  // a CTA that gives up leaves no copy in flight behind it
+            volatile int none = 0;
+            for (int k = max(0, it - N); k < it; ++k)
+                mbar_wait(&fulls[k % N], (k / N) & 1, &none, 20000000ll);
         }
     } else if (warp == kMmaWarp) {
-        // ---- MMAs, from one thread
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_16(!F8, TK, false), id_o = idesc_16(!F8, D, true);
-            const uint32_t q0 = smem_u32(q_tile);
-            int it = 0, g = 0, item = 0;
-            auto ready = [&](uint64_t* b, uint32_t parity) {
-                if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
-                return ok;
-            };
-            auto scores = [&](int at) {  // S = Q K^T of tile `at`
-                const int slot = it % NS;
-                if (!ready(&full[slot], (it / NS) & 1)) return;
-                tc_after_sync();
-                const uint32_t k0 = smem_u32(ring + slot * C::kTile);
+        // ---- MMAs: the warp waits together, one elected lane issues and commits
+        constexpr uint32_t id_s = idesc_16(!F8, TK, false), id_o = idesc_16(!F8, D, true);
+        const uint64_t q_desc = desc_k_major(smem_u32(q_tile));
+        const uint64_t k_desc = desc_k_major(smem_u32(ring));
+        const uint64_t v_desc = desc_mn_major(smem_u32(ring), TK * 128);
+        int slot = 0, g = 0, item = 0;
+        uint32_t phase = 0;  // of the ring
+        auto ready = [&](uint64_t* b, uint32_t parity) {
+            if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
+            return ok;
+        };
+        auto step = [&]() {
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        auto scores = [&](int at, bool last) {  // S = Q K^T of tile `at`
+            if (!ready(&full[slot], phase)) return;
+            __syncwarp();
+            tc_after_sync();
+            if (elect_one()) {
+                const uint64_t kd = k_desc + slot * (C::kTile >> 4);
+                const uint32_t d = tmem + C::kS + (at & 1) * TK;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(tmem + C::kS + (at & 1) * TK,
-                           desc_k_major(q0 + (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
-                           desc_k_major(k0 + (kk >> 2) * (TK * 128) + (kk & 3) * 32), id_s,
-                           kk > 0);
+                    mma_ss(d, q_desc + (((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                           kd + (((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4), id_s, kk > 0);
                 mma_commit(&empty[slot]);
                 mma_commit(&s_full[at & 1]);
-                ++it;
-            };
-            while (left > 0 && ok) {
-                const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
-                if (!ready(&q_full, item & 1)) break;
-                scores(g);
-                if (cnt == 1) mma_commit(&q_free);
-                for (int j = 0; j < cnt && ok; ++j) {
-                    if (j + 1 < cnt) {
-                        scores(g + 1);
-                        if (j + 2 == cnt) mma_commit(&q_free);
-                    }
-                    const int slot = it % NS;
-                    if (!ready(&full[slot], (it / NS) & 1)) break;
-                    if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
-                    if (j == 0 && item > 0 && !ready(&o_free, (item - 1) & 1)) break;
-                    tc_after_sync();
-                    const uint32_t v0 = smem_u32(ring + slot * C::kTile);
+                if (last) mma_commit(&q_free);
+            }
+            step();
+        };
+        while (left > 0 && ok) {
+            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+            if (!ready(&q_full, item & 1)) break;
+            scores(g, cnt == 1);
+            for (int j = 0; j < cnt && ok; ++j) {
+                if (j + 1 < cnt) scores(g + 1, j + 2 == cnt);
+                if (!ready(&full[slot], phase)) break;
+                if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
+                if (j == 0 && item > 0 && !ready(&o_free, (item - 1) & 1)) break;
+                __syncwarp();
+                tc_after_sync();
+                if (elect_one()) {
+                    const uint64_t vd = v_desc + slot * (C::kTile >> 4);
+                    const uint32_t a = tmem + C::kP + (g & 1) * (TK / 2);
 #pragma unroll
                     for (int kk = 0; kk < TK / 16; ++kk)
-                        mma_ts(tmem, tmem + C::kP + (g & 1) * (TK / 2) + kk * 8,
-                               desc_mn_major(v0 + kk * 2048, TK * 128), id_o,
+                        mma_ts(tmem, a + kk * 8, vd + kk * (2048 >> 4), id_o,
                                (j > 0 || kk > 0) ? 1u : 0u);
                     mma_commit(&empty[slot]);
                     mma_commit(&pv_done);
                     if (j + 1 == cnt) mma_commit(&o_full);
-                    ++it;
-                    ++g;
                 }
-                ++item;
-                left -= cnt;
-                cur.next(p);
+                step();
+                ++g;
             }
-            if (!ok) {  // let the MMAs that were issued end before tensor memory is freed
-                code = 6;
-                volatile int none = 0;
-                mma_commit(&drained);
-                mbar_wait(&drained, 0, &none, 10000000ull);
-            }
+            ++item;
+            left -= cnt;
+            cur.next(p);
         }
         __syncwarp();
+        if (!ok) {  // let the MMAs that were issued end before tensor memory is freed
+            code = 6;
+            volatile int none = 0;
+            if (elect_one()) mma_commit(&drained);
+            mbar_wait(&drained, 0, &none, 20000000ll);
+        }
     } else if (warp >= kQWarp && warp < kQWarp + kQWarps) {
         // ---- Q rows into the MMA's layout (K-major, 128-byte swizzle)
         const int t = tid - kQWarp * 32;
@@ -575,18 +606,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const bool busy = warp * 32 < rows;  // this warp has rows
             const int tok = (row0 + tid) / p.group;
             const int end = key_end(p, cur.q, cur.tile);
+            const bool mine = tid < rows;  // lanes past the rows compute on whatever is there
             // the last key this row sees
-            const int last = tid < rows ? min(cur.q.len - cur.q.n + tok, end - 1) : -1;
+            const int last = mine ? min(cur.q.len - cur.q.n + tok, end - 1) : INT32_MAX;
             const int32_t* const table = p.table + cur.r * p.ld_table;
-            auto holes_at = [&](int j) {  // lane i: whether 16 keys of the unit have no page
+            auto page_at = [&](int j) {  // lane i: the page of 16 keys of the unit
                 const int key = (cur.u + j) * TK + lane * 16;
-                if (j >= cnt || lane >= TK / 16 || key >= end) return false;
-                return (unsigned)table[key / p.block] >= (unsigned)p.blocks;
+                return j >= cnt || lane >= TK / 16 || key >= end ? 0 : table[key / p.block];
             };
             float m = -INFINITY, l = 0.f, c = p.c;
-            bool hole = holes_at(0);
+            int page = page_at(0);  // read a unit ahead
             for (int j = 0; j < cnt; ++j, ++g) {
-                const bool hole_next = holes_at(j + 1);
+                const int page_next = page_at(j + 1);
                 const int key0 = (cur.u + j) * TK;
                 if (!mbar_wait(&s_full[g & 1], (g >> 1) & 1, stop_v)) {
                     ok = false;
@@ -612,31 +643,42 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 }
                 __syncwarp();
                 // the scores are there, so the rows' scales are (q_full itself may be a phase on)
-                if (F8 && j == 0 && tid < rows) c *= q_scale[item & 1][tid];
+                if (F8 && j == 0 && mine) c *= q_scale[item & 1][tid];
                 if (busy) {
-                    uint32_t s[TK / 32][32];
-#pragma unroll
-                    for (int i = 0; i < TK / 32; ++i)
-                        tmem_ld32(tmem + lanes + C::kS + (g & 1) * TK + i * 32, s[i]);
-#pragma unroll
-                    for (int i = 0; i < TK / 32; ++i) tmem_wait_ld(s[i]);
-                    const uint32_t holes = __ballot_sync(~0u, hole);
+                    // 64 keys at a time.  The second half is kept in registers as well, or, where
+                    // 12 warps share the registers, read from tensor memory again.
+                    constexpr int H = TK / 64, kKeep = F8 ? 1 : H;
+                    uint32_t s[kKeep][2][32];
+                    const uint32_t holes = __ballot_sync(~0u, (unsigned)page >= (unsigned)p.blocks);
                     const int see = last - key0;  // keys 0..see of the unit
-                    if (holes || __any_sync(~0u, see < TK - 1)) {
+                    const bool masked = holes || __any_sync(~0u, see < TK - 1);
+                    auto fetch = [&](int h, uint32_t (&v)[2][32]) {
+                        const uint32_t from = tmem + lanes + C::kS + (g & 1) * TK + h * 64;
+                        tmem_ld32(from, v[0]);
+                        tmem_ld32(from + 32, v[1]);
+                        tmem_wait_ld(v[0]);
+                        tmem_wait_ld(v[1]);
+                        if (masked) {
 #pragma unroll
-                        for (int i = 0; i < TK; ++i)
-                            if (i > see || ((holes >> (i / 16)) & 1))
-                                s[i / 32][i % 32] = 0xff800000u;  // -inf
-                    }
+                            for (int i = 0; i < 64; ++i)
+                                if (h * 64 + i > see || ((holes >> (h * 4 + i / 16)) & 1))
+                                    v[i / 32][i % 32] = 0xff800000u;  // -inf
+                        }
+                    };
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < TK; ++i)
-                        mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i / 32][i % 32]));
+                    for (int h = 0; h < H; ++h) {
+                        fetch(h, s[h % kKeep]);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            mx[i & 3] =
+                                fmaxf(mx[i & 3], __uint_as_float(s[h % kKeep][i / 32][i % 32]));
+                    }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if (j == 0) {
                         m = top;
                     } else {
-                        const bool rise = (top - m) * c > 8.f;
+                        const bool rise = mine && (top - m) * c > 8.f;
                         if (__any_sync(~0u, rise)) {
                             const float f = rise ? exp2_approx((m - top) * c) : 1.f;
                             if (rise) m = top;
@@ -664,27 +706,29 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < TK / 64; ++i) {
+                    for (int h = 0; h < H; ++h) {
+                        if (kKeep < H) fetch(h, s[0]);
                         uint32_t w[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const int k = i * 64 + 2 * e;
-                            const float a = exp2_approx(
-                                fmaf(__uint_as_float(s[k / 32][k % 32]), c, -mc));
+                            const int k = 2 * e;
+                            const uint32_t(&v)[2][32] = s[h % kKeep];
+                            const float a =
+                                exp2_approx(fmaf(__uint_as_float(v[k / 32][k % 32]), c, -mc));
                             const float b = exp2_approx(
-                                fmaf(__uint_as_float(s[(k + 1) / 32][(k + 1) % 32]), c, -mc));
-                            sum[(2 * e) & 3] += a;
-                            sum[(2 * e + 1) & 3] += b;
+                                fmaf(__uint_as_float(v[k / 32][k % 32 + 1]), c, -mc));
+                            sum[k & 3] += a;
+                            sum[(k + 1) & 3] += b;
                             w[e] = pack16(F8, a, b);
                         }
-                        tmem_st32(tmem + lanes + C::kP + (g & 1) * (TK / 2) + i * 32, w);
+                        tmem_st32(tmem + lanes + C::kP + (g & 1) * (TK / 2) + h * 32, w);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_wait_st();
                 }
                 tc_before_sync();
                 mbar_arrive(&p_full[g & 1]);
-                hole = hole_next;
+                page = page_next;
             }
             if (!ok || !mbar_wait(&o_full, item & 1, stop_v)) {
                 ok = false;
@@ -700,14 +744,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 uint16_t* const out = p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +
                                       (int64_t)head * p.o_head_stride;
                 const float inv = l == 0.f ? 0.f : p.v_scale / l;
-                if (!whole && tid < rows)
+                if (!whole && mine)
                     p.part_ml[part] = make_float2(m == -INFINITY ? m : m * c, l);
 #pragma unroll 1
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
                     tmem_ld32(tmem + lanes + i * 32, o);
                     tmem_wait_ld(o);
-                    if (tid < rows) {
+                    if (mine) {
                         if (whole) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -742,7 +786,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     const int64_t x = range.end - cnt + cur.n - 1;  // its last unit
                     const int64_t e =
                         ((x + 1) * range.ctas + range.total - 1) / range.total - 1;
-                    cut.parts = (int)(e - blockIdx.x) + 1;
+                    cut.parts = (int)min(e - blockIdx.x + 1, (int64_t)(range.ctas - blockIdx.x));
                     cut.token0 = cur.q.token0;
                     cut.row0 = row0;
                     cut.rows = rows;
@@ -777,7 +821,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_attn_join_kernel(const 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int owner = blockIdx.x / kJoinSplit;
     const Cut cut = p.cuts[owner];
-    if (cut.parts == 0) return;
+    if (cut.parts <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kPer = D / 32;
     for (int row = (blockIdx.x % kJoinSplit) * kJoinWarps + warp; row < cut.rows;

@@ -140,8 +140,9 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
     for (int64_t i = me; i < wanted; i += stride) {
         const int r = last_at_most(first, p.requests, i);  // the last one: need > 0
         const int64_t old = ((int64_t)max(p.lens[r], 0) + p.block - 1) / p.block;
-        p.table[r * p.ld_table + old + i - first[r]] =
-            i < left ? p.free_pages[head + i] : -1;
+        const int64_t c = old + i - first[r];
+        // (always true unless the lengths change while the call runs)
+        if (c < p.columns) p.table[r * p.ld_table + c] = i < left ? p.free_pages[head + i] : -1;
     }
     for (int64_t t = me; t < p.tokens; t += stride) {
         int32_t slot = -1, req = -1, at = 0;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
             if (c < p.columns) {
                 const int64_t i = first[r] + c - old;
                 if (c < old) page = p.table[r * p.ld_table + c];
-                else if (i < left) page = p.free_pages[head + i];
+                else if (i >= 0 && i < left) page = p.free_pages[head + i];
             }
             const int64_t s = page * p.block + pos % p.block;
             if (page >= 0 && s <= INT32_MAX) slot = (int32_t)s;

@@ -39,23 +39,17 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
     return done != 0;
 }
 
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Bounded wait: false after limit_ns, or as soon as *stop is set (another role gave up).
+// Bounded wait: false after about a second (limit cycles), or once *stop is set (another role gave
+// up).  Both are looked at only every 64 tries: the usual wait is short, and a try already sleeps.
 __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, volatile int* stop,
-                                          uint64_t limit_ns = 1000000000ull) {
-    if (mbar_try(b, parity)) return true;
-    for (int it = 0; it < 32; ++it)
-        if (mbar_try(b, parity)) return true;
-    const uint64_t t0 = now_ns();
+                                          int64_t limit = 2000000000ll) {
+    int64_t t0 = 0;
     for (;;) {
-        for (int it = 0; it < 32; ++it)
+        for (int it = 0; it < 64; ++it)
             if (mbar_try(b, parity)) return true;
-        if (*stop || now_ns() - t0 > limit_ns) return false;
+        const int64_t t = clock64();
+        if (t0 == 0) t0 = t;
+        if (*stop || t - t0 > limit) return false;
     }
 }
 
@@ -81,6 +75,16 @@ __device__ __forceinline__ void tc_before_sync() {
 }
 __device__ __forceinline__ void tc_after_sync() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// One lane of a converged warp.  The compiler knows that one thread runs what this guards, and
+// so keeps descriptors and addresses in uniform registers, where tcgen05.mma wants them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // Shared-memory matrix descriptors, 128-byte swizzle.  K-major: rows of 128 bytes, 8-row atoms
