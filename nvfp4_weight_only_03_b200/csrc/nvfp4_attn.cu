@@ -117,6 +117,25 @@ __device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
     return r;
 }
 
+// Four e4m3 codes -> four f16 values times 2^-8, exact: an e4m3 code's exponent and mantissa,
+// seven bits, moved to the same place below f16's exponent bias (15 against 7); subnormals come
+// out right.  The factor goes into the scores' and the output's scale.  Shifts and masks instead of
+// cvt, whose rate is that of the exponentials, with which it would share a pipe.
+__device__ __forceinline__ void widen_scaled(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+    lo = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
+    hi = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
+}
+// The same by cvt, for words with a NaN code (which the above takes for 480).
+__device__ __forceinline__ void widen_nan(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t"
+        "mul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
+        : "=&r"(lo), "=&r"(hi)
+        : "r"(w), "r"(0x1c001c00u));  // 2^-8 twice
+}
+constexpr float kWidened = 256.f;
+
 // ---- the order of the work ---------------------------------------------------------------
 
 struct Request {
@@ -172,6 +191,15 @@ struct Cursor {
         n = units_of<TK>(p, q, tile);
     }
 };
+
+// The order in which the tiles of a row tile's `cnt` units go through the ring, K one unit ahead of
+// V: K0 K1 V0 K2 V1 ... K(cnt-1) V(cnt-2) V(cnt-1).
+__device__ __forceinline__ bool is_value(int i, int cnt) {
+    return i + 1 == 2 * cnt || (i > 0 && (i & 1) == 0);
+}
+__device__ __forceinline__ bool last_scores(int i, int cnt) {  // K(cnt-1)
+    return i == (cnt == 1 ? 0 : 2 * cnt - 3);
+}
 
 struct Range {
     int64_t begin, end, total;
@@ -337,7 +365,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const int32_t* const row = p.table + cur.r * p.ld_table;
             // this lane's page and place in unit j of the range
             auto page_at = [&](int j, int& place) {
-                const int key = (cur.u + j) * TK + lane * p.box;
+                const int key = (cur.u + j) * TK + lane * p.box;  // (j may be past cnt)
                 place = 0;
                 if (j >= cnt || lane >= groups || key >= end) return p.outside;
                 const int col = key / p.block;
@@ -380,18 +408,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     phase ^= 1;
                 }
             };
-            // pages are read two units ahead
-            int place, place1, place2;
-            int page = page_at(0, place), page1 = page_at(1, place1);
-            load(&map_k, page, place);
-            for (int j = 0; j < cnt && ok; ++j) {
-                const int page2 = page_at(j + 2, place2);
-                if (j + 1 < cnt) load(&map_k, page1, place1);
-                if (ok) load(&map_v, page, place);
-                page = page1;
-                place = place1;
-                page1 = page2;
-                place1 = place2;
+            // pages are read ahead of their unit's first box
+            int place0, place1, place2;
+            int page0 = page_at(0, place0), page1 = page_at(1, place1), page2 = page_at(2, place2);
+            for (int i = 0; i < 2 * cnt && ok; ++i) {
+                const bool v = is_value(i, cnt), head = v || i == 0;
+                load(v ? &map_v : &map_k, head ? page0 : page1, head ? place0 : place1);
+                if (v) {
+                    page0 = page1, place0 = place1;
+                    page1 = page2, place1 = place2;
+                    page2 = page_at(i / 2 + 2, place2);
+                }
             }
             left -= cnt;
             cur.next(p);
@@ -414,53 +441,51 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
             return ok;
         };
-        auto step = [&]() {
-            if (++slot == NS) {
-                slot = 0;
-                phase ^= 1;
-            }
-        };
-        auto scores = [&](int at, bool last) {  // S = Q K^T of tile `at`
-            if (!ready(&full[slot], phase)) return;
-            __syncwarp();
-            tc_after_sync();
-            if (elect_one()) {
-                const uint64_t kd = k_desc + slot * (C::kTile >> 4);
-                const uint32_t d = tmem + C::kS + (at & 1) * TK;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(d, q_desc + (((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
-                           kd + (((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4), id_s, kk > 0);
-                mma_commit(&empty[slot]);
-                mma_commit(&s_full[at & 1]);
-                if (last) mma_commit(&q_free);
-            }
-            step();
-        };
         while (left > 0 && ok) {
             const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
             if (!ready(&q_full, item & 1)) break;
-            scores(g, cnt == 1);
-            for (int j = 0; j < cnt && ok; ++j) {
-                if (j + 1 < cnt) scores(g + 1, j + 2 == cnt);
+            int at = g;  // the next unit's scores
+            for (int i = 0; i < 2 * cnt; ++i) {
                 if (!ready(&full[slot], phase)) break;
-                if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
-                if (j == 0 && item > 0 && !ready(&o_free, (item - 1) & 1)) break;
-                __syncwarp();
-                tc_after_sync();
-                if (elect_one()) {
-                    const uint64_t vd = v_desc + slot * (C::kTile >> 4);
-                    const uint32_t a = tmem + C::kP + (g & 1) * (TK / 2);
+                if (!is_value(i, cnt)) {  // S = Q K^T
+                    __syncwarp();
+                    tc_after_sync();
+                    if (elect_one()) {
+                        const uint64_t kd = k_desc + slot * (C::kTile >> 4);
+                        const uint32_t d = tmem + C::kS + (at & 1) * TK;
 #pragma unroll
-                    for (int kk = 0; kk < TK / 16; ++kk)
-                        mma_ts(tmem, a + kk * 8, vd + kk * (2048 >> 4), id_o,
-                               (j > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(&empty[slot]);
-                    mma_commit(&pv_done);
-                    if (j + 1 == cnt) mma_commit(&o_full);
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_ss(d, q_desc + (((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                                   kd + (((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4), id_s,
+                                   kk > 0);
+                        mma_commit(&empty[slot]);
+                        mma_commit(&s_full[at & 1]);
+                        if (last_scores(i, cnt)) mma_commit(&q_free);
+                    }
+                    ++at;
+                } else {  // O += P V
+                    const bool first = i <= 2 && (cnt == 1 || i == 2);
+                    if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
+                    if (first && item > 0 && !ready(&o_free, (item - 1) & 1)) break;
+                    __syncwarp();
+                    tc_after_sync();
+                    if (elect_one()) {
+                        const uint64_t vd = v_desc + slot * (C::kTile >> 4);
+                        const uint32_t a = tmem + C::kP + (g & 1) * (TK / 2);
+#pragma unroll
+                        for (int kk = 0; kk < TK / 16; ++kk)
+                            mma_ts(tmem, a + kk * 8, vd + kk * (2048 >> 4), id_o,
+                                   kk > 0 || !first);
+                        mma_commit(&empty[slot]);
+                        mma_commit(&pv_done);
+                        if (i + 1 == 2 * cnt) mma_commit(&o_full);
+                    }
+                    ++g;
                 }
-                step();
-                ++g;
+                if (++slot == NS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
             ++item;
             left -= cnt;
@@ -544,52 +569,58 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     } else if (F8 && warp >= kWidenWarp) {
         // ---- e4m3 tiles to f16 in the MMA's layout.  A lane takes 16 codes of a key: two 16-byte
         // pieces of its row; lanes 4..7 of 8 store theirs in the other order, so that 8 lanes
-        // always cover a panel's 128 bytes.
+        // always cover a panel's 128 bytes.  All of a thread's pieces have the same place in
+        // their rows.
         const int t = tid - kWidenWarp * 32;
-        int it = 0;
-        auto widen = [&](bool value, int key0, int end) {
-            const int rs = it % NR, ts = it % NS;
-            if (!mbar_wait(&raw_full[rs], (it / NR) & 1, stop_v) ||
-                (it >= NS && !mbar_wait(&empty[ts], (it / NS - 1) & 1, stop_v))) {
-                ok = false;
-                return;
-            }
-            const uint8_t* const src = raw + rs * C::kRaw;
-            uint8_t* const dst = ring + ts * C::kTile;
-            constexpr int kPer = D / 16;  // pieces per key
-#pragma unroll 4
-            for (int i = t; i < TK * kPer; i += kWidenWarps * 32) {
-                const int key = i / kPer, c = i % kPer;
-                uint4 w = *reinterpret_cast<const uint4*>(src + (size_t)i * 16);
-                // a value past the end must not meet a weight of zero as NaN or infinity
-                if (value && key0 + key >= end) w = make_uint4(0, 0, 0, 0);
-                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                uint32_t out[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-                        : "=r"(out[2 * j]), "=r"(out[2 * j + 1])
-                        : "r"(in[j]));
-                uint8_t* const row = dst + (c >> 2) * (TK * 128) + key * 128;
-                const int u0 = (c & 3) * 2, swap = (lane >> 2) & 1, x = key & 7;
-                const uint4 a = make_uint4(out[0], out[1], out[2], out[3]);
-                const uint4 b = make_uint4(out[4], out[5], out[6], out[7]);
-                *reinterpret_cast<uint4*>(row + (((u0 + swap) ^ x) << 4)) = swap ? b : a;
-                *reinterpret_cast<uint4*>(row + (((u0 + 1 - swap) ^ x) << 4)) = swap ? a : b;
-            }
-            fence_async_smem();
-            mbar_arrive(&full[ts]);
-            mbar_arrive(&raw_empty[rs]);
-            ++it;
-        };
+        constexpr int kPer = D / 16, kThr = kWidenWarps * 32, kPieces = TK * kPer / kThr;
+        constexpr int kStep = kThr / kPer;  // keys from one piece of a thread to the next
+        static_assert(kStep % 8 == 0, "the swizzle of a thread's pieces is one");
+        const int key = t / kPer, c = t % kPer, u0 = (c & 3) * 2, swap = (lane >> 2) & 1;
+        const int first = (c >> 2) * (TK * 128) + key * 128 + (((u0 + swap) ^ (key & 7)) << 4);
+        const int second =
+            (c >> 2) * (TK * 128) + key * 128 + (((u0 + 1 - swap) ^ (key & 7)) << 4);
+        int rs = 0, ts = 0;
+        uint32_t rphase = 0, tphase = 1;
         while (left > 0 && ok) {
             const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
-            const int end = key_end(p, cur.q, cur.tile), k0 = cur.u * TK;
-            widen(false, k0, end);
-            for (int j = 0; j < cnt && ok; ++j) {
-                if (j + 1 < cnt) widen(false, k0, end);
-                if (ok) widen(true, k0 + j * TK, end);
+            const int end = key_end(p, cur.q, cur.tile);
+            for (int i = 0; i < 2 * cnt; ++i) {
+                if (!mbar_wait(&raw_full[rs], rphase, stop_v) ||
+                    !mbar_wait(&empty[ts], tphase, stop_v)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* const src = raw + rs * C::kRaw + t * 16;
+                uint8_t* const dst = ring + ts * C::kTile;
+                // a value past the end must not meet a weight of zero as NaN or infinity: only the
+                // last tile of all, V(n-1), holds any
+                int valid = TK;
+                if (i + 1 == 2 * cnt) valid = end - (cur.u + cnt - 1) * TK;
+#pragma unroll 2
+                for (int x = 0; x < kPieces; ++x) {
+                    uint4 w = *reinterpret_cast<const uint4*>(src + x * kThr * 16);
+                    if (key + x * kStep >= valid) w = make_uint4(0, 0, 0, 0);
+                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t out[8], nan = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        widen_scaled(in[j], out[2 * j], out[2 * j + 1]);
+                        nan |= (in[j] & 0x7f7f7f7fu) + 0x01010101u;
+                    }
+                    if (nan & 0x80808080u) {  // a NaN code: rare, and only cvt knows it
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) widen_nan(in[j], out[2 * j], out[2 * j + 1]);
+                    }
+                    const uint4 a = make_uint4(out[0], out[1], out[2], out[3]);
+                    const uint4 b = make_uint4(out[4], out[5], out[6], out[7]);
+                    *reinterpret_cast<uint4*>(dst + first + x * kStep * 128) = swap ? b : a;
+                    *reinterpret_cast<uint4*>(dst + second + x * kStep * 128) = swap ? a : b;
+                }
+                fence_async_smem();
+                mbar_arrive(&raw_empty[rs]);
+                mbar_arrive(&full[ts]);
+                if (++rs == NR) rs = 0, rphase ^= 1;
+                if (++ts == NS) ts = 0, tphase ^= 1;
             }
             left -= cnt;
             cur.next(p);
@@ -1010,8 +1041,8 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     p.box = box;
     const int64_t cap = a.table_columns * kv.block_size;
     p.capacity = (int)(cap > INT32_MAX - 1024 ? INT32_MAX - 1024 : cap);
-    p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;
-    p.v_scale = f8 ? kv.v_scale : 1.f;
+    p.c = a.scale * (f8 ? kv.k_scale * kWidened : 1.f) * 1.4426950408889634f;
+    p.v_scale = f8 ? kv.v_scale * kWidened : 1.f;
     // a factor that left fp32's normal range would turn a masked score of -infinity into NaN
     if (!(p.c >= 1.1754944e-38f) || isinf(p.c)) return NVFP4_ERR_SHAPE;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
