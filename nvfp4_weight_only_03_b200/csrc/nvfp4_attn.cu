@@ -49,10 +49,26 @@ using nvfp4_host::misaligned;
 using nvfp4_host::overlaps;
 
 constexpr int kRows = 128;  // rows of a tile: the MMA's M and tensor memory's lanes
-constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kTmaWarp = 5, kQWarp = 6, kQWarps = 2;
-constexpr int kWidenWarp = 8, kWidenWarps = 4;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kQWarp = 10, kQWarps = 2;
+constexpr int kWidenWarp = 12, kWidenWarps = 4;
 constexpr int kTmemCols = 512;
-constexpr size_t kSmemBudget = 229376;  // of 232448: the rest holds barriers and 1 KB alignment
+constexpr size_t kSmemMost = 232448;  // shared memory of a block
+
+// The small things in shared memory, ahead of the tiles.
+template <int NS, int NR, bool F8>
+struct Small {
+    uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[NR];
+    uint64_t q_full, q_free, s_full[2], p_full[2], pv_done, o_full, o_free, drained;
+    int64_t sums[20];
+    int start[2][12];  // a Cursor: where the range begins; then, by turns, the softmax's next tile
+    uint32_t tmem;
+    int stop;
+    union {
+        float max[2][2][kRows];  // of a unit: [its parity][warpgroup][lane]
+        float2 ml[2][kRows];     // of a row tile, maximum and sum: [warpgroup][lane]
+    } row;
+    float q_scale[F8 ? 2 : 1][F8 ? kRows : 1];
+};
 
 template <int D, bool F8>
 struct Cfg {
@@ -62,16 +78,18 @@ struct Cfg {
     static constexpr int kTile = TK * D * 2;                // one K or V tile, 16-bit
     static constexpr int kRaw = F8 ? TK * D : 0;            // the same in e4m3
     static constexpr int kThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kQWarp + kQWarps);
+    static constexpr size_t kHead = F8 ? 4096 : 3072;       // Small, in front of the tiles
     static constexpr int kStages =
-        F8 ? (D == 64 ? 4 : 3) : (int)((kSmemBudget - kQBytes) / kTile);
+        F8 ? (D == 64 ? 4 : 3) : (int)((kSmemMost - kHead - kQBytes) / kTile);
     static constexpr int kRawStages =
-        F8 ? (int)((kSmemBudget - kQBytes - kStages * kTile) / (F8 ? kRaw : 1)) : 1;
+        F8 ? (int)((kSmemMost - kHead - kQBytes - kStages * kTile) / (F8 ? kRaw : 1)) : 1;
     static constexpr size_t kSmem =
-        1024 + kQBytes + (size_t)kStages * kTile + (F8 ? (size_t)kRawStages * kRaw : 0);
+        kHead + kQBytes + (size_t)kStages * kTile + (F8 ? (size_t)kRawStages * kRaw : 0);
+    using Shared = Small<kStages, kRawStages, F8>;
     // tensor memory columns: O, then two S, then two P (two 16-bit values per column)
     static constexpr int kS = D, kP = D + 2 * TK, kEnd = D + 2 * TK + TK;
     static_assert(kEnd <= kTmemCols, "tensor memory");
-    static_assert(kSmem <= kSmemBudget + 1024, "shared memory");
+    static_assert(kSmem <= kSmemMost && sizeof(Shared) <= kHead, "shared memory");
 };
 
 // A row tile that was cut: its parts lie with the CTAs `owner` (which holds its first unit) to
@@ -117,24 +135,13 @@ __device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
     return r;
 }
 
-// Four e4m3 codes -> four f16 values times 2^-8, exact: an e4m3 code's exponent and mantissa,
-// seven bits, moved to the same place below f16's exponent bias (15 against 7); subnormals come
-// out right.  The factor goes into the scores' and the output's scale.  Shifts and masks instead of
-// cvt, whose rate is that of the exponentials, with which it would share a pipe.
-__device__ __forceinline__ void widen_scaled(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-    lo = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
-    hi = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
-}
-// The same by cvt, for words with a NaN code (which the above takes for 480).
-__device__ __forceinline__ void widen_nan(uint32_t w, uint32_t& lo, uint32_t& hi) {
+// Four e4m3 codes -> four f16 values, exact.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t"
-        "mul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
         : "=&r"(lo), "=&r"(hi)
-        : "r"(w), "r"(0x1c001c00u));  // 2^-8 twice
+        : "r"(w));
 }
-constexpr float kWidened = 256.f;
 
 // ---- the order of the work ---------------------------------------------------------------
 
@@ -167,16 +174,27 @@ __device__ __forceinline__ int units_of(const Params& p, const Request& q, int t
     return max(1, (key_end(p, q, tile) + TK - 1) / TK);  // 1: rows without keys are written too
 }
 
+// What beginning and ending a row tile costs, in units: Q's rows, the first scores and the
+// epilogue pass without overlap, about as long as two units take.  The split counts it, or a CTA
+// with many short row tiles would be the last by far.
+constexpr int kTileCost = 2;
+
 template <int TK>
 struct Cursor {
     int r, h, tile, tiles, u, n;  // unit u of the row tile's n
+    int lead;                     // how much of kTileCost counts here: all, unless a cut fell in it
     Request q;
+    // Units of this row tile in a range with `left` to go; none: the range is done.
+    __device__ __forceinline__ int take(int64_t left) const {
+        return (int)min((int64_t)(n - u), left - lead);
+    }
     __device__ __forceinline__ void enter(const Params& p) {
         tiles = row_tiles(p, q);
         n = units_of<TK>(p, q, tile);
     }
     __device__ __forceinline__ void next(const Params& p) {  // the next row tile
         u = 0;
+        lead = kTileCost;
         if (++tile == tiles) {
             tile = 0;
             if (++h == p.kv_heads) {
@@ -197,10 +215,6 @@ struct Cursor {
 __device__ __forceinline__ bool is_value(int i, int cnt) {
     return i + 1 == 2 * cnt || (i > 0 && (i & 1) == 0);
 }
-__device__ __forceinline__ bool last_scores(int i, int cnt) {  // K(cnt-1)
-    return i == (cnt == 1 ? 0 : 2 * cnt - 3);
-}
-
 struct Range {
     int64_t begin, end, total;
     int ctas;
@@ -223,7 +237,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
         const Request q = request_of(p, r);
         const int tiles = row_tiles(p, q);
         int64_t s = 0;
-        for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t);
+        for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + kTileCost;
         mine += s * p.kv_heads;
     }
     int64_t incl = mine;
@@ -256,7 +270,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
             const Request q = request_of(p, r);
             const int tiles = row_tiles(p, q);
             int64_t s = 0;
-            for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t);
+            for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + kTileCost;
             if (at >= s * p.kv_heads) {
                 at -= s * p.kv_heads;
                 continue;
@@ -267,8 +281,10 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
             c.h = (int)(at / s);
             at -= c.h * s;
             c.tile = 0;
-            while (at >= units_of<TK>(p, q, c.tile)) at -= units_of<TK>(p, q, c.tile++);
-            c.u = (int)at;
+            while (at >= units_of<TK>(p, q, c.tile) + kTileCost)
+                at -= units_of<TK>(p, q, c.tile++) + kTileCost;
+            c.lead = (int)max((int64_t)kTileCost - at, (int64_t)0);
+            c.u = (int)max(at - kTileCost, (int64_t)0);
             c.enter(p);
             *start = c;
             break;
@@ -289,24 +305,26 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                       const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<D, F8>;
     constexpr int TK = C::TK, NS = C::kStages, NR = C::kRawStages;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    uint8_t* const base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* const q_tile = base;
-    uint8_t* const ring = base + C::kQBytes;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    typename C::Shared& sm = *reinterpret_cast<typename C::Shared*>(smem_raw);
+    uint8_t* const q_tile = smem_raw + C::kHead;
+    uint8_t* const ring = q_tile + C::kQBytes;
     uint8_t* const raw = ring + NS * C::kTile;
-    __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[NR], q_full,
-        q_free, s_full[2], p_full[2], pv_done, o_full, o_free, drained;
-    __shared__ uint32_t tmem_base;
-    __shared__ int stop;
-    __shared__ int64_t sums[C::kThreads / 32];
-    __shared__ Cursor<TK> start;
-    __shared__ float q_scale[2][kRows];
-
+    uint64_t *const full = sm.full, *const empty = sm.empty, *const s_full = sm.s_full,
+             *const p_full = sm.p_full;
+    // (the tiles' swizzle wants 1024-byte alignment, which the block's only allocation has)
+    if (smem_u32(smem_raw) & 1023u) {
+        if (threadIdx.x == 0) {
+            atomicCAS(p.error, 0, 10);
+            p.cuts[blockIdx.x].parts = 0;
+        }
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&tmem_base)),
+                         smem_u32(&sm.tmem)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -316,36 +334,39 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < NR; ++i) {
-            mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], kWidenWarps * 32);
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_empty[i], kWidenWarps * 32);
         }
-        mbar_init(&q_full, kQWarps * 32);
-        mbar_init(&q_free, 1);
+        mbar_init(&sm.q_full, kQWarps * 32);
+        mbar_init(&sm.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kSoftmaxWarps * 32);
+            mbar_init(&p_full[i], kSoftmaxWarps);
         }
-        mbar_init(&pv_done, 1);
-        mbar_init(&o_full, 1);
-        mbar_init(&drained, 1);
-        mbar_init(&o_free, kSoftmaxWarps * 32);
-        stop = 0;
+        mbar_init(&sm.pv_done, 1);
+        mbar_init(&sm.o_full, 1);
+        mbar_init(&sm.drained, 1);
+        mbar_init(&sm.o_free, kSoftmaxWarps);
+        sm.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&map_k);
         prefetch_map(&map_v);
     }
     tc_before_sync();
-    const Range range = find_range<TK, C::kThreads>(p, &start, sums);  // two __syncthreads
+    Cursor<TK>* const start = reinterpret_cast<Cursor<TK>*>(sm.start[0]);
+    static_assert(sizeof(Cursor<TK>) <= sizeof(sm.start[0]) && C::kThreads / 32 <= 20, "Small");
+    const Range range = find_range<TK, C::kThreads>(p, start, sm.sums);  // two __syncthreads
     tc_after_sync();
-    const uint32_t tmem = tmem_base;
-    volatile int* const stop_v = &stop;
+    const uint32_t tmem = sm.tmem;
+    volatile int* const stop_v = &sm.stop;
     int64_t left = range.end - range.begin;
-    Cursor<TK> cur = start;
+    Cursor<TK> cur = *start;
     bool ok = true;
     int code = 0;
 
+    if (tid == 0) p.cuts[blockIdx.x].parts = 0;
     if (left == 0) {
-        if (tid == 0) p.cuts[blockIdx.x].parts = 0;
+        // nothing to do
     } else if (warp == kTmaWarp) {
         // ---- K and V tiles, in the order of the MMAs: K0 K1 V0 K2 V1 ... V(n-1).  A tile is
         // TK / box groups of `box` keys of one page each (lane i knows group i's page and place),
@@ -354,13 +375,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // boxes: a divergent issue, a lane per box, took 95 cycles a box.
         constexpr int N = F8 ? NR : NS, kMost = TK / 16;
         const int groups = TK / p.box;
-        uint64_t* const fulls = F8 ? raw_full : full;
-        uint64_t* const empties = F8 ? raw_empty : empty;
+        uint64_t* const fulls = F8 ? sm.raw_full : full;
+        uint64_t* const empties = F8 ? sm.raw_empty : empty;
         uint8_t* const tiles = F8 ? raw : ring;
         int slot = 0, it = 0;
         uint32_t phase = 1;  // of `empties`: the first lap finds them free
         while (left > 0 && ok) {
-            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+            const int cnt = cur.take(left);
+            if (cnt <= 0) break;
             const int end = key_end(p, cur.q, cur.tile);
             const int32_t* const row = p.table + cur.r * p.ld_table;
             // this lane's page and place in unit j of the range
@@ -420,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     page2 = page_at(i / 2 + 2, place2);
                 }
             }
-            left -= cnt;
+            left -= cur.lead + cnt;
             cur.next(p);
         }
         if (!ok) code = 5;
@@ -442,69 +464,74 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             return ok;
         };
         while (left > 0 && ok) {
-            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
-            if (!ready(&q_full, item & 1)) break;
-            int at = g;  // the next unit's scores
-            for (int i = 0; i < 2 * cnt; ++i) {
-                if (!ready(&full[slot], phase)) break;
-                if (!is_value(i, cnt)) {  // S = Q K^T
-                    __syncwarp();
-                    tc_after_sync();
+            const int cnt = cur.take(left);
+            if (cnt <= 0) break;
+            if (!ready(&sm.q_full, item & 1)) break;
+            // K0 K1 V0 K2 V1 ...: unit j's weights are formed while unit j+1's scores are
+            for (int j = -1; j < cnt; ++j) {
+                if (j + 1 < cnt) {  // S = Q K^T of unit j + 1
+                    if (!ready(&full[slot], phase)) break;
                     if (elect_one()) {
                         const uint64_t kd = k_desc + slot * (C::kTile >> 4);
-                        const uint32_t d = tmem + C::kS + (at & 1) * TK;
+                        const int b = (g + 1 + (j < 0 ? -1 : 0)) & 1;
+                        const uint32_t d = tmem + C::kS + b * TK;
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             mma_ss(d, q_desc + (((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
                                    kd + (((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4), id_s,
                                    kk > 0);
+                        mma_commit(&s_full[b]);
                         mma_commit(&empty[slot]);
-                        mma_commit(&s_full[at & 1]);
-                        if (last_scores(i, cnt)) mma_commit(&q_free);
+                        if (j + 2 == cnt) mma_commit(&sm.q_free);
                     }
-                    ++at;
-                } else {  // O += P V
-                    const bool first = i <= 2 && (cnt == 1 || i == 2);
-                    if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
-                    if (first && item > 0 && !ready(&o_free, (item - 1) & 1)) break;
                     __syncwarp();
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (j >= 0) {  // O += P V of unit j
+                    if (!ready(&full[slot], phase)) break;
+                    if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
+                    if (j == 0 && item > 0 && !ready(&sm.o_free, (item - 1) & 1)) break;
                     tc_after_sync();
                     if (elect_one()) {
                         const uint64_t vd = v_desc + slot * (C::kTile >> 4);
                         const uint32_t a = tmem + C::kP + (g & 1) * (TK / 2);
 #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
-                            mma_ts(tmem, a + kk * 8, vd + kk * (2048 >> 4), id_o,
-                                   kk > 0 || !first);
+                            mma_ts(tmem, a + kk * 8, vd + kk * (2048 >> 4), id_o, kk > 0 || j > 0);
                         mma_commit(&empty[slot]);
-                        mma_commit(&pv_done);
-                        if (i + 1 == 2 * cnt) mma_commit(&o_full);
+                        mma_commit(&sm.pv_done);
+                        if (j + 1 == cnt) mma_commit(&sm.o_full);
                     }
+                    __syncwarp();
                     ++g;
-                }
-                if (++slot == NS) {
-                    slot = 0;
-                    phase ^= 1;
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             ++item;
-            left -= cnt;
+            left -= cur.lead + cnt;
             cur.next(p);
         }
         __syncwarp();
         if (!ok) {  // let the MMAs that were issued end before tensor memory is freed
             code = 6;
             volatile int none = 0;
-            if (elect_one()) mma_commit(&drained);
-            mbar_wait(&drained, 0, &none, 20000000ll);
+            if (elect_one()) mma_commit(&sm.drained);
+            mbar_wait(&sm.drained, 0, &none, 20000000ll);
         }
     } else if (warp >= kQWarp && warp < kQWarp + kQWarps) {
         // ---- Q rows into the MMA's layout (K-major, 128-byte swizzle)
         const int t = tid - kQWarp * 32;
         int item = 0;
         while (left > 0) {
-            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
-            if (item > 0 && !mbar_wait(&q_free, (item - 1) & 1, stop_v)) {
+            const int cnt = cur.take(left);
+            if (cnt <= 0) break;
+            if (item > 0 && !mbar_wait(&sm.q_free, (item - 1) & 1, stop_v)) {
                 ok = false;
                 break;
             }
@@ -526,43 +553,56 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
             } else {
-                // a warp per row: x 2^e with the largest magnitude in [2^14, 2^15), as f16
-                for (int r = warp - kQWarp; r < rows; r += kQWarps) {
-                    const uint16_t* const src = src_of(r);
-                    constexpr int kPer = D / 32;  // 2, 4 or 8 consecutive values per lane
-                    uint32_t w[kPer / 2];
+                // x 2^e with the row's largest magnitude in [2^14, 2^15), as f16.  D / 8 lanes take a
+                // row, 16 bytes each; a warp reads kBatch such groups of rows before it works on
+                // them, since a row alone is a memory latency.
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
+                const int sub = lane / kLanes, c = lane % kLanes;
+                for (int r0 = (warp - kQWarp) * kAtOnce; r0 < rows;
+                     r0 += kQWarps * kAtOnce * kBatch) {
+                    uint4 v[kBatch];
 #pragma unroll
-                    for (int i = 0; i < kPer / 2; ++i)
-                        w[i] = *reinterpret_cast<const uint32_t*>(src + lane * kPer + 2 * i);
-                    uint32_t big = 0;  // largest magnitude's bits; NaN and infinity are the largest
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = r0 + i * kQWarps * kAtOnce + sub;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (r < rows)
+                            v[i] = *reinterpret_cast<const uint4*>(src_of(r) + c * 8);
+                    }
 #pragma unroll
-                    for (int i = 0; i < kPer / 2; ++i)
-                        big = max(big, max((w[i] & 0x7fffu), (w[i] >> 16) & 0x7fffu));
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = r0 + i * kQWarps * kAtOnce + sub;
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t big = 0;  // largest magnitude's bits; NaN and infinity lead
 #pragma unroll
-                    for (int d = 16; d; d >>= 1) big = max(big, __shfl_xor_sync(~0u, big, d));
-                    // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value is
-                    // below 2^-50 has scores of zero to fp32 either way
-                    const int up = min(127 + 14 + 127 - (int)(big >> 7), 127 + 64);
-                    const float mul = __uint_as_float((uint32_t)up << 23);
-                    const float back = __uint_as_float((uint32_t)(254 - up) << 23);
-                    if (lane == 0) q_scale[item & 1][r] = back;
-                    uint8_t* const row = q_tile + r * 128;
+                        for (int e = 0; e < 4; ++e)
+                            big = max(big, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
 #pragma unroll
-                    for (int i = 0; i < kPer / 2; ++i) {
-                        const int el = lane * kPer + 2 * i;
-                        const uint32_t h =
-                            pack16(true, __uint_as_float(w[i] << 16) * mul,
-                                   __uint_as_float(w[i] & 0xffff0000u) * mul);
-                        *reinterpret_cast<uint32_t*>(
-                            row + (el >> 6) * (kRows * 128) +
-                            ((((el & 63) >> 3) ^ (r & 7)) << 4) + (el & 7) * 2) = h;
+                        for (int d = kLanes / 2; d; d >>= 1)
+                            big = max(big, __shfl_xor_sync(~0u, big, d));
+                        // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value
+                        // is below 2^-50 has scores of zero to fp32 either way
+                        const int up = min(127 + 14 + 127 - (int)(big >> 7), 127 + 64);
+                        const float mul = __uint_as_float((uint32_t)up << 23);
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            h[e] = pack16(true, __uint_as_float(w[e] << 16) * mul,
+                                          __uint_as_float(w[e] & 0xffff0000u) * mul);
+                        if (r < rows) {
+                            if (c == 0)
+                                sm.q_scale[item & 1][r] =
+                                    __uint_as_float((uint32_t)(254 - up) << 23);
+                            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kRows * 128) + r * 128 +
+                                                      (((c & 7) ^ (r & 7)) << 4)) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
                 }
             }
             fence_async_smem();
-            mbar_arrive(&q_full);
+            mbar_arrive(&sm.q_full);
             ++item;
-            left -= cnt;
+            left -= cur.lead + cnt;
             cur.next(p);
         }
         if (!ok) code = 7;
@@ -582,10 +622,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         int rs = 0, ts = 0;
         uint32_t rphase = 0, tphase = 1;
         while (left > 0 && ok) {
-            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+            const int cnt = cur.take(left);
+            if (cnt <= 0) break;
             const int end = key_end(p, cur.q, cur.tile);
             for (int i = 0; i < 2 * cnt; ++i) {
-                if (!mbar_wait(&raw_full[rs], rphase, stop_v) ||
+                if (!mbar_wait(&sm.raw_full[rs], rphase, stop_v) ||
                     !mbar_wait(&empty[ts], tphase, stop_v)) {
                     ok = false;
                     break;
@@ -601,43 +642,50 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     uint4 w = *reinterpret_cast<const uint4*>(src + x * kThr * 16);
                     if (key + x * kStep >= valid) w = make_uint4(0, 0, 0, 0);
                     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t out[8], nan = 0;
+                    uint32_t out[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        widen_scaled(in[j], out[2 * j], out[2 * j + 1]);
-                        nan |= (in[j] & 0x7f7f7f7fu) + 0x01010101u;
-                    }
-                    if (nan & 0x80808080u) {  // a NaN code: rare, and only cvt knows it
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) widen_nan(in[j], out[2 * j], out[2 * j + 1]);
-                    }
+                    for (int j = 0; j < 4; ++j) widen(in[j], out[2 * j], out[2 * j + 1]);
                     const uint4 a = make_uint4(out[0], out[1], out[2], out[3]);
                     const uint4 b = make_uint4(out[4], out[5], out[6], out[7]);
                     *reinterpret_cast<uint4*>(dst + first + x * kStep * 128) = swap ? b : a;
                     *reinterpret_cast<uint4*>(dst + second + x * kStep * 128) = swap ? a : b;
                 }
                 fence_async_smem();
-                mbar_arrive(&raw_empty[rs]);
+                mbar_arrive(&sm.raw_empty[rs]);
                 mbar_arrive(&full[ts]);
                 if (++rs == NR) rs = 0, rphase ^= 1;
                 if (++ts == NS) ts = 0, tphase ^= 1;
             }
-            left -= cnt;
+            left -= cur.lead + cnt;
             cur.next(p);
         }
         if (!ok) code = 8;
     } else if (warp < kSoftmaxWarps) {
-        // ---- softmax: thread = row = tensor memory lane
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        // ---- softmax: thread = row = tensor memory lane.  Two warpgroups take half of a unit's
+        // keys each and share the row's maximum.
+        // The warps meet at barriers, so they must all take the same way: one thread reads what
+        // comes next for all of them, and after a wait that gave up they go on (without waiting,
+        // on whatever is there) to the end of the range.
+        const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int g = 0, item = 0, ring_at = 0;
-        while (left > 0 && ok) {
-            const int cnt = (int)min((int64_t)(cur.n - cur.u), left);
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+            if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
+        };
+        while (left > 0) {
+            const int cnt = cur.take(left);
+            if (cnt <= 0) break;
+            if (tid == 0) {
+                Cursor<TK> after = cur;
+                after.next(p);
+                *reinterpret_cast<Cursor<TK>*>(sm.start[(item + 1) & 1]) = after;
+            }
             const int row0 = cur.tile * kRows;
             const int rows = (int)min((int64_t)kRows, (int64_t)cur.q.n * p.group - row0);
-            const bool busy = warp * 32 < rows;  // this warp has rows
-            const int tok = (row0 + tid) / p.group;
+            const bool busy = quarter * 32 < rows;  // this warp has rows
+            const bool mine = row < rows;  // lanes past the rows compute on whatever is there
+            const int tok = (row0 + row) / p.group;
             const int end = key_end(p, cur.q, cur.tile);
-            const bool mine = tid < rows;  // lanes past the rows compute on whatever is there
             // the last key this row sees
             const int last = mine ? min(cur.q.len - cur.q.n + tok, end - 1) : INT32_MAX;
             const int32_t* const table = p.table + cur.r * p.ld_table;
@@ -645,25 +693,95 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 const int key = (cur.u + j) * TK + lane * 16;
                 return j >= cnt || lane >= TK / 16 || key >= end ? 0 : table[key / p.block];
             };
-            float m = -INFINITY, l = 0.f, c = p.c;
             int page = page_at(0);  // read a unit ahead
+            float m = -INFINITY, l = 0.f, c = p.c;
+
+            // one unit's weights for this thread's keys
+            auto weigh = [&](int j) {
+                constexpr int W = TK / 2, kChunk = 32, kChunks = W / kChunk;  // keys per thread
+                const int col0 = wg * W;
+                const int key0 = (cur.u + j) * TK + col0;
+                uint32_t s[kChunks][kChunk];
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i)
+                    tmem_ld(tmem + lanes + C::kS + (g & 1) * TK + col0 + i * kChunk, s[i]);
+                const uint32_t holes =
+                    __ballot_sync(~0u, (unsigned)page >= (unsigned)p.blocks) >> (col0 / 16);
+                const int see = last - key0;  // keys 0..see of this thread's
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) tmem_wait_ld(s[i]);
+                if (holes || __any_sync(~0u, see < W - 1)) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        if (i > see || ((holes >> (i / 16)) & 1))
+                            s[i / kChunk][i % kChunk] = 0xff800000u;  // -inf
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i / kChunk][i % kChunk]));
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                sm.row.max[g & 1][wg][row] = top;
+                bar_sync(1 + quarter, 64);
+                top = fmaxf(top, sm.row.max[g & 1][wg ^ 1][row]);
+                if (j == 0) {
+                    m = top;
+                } else {
+                    const bool rise = mine && (top - m) * c > 8.f;
+                    if (__any_sync(~0u, rise)) {
+                        const float f = rise ? exp2_approx((m - top) * c) : 1.f;
+                        if (rise) m = top;
+                        l *= f;
+                        // these scores came after PV of unit g - 2, and that of unit g waits for
+                        // this warp: the phase is g - 1 or its completion, no other
+                        wait(&sm.pv_done, (g - 1) & 1);
+                        __syncwarp();
+                        tc_after_sync();
+#pragma unroll 1
+                        for (int i = 0; i < D / 64; ++i) {  // this warpgroup's half of O
+                            uint32_t o[32];
+                            tmem_ld(tmem + lanes + wg * (D / 2) + i * 32, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st(tmem + lanes + wg * (D / 2) + i * 32, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    uint32_t w[kChunk / 2];
+#pragma unroll
+                    for (int e = 0; e < kChunk / 2; ++e) {
+                        const float a =
+                            exp2_approx(fmaf(__uint_as_float(s[i][2 * e]), c, -mc));
+                        const float b =
+                            exp2_approx(fmaf(__uint_as_float(s[i][2 * e + 1]), c, -mc));
+                        sum[(2 * e) & 3] += a;
+                        sum[(2 * e + 1) & 3] += b;
+                        w[e] = pack16(F8, a, b);
+                    }
+                    tmem_st(tmem + lanes + C::kP + (g & 1) * (TK / 2) + (col0 + i * kChunk) / 2,
+                            w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+            };
+
             for (int j = 0; j < cnt; ++j, ++g) {
                 const int page_next = page_at(j + 1);
-                const int key0 = (cur.u + j) * TK;
-                if (!mbar_wait(&s_full[g & 1], (g >> 1) & 1, stop_v)) {
-                    ok = false;
-                    break;
-                }
+                wait(&s_full[g & 1], (g >> 1) & 1);
                 tc_after_sync();
-                if (!F8 && key0 + TK > end) {
+                const int unit0 = (cur.u + j) * TK;
+                if (!F8 && unit0 + TK > end) {
                     // values past the end are whatever the page held: zeros, so that their weights
                     // of zero add nothing
                     const int vi = ring_at + 2 * cnt - 1, slot = vi % NS;
-                    if (!mbar_wait(&full[slot], (vi / NS) & 1, stop_v)) {
-                        ok = false;
-                        break;
-                    }
-                    const int from = max(end - key0, 0);
+                    wait(&full[slot], (vi / NS) & 1);
+                    const int from = max(end - unit0, 0);
                     uint8_t* const v = ring + slot * C::kTile;
                     for (int i = tid; i < (TK - from) * (D / 8); i += kSoftmaxWarps * 32) {
                         const int key = from + i / (D / 8), x = i % (D / 8);
@@ -674,166 +792,85 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 }
                 __syncwarp();
                 // the scores are there, so the rows' scales are (q_full itself may be a phase on)
-                if (F8 && j == 0 && mine) c *= q_scale[item & 1][tid];
-                if (busy) {
-                    // 64 keys at a time.  The second half is kept in registers as well, or, where
-                    // 12 warps share the registers, read from tensor memory again.
-                    constexpr int H = TK / 64, kKeep = F8 ? 1 : H;
-                    uint32_t s[kKeep][2][32];
-                    const uint32_t holes = __ballot_sync(~0u, (unsigned)page >= (unsigned)p.blocks);
-                    const int see = last - key0;  // keys 0..see of the unit
-                    const bool masked = holes || __any_sync(~0u, see < TK - 1);
-                    auto fetch = [&](int h, uint32_t (&v)[2][32]) {
-                        const uint32_t from = tmem + lanes + C::kS + (g & 1) * TK + h * 64;
-                        tmem_ld32(from, v[0]);
-                        tmem_ld32(from + 32, v[1]);
-                        tmem_wait_ld(v[0]);
-                        tmem_wait_ld(v[1]);
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (h * 64 + i > see || ((holes >> (h * 4 + i / 16)) & 1))
-                                    v[i / 32][i % 32] = 0xff800000u;  // -inf
-                        }
-                    };
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        fetch(h, s[h % kKeep]);
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            mx[i & 3] =
-                                fmaxf(mx[i & 3], __uint_as_float(s[h % kKeep][i / 32][i % 32]));
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (j == 0) {
-                        m = top;
-                    } else {
-                        const bool rise = mine && (top - m) * c > 8.f;
-                        if (__any_sync(~0u, rise)) {
-                            const float f = rise ? exp2_approx((m - top) * c) : 1.f;
-                            if (rise) m = top;
-                            l *= f;
-                            // these scores came after PV of unit g - 2, and that of unit g waits
-                            // for this warp: the phase is g - 1 or its completion, no other
-                            if (!mbar_wait(&pv_done, (g - 1) & 1, stop_v)) {
-                                ok = false;
-                                break;
-                            }
-                            __syncwarp();
-                            tc_after_sync();
-#pragma unroll 1
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t o[32];
-                                tmem_ld32(tmem + lanes + i * 32, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(tmem + lanes + i * 32, o);
-                            }
-                        }
-                    }
-                    const float mc = m == -INFINITY ? 0.f : m * c;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        if (kKeep < H) fetch(h, s[0]);
-                        uint32_t w[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int k = 2 * e;
-                            const uint32_t(&v)[2][32] = s[h % kKeep];
-                            const float a =
-                                exp2_approx(fmaf(__uint_as_float(v[k / 32][k % 32]), c, -mc));
-                            const float b = exp2_approx(
-                                fmaf(__uint_as_float(v[k / 32][k % 32 + 1]), c, -mc));
-                            sum[k & 3] += a;
-                            sum[(k + 1) & 3] += b;
-                            w[e] = pack16(F8, a, b);
-                        }
-                        tmem_st32(tmem + lanes + C::kP + (g & 1) * (TK / 2) + h * 32, w);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_wait_st();
-                }
+                if (F8 && j == 0 && mine) c *= sm.q_scale[item & 1][row];
+                if (busy) weigh(j);
                 tc_before_sync();
-                mbar_arrive(&p_full[g & 1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[g & 1]);
                 page = page_next;
             }
-            if (!ok || !mbar_wait(&o_full, item & 1, stop_v)) {
-                ok = false;
-                break;
-            }
+            wait(&sm.o_full, item & 1);
             __syncwarp();
             tc_after_sync();
+
+            // ---- O: divided by the sum and written, or left as a part
+            sm.row.ml[wg][row] = make_float2(m == -INFINITY ? m : m * c, l);
+            bar_sync(5, kSoftmaxWarps * 32);
+            const float total = l + sm.row.ml[wg ^ 1][row].y;
+            bar_sync(5, kSoftmaxWarps * 32);  // its place serves the next unit's maxima
             const bool whole = cur.u == 0 && cnt == cur.n;
             const int which = cur.u == 0 ? 1 : 0;  // this CTA's cut at its end, or at its start
-            const int64_t part = ((int64_t)blockIdx.x * 2 + which) * kRows + tid;
+            const int64_t part0 = ((int64_t)blockIdx.x * 2 + which) * kRows;
+            const float inv = total == 0.f ? 0.f : p.v_scale / total;
+            if (!whole && mine && wg == 0)
+                p.part_ml[part0 + row] = make_float2(m == -INFINITY ? m : m * c, total);
             if (busy) {
-                const int head = cur.h * p.group + (row0 + tid) - tok * p.group;
-                uint16_t* const out = p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +
-                                      (int64_t)head * p.o_head_stride;
-                const float inv = l == 0.f ? 0.f : p.v_scale / l;
-                if (!whole && mine)
-                    p.part_ml[part] = make_float2(m == -INFINITY ? m : m * c, l);
+                uint16_t* const out =
+                    p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +
+                    (int64_t)(cur.h * p.group + (row0 + row) - tok * p.group) * p.o_head_stride;
 #pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
+                for (int i = 0; i < D / 64; ++i) {
+                    const int col = wg * (D / 2) + i * 32;
                     uint32_t o[32];
-                    tmem_ld32(tmem + lanes + i * 32, o);
+                    tmem_ld(tmem + lanes + col, o);
                     tmem_wait_ld(o);
-                    if (mine) {
-                        if (whole) {
+                    if (mine && whole) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint4 w;
-                                uint32_t* const ww = &w.x;
+                        for (int e = 0; e < 4; ++e) {
+                            uint4 w;
+                            uint32_t* const ww = &w.x;
 #pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    ww[x] = pack16(false,
-                                                   __uint_as_float(o[e * 8 + 2 * x]) * inv,
-                                                   __uint_as_float(o[e * 8 + 2 * x + 1]) * inv);
-                                *reinterpret_cast<uint4*>(out + i * 32 + e * 8) = w;
-                            }
-                        } else {
-                            float* const dst = p.part_o + part * D + i * 32;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4*>(dst + e * 4) = make_uint4(
-                                    o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+                            for (int x = 0; x < 4; ++x)
+                                ww[x] = pack16(false,
+                                               __uint_as_float(o[e * 8 + 2 * x]) * inv,
+                                               __uint_as_float(o[e * 8 + 2 * x + 1]) * inv);
+                            *reinterpret_cast<uint4*>(out + col + e * 8) = w;
                         }
+                    } else if (mine) {
+                        float* const dst = p.part_o + (part0 + row) * D + col;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4*>(dst + e * 4) = make_uint4(
+                                o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
                     }
                 }
             }
             tc_before_sync();
-            mbar_arrive(&o_free);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.o_free);
             ring_at += 2 * cnt;
-            left -= cnt;
+            left -= cur.lead + cnt;
             ++item;
-            if (tid == 0 && left == 0) {
+            if (tid == 0 && cur.u == 0 && !whole) {  // the last row tile goes on in later CTAs
+                const int64_t x = range.end - cnt + cur.n - 1;  // where its last unit counts
+                const int64_t e = ((x + 1) * range.ctas + range.total - 1) / range.total - 1;
                 Cut cut;
                 memset(&cut, 0, sizeof(cut));
-                if (cur.u == 0 && !whole) {  // the last row tile goes on in later CTAs
-                    const int64_t x = range.end - cnt + cur.n - 1;  // its last unit
-                    const int64_t e =
-                        ((x + 1) * range.ctas + range.total - 1) / range.total - 1;
-                    cut.parts = (int)min(e - blockIdx.x + 1, (int64_t)(range.ctas - blockIdx.x));
-                    cut.token0 = cur.q.token0;
-                    cut.row0 = row0;
-                    cut.rows = rows;
-                    cut.head = cur.h;
-                }
+                cut.parts = (int)min(e - blockIdx.x + 1, (int64_t)(range.ctas - blockIdx.x));
+                cut.token0 = cur.q.token0;
+                cut.row0 = row0;
+                cut.rows = rows;
+                cut.head = cur.h;
                 p.cuts[blockIdx.x] = cut;
             }
-            cur.next(p);
+            cur = *reinterpret_cast<const Cursor<TK>*>(sm.start[item & 1]);
         }
         if (!ok) code = 9;
     }
 
     if (code) {
         *stop_v = 1;
-        if (lane == 0 || code == 9) atomicCAS(p.error, 0, code);
-        if (code == 9 && tid == 0) p.cuts[blockIdx.x].parts = 0;
+        if (lane == 0) atomicCAS(p.error, 0, code);
     }
     tc_before_sync();
     __syncthreads();
@@ -1041,8 +1078,8 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     p.box = box;
     const int64_t cap = a.table_columns * kv.block_size;
     p.capacity = (int)(cap > INT32_MAX - 1024 ? INT32_MAX - 1024 : cap);
-    p.c = a.scale * (f8 ? kv.k_scale * kWidened : 1.f) * 1.4426950408889634f;
-    p.v_scale = f8 ? kv.v_scale * kWidened : 1.f;
+    p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;
+    p.v_scale = f8 ? kv.v_scale : 1.f;
     // a factor that left fp32's normal range would turn a masked score of -infinity into NaN
     if (!(p.c >= 1.1754944e-38f) || isinf(p.c)) return NVFP4_ERR_SHAPE;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
