@@ -80,7 +80,7 @@ struct Cfg {
     static constexpr int kThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kQWarp + kQWarps);
     static constexpr size_t kHead = F8 ? 4096 : 3072;       // Small, in front of the tiles
     static constexpr int kStages =
-        F8 ? (D == 64 ? 4 : 3) : (int)((kSmemMost - kHead - kQBytes) / kTile);
+        F8 ? (D == 64 ? 6 : D == 128 ? 4 : 3) : (int)((kSmemMost - kHead - kQBytes) / kTile);
     static constexpr int kRawStages =
         F8 ? (int)((kSmemMost - kHead - kQBytes - kStages * kTile) / (F8 ? kRaw : 1)) : 1;
     static constexpr size_t kSmem =
@@ -100,6 +100,27 @@ struct Cut {
     int32_t pad[3];
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication with ceil(2^(31 + L) / d), L = ceil(log2 d), whose
+// excess over 2^(31 + L) / d is below 1 and so moves the quotient by less than 2^-L <= 1 / d.  A
+// division is twenty instructions, and the roles of a block share the instruction cache.
+struct Divisor {
+    uint32_t mul, shift;
+};
+__device__ __forceinline__ uint32_t div_by(uint32_t n, Divisor d) {
+    return d.mul ? __umulhi(n, d.mul) >> d.shift : n;
+}
+inline Divisor divisor_of(uint32_t d) {
+    uint32_t log = 0;
+    while ((1ull << log) < d) ++log;
+    Divisor r = {0, 0};  // d = 1
+    if (log > 0) {
+        r.mul = (uint32_t)(((1ull << (31 + log)) + d - 1) / d);
+        r.shift = log - 1;
+    }
+    return r;
+}
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
+
 struct Params {
     const uint16_t* q;
     int64_t ldq, q_head_stride;
@@ -109,6 +130,7 @@ struct Params {
     int64_t ld_table;
     const int32_t *starts, *lens;
     int requests, tokens, kv_heads, group, block, blocks, box;
+    Divisor by_group, by_block;
     int outside;       // a page index past the tensor: its boxes arrive as zeros
     int capacity;      // keys that a table row can hold
     int min_units;     // fewest units worth a CTA of their own
@@ -135,13 +157,25 @@ __device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
     return r;
 }
 
-// Four e4m3 codes -> four f16 values, exact.
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=&r"(lo), "=&r"(hi)
-        : "r"(w));
+// Four e4m3 codes (bytes 0..3) -> f16 values times 2^-8, exact, as the pairs {0, 2} and {1, 3}: a
+// code's exponent and mantissa, seven bits, moved to the same place below f16's exponent bias (15
+// against 7), subnormals included; the factor goes into the scores' and the output's scale.  Seven
+// shifts and masks; cvt has the rate of the exponentials and shares their pipe (measured: a verify
+// batch is 1.5 times as fast this way).  Q and O are put in the pairs' order where they are packed.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd) {
+    even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
+    odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
 }
+// The same by cvt, for words with a NaN code (which the above takes for 480).
+__device__ __forceinline__ void widen_nan(uint32_t w, uint32_t& even, uint32_t& odd) {
+    const uint32_t x = __byte_perm(w, 0, 0x3120);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t"
+        "mul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
+        : "=&r"(even), "=&r"(odd)
+        : "r"(x), "r"(0x1c001c00u));  // 2^-8 twice
+}
+constexpr float kWidened = 256.f;
 
 // ---- the order of the work ---------------------------------------------------------------
 
@@ -159,13 +193,13 @@ __device__ __forceinline__ Request request_of(const Params& p, int r) {
 }
 
 __device__ __forceinline__ int row_tiles(const Params& p, const Request& q) {
-    return (int)(((int64_t)q.n * p.group + kRows - 1) / kRows);
+    return (q.n * p.group + kRows - 1) / kRows;  // (tokens * group is at most 2^30)
 }
 
 // Keys below this are loaded for a row tile: the last row's own position, within the table.
 __device__ __forceinline__ int key_end(const Params& p, const Request& q, int tile) {
-    const int64_t rows = min((int64_t)(tile + 1) * kRows, (int64_t)q.n * p.group);
-    const int last = (int)((rows - 1) / p.group);
+    const int rows = min((tile + 1) * kRows, q.n * p.group);
+    const int last = (int)div_by(rows - 1, p.by_group);
     return min(max(q.len - q.n + last + 1, 0), p.capacity);
 }
 
@@ -185,8 +219,8 @@ struct Cursor {
     int lead;                     // how much of kTileCost counts here: all, unless a cut fell in it
     Request q;
     // Units of this row tile in a range with `left` to go; none: the range is done.
-    __device__ __forceinline__ int take(int64_t left) const {
-        return (int)min((int64_t)(n - u), left - lead);
+    __device__ __forceinline__ int take(int left) const {
+        return min(n - u, left - lead);
     }
     __device__ __forceinline__ void enter(const Params& p) {
         tiles = row_tiles(p, q);
@@ -221,7 +255,7 @@ struct Range {
 };
 
 __device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int c) {
-    return total * c / ctas;
+    return div64(total * c, ctas);
 }
 
 // This CTA's units and the row tile they start in.  Every thread sums the units of a run of
@@ -278,7 +312,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
             Cursor<TK> c;
             c.r = r;
             c.q = q;
-            c.h = (int)(at / s);
+            c.h = (int)div64(at, s);
             at -= c.h * s;
             c.tile = 0;
             while (at >= units_of<TK>(p, q, c.tile) + kTileCost)
@@ -320,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -359,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     tc_after_sync();
     const uint32_t tmem = sm.tmem;
     volatile int* const stop_v = &sm.stop;
-    int64_t left = range.end - range.begin;
+    int left = (int)min(range.end - range.begin, (int64_t)INT32_MAX);
     Cursor<TK> cur = *start;
     bool ok = true;
     int code = 0;
@@ -374,14 +408,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // boxes outside the tensor, which arrive as zeros.  One elected lane issues all of a tile's
         // boxes: a divergent issue, a lane per box, took 95 cycles a box.
         constexpr int N = F8 ? NR : NS, kMost = TK / 16;
-        const int groups = TK / p.box;
+        const int groups = TK / p.box, step = p.box * (F8 ? D : 128);  // bytes of a group (a panel's)
         uint64_t* const fulls = F8 ? sm.raw_full : full;
         uint64_t* const empties = F8 ? sm.raw_empty : empty;
         uint8_t* const tiles = F8 ? raw : ring;
         int slot = 0, it = 0;
         uint32_t phase = 1;  // of `empties`: the first lap finds them free
         while (left > 0 && ok) {
-            const int cnt = cur.take(left);
+            const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
             const int end = key_end(p, cur.q, cur.tile);
             const int32_t* const row = p.table + cur.r * p.ld_table;
@@ -390,15 +424,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 const int key = (cur.u + j) * TK + lane * p.box;  // (j may be past cnt)
                 place = 0;
                 if (j >= cnt || lane >= groups || key >= end) return p.outside;
-                const int col = key / p.block;
+                const int col = (int)div_by(key, p.by_block);
                 place = key - col * p.block;
                 return row[col];
             };
             auto load = [&](const CUtensorMap* map, int page, int place) {
-                if (!mbar_wait(&empties[slot], phase, stop_v)) {
-                    ok = false;
-                    return;
-                }
+                ok = __all_sync(~0u, mbar_wait(&empties[slot], phase, stop_v));
+                if (!ok) return;
                 const int at = (unsigned)page < (unsigned)p.blocks ? page : p.outside;
                 int w[kMost], y[kMost];
 #pragma unroll
@@ -406,20 +438,21 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     w[i] = __shfl_sync(~0u, at, i);
                     y[i] = __shfl_sync(~0u, place, i);
                 }
+                const uint32_t fb = uniform(smem_u32(&fulls[slot]));
+                const uint32_t dst = uniform(smem_u32(tiles + slot * (F8 ? C::kRaw : C::kTile)));
+                const int head = uniform(cur.h);
                 if (elect_one()) {
-                    uint64_t* const fb = &fulls[slot];
-                    uint8_t* const dst = tiles + slot * (F8 ? C::kRaw : C::kTile);
                     mbar_expect_tx(fb, F8 ? C::kRaw : C::kTile);
 #pragma unroll
                     for (int i = 0; i < kMost; ++i) {
                         if (i >= groups) break;
                         if (F8) {
-                            tma_load_4d(dst + i * p.box * D, map, 0, y[i], cur.h, w[i], fb);
+                            tma_load_4d(dst + i * step, map, 0, y[i], head, w[i], fb);
                         } else {
 #pragma unroll
                             for (int pn = 0; pn < C::kPanels; ++pn)
-                                tma_load_4d(dst + pn * (TK * 128) + i * p.box * 128, map, pn * 64,
-                                            y[i], cur.h, w[i], fb);
+                                tma_load_4d(dst + pn * (TK * 128) + i * step, map, pn * 64,
+                                            y[i], head, w[i], fb);
                         }
                     }
                 }
@@ -454,31 +487,29 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     } else if (warp == kMmaWarp) {
         // ---- MMAs: the warp waits together, one elected lane issues and commits
         constexpr uint32_t id_s = idesc_16(!F8, TK, false), id_o = idesc_16(!F8, D, true);
-        const uint64_t q_desc = desc_k_major(smem_u32(q_tile));
-        const uint64_t k_desc = desc_k_major(smem_u32(ring));
-        const uint64_t v_desc = desc_mn_major(smem_u32(ring), TK * 128);
+        const uint32_t q_low = uniform(smem_u32(q_tile) >> 4), ring_low = smem_u32(ring) >> 4;
         int slot = 0, g = 0, item = 0;
         uint32_t phase = 0;  // of the ring
         auto ready = [&](uint64_t* b, uint32_t parity) {
-            if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
+            ok = __all_sync(~0u, mbar_wait(b, parity, stop_v));
             return ok;
         };
         while (left > 0 && ok) {
-            const int cnt = cur.take(left);
+            const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
             if (!ready(&sm.q_full, item & 1)) break;
             // K0 K1 V0 K2 V1 ...: unit j's weights are formed while unit j+1's scores are
             for (int j = -1; j < cnt; ++j) {
                 if (j + 1 < cnt) {  // S = Q K^T of unit j + 1
                     if (!ready(&full[slot], phase)) break;
+                    const int b = (g + 1 + (j < 0 ? -1 : 0)) & 1;
+                    const uint32_t low = uniform(ring_low + slot * (C::kTile >> 4));
+                    const uint32_t d = uniform(tmem + C::kS + b * TK);
                     if (elect_one()) {
-                        const uint64_t kd = k_desc + slot * (C::kTile >> 4);
-                        const int b = (g + 1 + (j < 0 ? -1 : 0)) & 1;
-                        const uint32_t d = tmem + C::kS + b * TK;
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            mma_ss(d, q_desc + (((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
-                                   kd + (((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4), id_s,
+                            mma_ss(d, desc_at(q_low, 16, (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
+                                   desc_at(low, 16, (kk >> 2) * (TK * 128) + (kk & 3) * 32), id_s,
                                    kk > 0);
                         mma_commit(&s_full[b]);
                         mma_commit(&empty[slot]);
@@ -495,12 +526,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
                     if (j == 0 && item > 0 && !ready(&sm.o_free, (item - 1) & 1)) break;
                     tc_after_sync();
+                    const uint32_t low = uniform(ring_low + slot * (C::kTile >> 4));
+                    const uint32_t a = uniform(tmem + C::kP + (g & 1) * (TK / 2));
+                    const uint32_t d = uniform(tmem);
                     if (elect_one()) {
-                        const uint64_t vd = v_desc + slot * (C::kTile >> 4);
-                        const uint32_t a = tmem + C::kP + (g & 1) * (TK / 2);
 #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
-                            mma_ts(tmem, a + kk * 8, vd + kk * (2048 >> 4), id_o, kk > 0 || j > 0);
+                            mma_ts(d, a + kk * 8, desc_at(low, TK * 128, kk * 2048), id_o,
+                                   kk > 0 || j > 0);
                         mma_commit(&empty[slot]);
                         mma_commit(&sm.pv_done);
                         if (j + 1 == cnt) mma_commit(&sm.o_full);
@@ -536,9 +569,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 break;
             }
             const int row0 = cur.tile * kRows;
-            const int rows = (int)min((int64_t)kRows, (int64_t)cur.q.n * p.group - row0);
+            const int rows = min(kRows, cur.q.n * p.group - row0);
             auto src_of = [&](int r) {
-                const int tok = (row0 + r) / p.group, h = (row0 + r) - tok * p.group;
+                const int tok = (int)div_by(row0 + r, p.by_group), h = (row0 + r) - tok * p.group;
                 return p.q + (int64_t)(cur.q.token0 + tok) * p.ldq +
                        (int64_t)(cur.h * p.group + h) * p.q_head_stride;
             };
@@ -585,9 +618,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         const float mul = __uint_as_float((uint32_t)up << 23);
                         uint32_t h[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 4; e += 2) {  // values 0, 2 and 1, 3 of four
                             h[e] = pack16(true, __uint_as_float(w[e] << 16) * mul,
-                                          __uint_as_float(w[e] & 0xffff0000u) * mul);
+                                          __uint_as_float(w[e + 1] << 16) * mul);
+                            h[e + 1] = pack16(true, __uint_as_float(w[e] & 0xffff0000u) * mul,
+                                              __uint_as_float(w[e + 1] & 0xffff0000u) * mul);
+                        }
                         if (r < rows) {
                             if (c == 0)
                                 sm.q_scale[item & 1][r] =
@@ -637,18 +673,47 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 // last tile of all, V(n-1), holds any
                 int valid = TK;
                 if (i + 1 == 2 * cnt) valid = end - (cur.u + cnt - 1) * TK;
-#pragma unroll 2
-                for (int x = 0; x < kPieces; ++x) {
-                    uint4 w = *reinterpret_cast<const uint4*>(src + x * kThr * 16);
-                    if (key + x * kStep >= valid) w = make_uint4(0, 0, 0, 0);
-                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t out[8];
+                constexpr int kBatch = 4;
+#pragma unroll 1
+                for (int x = 0; x < kPieces; x += kBatch) {
+                    uint4 w[kBatch];
+                    uint32_t nan = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) widen(in[j], out[2 * j], out[2 * j + 1]);
-                    const uint4 a = make_uint4(out[0], out[1], out[2], out[3]);
-                    const uint4 b = make_uint4(out[4], out[5], out[6], out[7]);
-                    *reinterpret_cast<uint4*>(dst + first + x * kStep * 128) = swap ? b : a;
-                    *reinterpret_cast<uint4*>(dst + second + x * kStep * 128) = swap ? a : b;
+                    for (int y = 0; y < kBatch; ++y)
+                        w[y] = *reinterpret_cast<const uint4*>(src + (x + y) * kThr * 16);
+#pragma unroll
+                    for (int y = 0; y < kBatch; ++y) {
+                        if (key + (x + y) * kStep >= valid) w[y] = make_uint4(0, 0, 0, 0);
+                        const uint32_t in[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+                        uint32_t out[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            widen(in[j], out[2 * j], out[2 * j + 1]);
+                            nan |= (in[j] & 0x7f7f7f7fu) + 0x01010101u;
+                        }
+                        const uint4 a = make_uint4(out[0], out[1], out[2], out[3]);
+                        const uint4 b = make_uint4(out[4], out[5], out[6], out[7]);
+                        uint8_t* const to = dst + (x + y) * kStep * 128;
+                        *reinterpret_cast<uint4*>(to + first) = swap ? b : a;
+                        *reinterpret_cast<uint4*>(to + second) = swap ? a : b;
+                    }
+                    if (nan & 0x80808080u) {  // a NaN code: rare, and only cvt knows it
+#pragma unroll 1
+                        for (int y = 0; y < kBatch; ++y) {
+                            if (key + (x + y) * kStep >= valid) continue;
+                            uint8_t* const to = dst + (x + y) * kStep * 128;
+                            const uint32_t* const in =
+                                reinterpret_cast<const uint32_t*>(src + (x + y) * kThr * 16);
+#pragma unroll 1
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t even, odd;
+                                widen_nan(in[j], even, odd);
+                                const bool low = j < 2;  // which 16-byte piece
+                                *reinterpret_cast<uint2*>(to + (low != (swap != 0) ? first : second) +
+                                                          (j & 1) * 8) = make_uint2(even, odd);
+                            }
+                        }
+                    }
                 }
                 fence_async_smem();
                 mbar_arrive(&sm.raw_empty[rs]);
@@ -681,17 +746,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 *reinterpret_cast<Cursor<TK>*>(sm.start[(item + 1) & 1]) = after;
             }
             const int row0 = cur.tile * kRows;
-            const int rows = (int)min((int64_t)kRows, (int64_t)cur.q.n * p.group - row0);
+            const int rows = min(kRows, cur.q.n * p.group - row0);
             const bool busy = quarter * 32 < rows;  // this warp has rows
             const bool mine = row < rows;  // lanes past the rows compute on whatever is there
-            const int tok = (row0 + row) / p.group;
+            const int tok = (int)div_by(row0 + row, p.by_group);
             const int end = key_end(p, cur.q, cur.tile);
             // the last key this row sees
             const int last = mine ? min(cur.q.len - cur.q.n + tok, end - 1) : INT32_MAX;
             const int32_t* const table = p.table + cur.r * p.ld_table;
             auto page_at = [&](int j) {  // lane i: the page of 16 keys of the unit
                 const int key = (cur.u + j) * TK + lane * 16;
-                return j >= cnt || lane >= TK / 16 || key >= end ? 0 : table[key / p.block];
+                return j >= cnt || lane >= TK / 16 || key >= end ? 0
+                                                                     : table[div_by(key, p.by_block)];
             };
             int page = page_at(0);  // read a unit ahead
             float m = -INFINITY, l = 0.f, c = p.c;
@@ -824,6 +890,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     uint32_t o[32];
                     tmem_ld(tmem + lanes + col, o);
                     tmem_wait_ld(o);
+                    if (F8) {  // the values' own order
+#pragma unroll
+                        for (int e = 1; e < 32; e += 4) {
+                            const uint32_t x = o[e];
+                            o[e] = o[e + 1];
+                            o[e + 1] = x;
+                        }
+                    }
                     if (mine && whole) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -853,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             ++item;
             if (tid == 0 && cur.u == 0 && !whole) {  // the last row tile goes on in later CTAs
                 const int64_t x = range.end - cnt + cur.n - 1;  // where its last unit counts
-                const int64_t e = ((x + 1) * range.ctas + range.total - 1) / range.total - 1;
+                const int64_t e = div64((x + 1) * range.ctas + range.total - 1, range.total) - 1;
                 Cut cut;
                 memset(&cut, 0, sizeof(cut));
                 cut.parts = (int)min(e - blockIdx.x + 1, (int64_t)(range.ctas - blockIdx.x));
@@ -1073,13 +1147,15 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     p.kv_heads = kv.heads;
     p.group = a.heads / kv.heads;
     p.block = kv.block_size;
+    p.by_group = divisor_of(p.group);
+    p.by_block = divisor_of(p.block);
     p.blocks = (int)kv.blocks;
     p.outside = kv.blocks ? (int)kv.blocks : 1;
     p.box = box;
     const int64_t cap = a.table_columns * kv.block_size;
     p.capacity = (int)(cap > INT32_MAX - 1024 ? INT32_MAX - 1024 : cap);
-    p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;
-    p.v_scale = f8 ? kv.v_scale : 1.f;
+    p.c = a.scale * (f8 ? kv.k_scale * kWidened : 1.f) * 1.4426950408889634f;
+    p.v_scale = f8 ? kv.v_scale * kWidened : 1.f;
     // a factor that left fp32's normal range would turn a masked score of -infinity into NaN
     if (!(p.c >= 1.1754944e-38f) || isinf(p.c)) return NVFP4_ERR_SHAPE;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);

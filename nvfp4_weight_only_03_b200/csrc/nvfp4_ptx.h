@@ -17,9 +17,8 @@ __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count));
 }
 
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)),
-                 "r"(bytes)
+__device__ __forceinline__ void mbar_expect_tx(uint32_t b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes)
                  : "memory");
 }
 
@@ -59,12 +58,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, volatile
     return mbar_try(a, parity) || mbar_wait_long(a, parity, stop, limit);
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                            int w, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
 
@@ -93,18 +92,19 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// Shared-memory matrix descriptors, 128-byte swizzle.  K-major: rows of 128 bytes, 8-row atoms
-// 1024 bytes apart.  MN-major: 64 values of the M/N side per 128-byte row, 8 rows of the K side
-// per atom (the next 8 another 1024 bytes on), the next 64 values `panel` bytes on.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr, uint32_t panel) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((panel >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// A value that is the same in all lanes, as one that the compiler knows to be: it can then live in a
+// uniform register, where tcgen05.mma and TMA take their operands from.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 
+// Shared-memory matrix descriptor, 128-byte swizzle, of the tile at 16 * low plus offset bytes.
+// K-major: rows of 128 bytes, 8-row atoms 1024 bytes apart (panel is 16, unused).  MN-major: 64
+// values of the M/N side per 128-byte row, 8 rows of the K side per atom (the next 8 another 1024
+// bytes on), the next 64 values `panel` bytes on.
+__device__ __forceinline__ uint64_t desc_at(uint32_t low, uint32_t panel, uint32_t offset) {
+    return (uint64_t)(low + (offset >> 4)) | ((uint64_t)((panel >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
 // Instruction descriptor of kind::f16: D fp32, A and B both bf16 or both f16, M = 128.
 __host__ __device__ constexpr uint32_t idesc_16(bool bf16, int n, bool b_mn_major) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u) |

@@ -225,6 +225,26 @@ def test_large_scores_and_rising_maxima():
 
 
 @pytest.mark.parametrize("f8", [False, True])
+def test_nan_of_a_visible_token_reaches_its_rows_and_no_others(f8):
+    # request 1's key 37 and request 2's value 5 are NaN: every row of theirs sees them, and the
+    # value's NaN stays in its dimension
+    b = Batch(16, [90, 70, 60], [1, 1, 1], 12, 2, 128, 16, f8)
+    want = b.call()
+    for r, key, cache, dims in ((1, 37, b.kc, slice(3, 4)), (2, 5, b.vc, slice(77, 79))):
+        page = int(b.table[r, key // 16])
+        if f8:
+            cache.view(torch.uint8)[page, key % 16, :, dims] = 0xFF
+        else:
+            cache[page, key % 16, :, dims] = float("nan")
+    out = b.call()
+    assert torch.equal(out[0], want[0])
+    assert torch.isnan(out[1]).all()
+    assert torch.isnan(out[2, :, 77:79]).all()
+    rest = [d for d in range(128) if d not in (77, 78)]
+    assert torch.equal(out[2][:, rest], want[2][:, rest])
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_many_requests_and_long_context(f8):
     rng = np.random.default_rng(9)
     lens = [int(x) for x in rng.integers(1, 400, 300)]
