@@ -21,8 +21,8 @@
 //   memory; it is rescaled only when a row's maximum rose by more than 2^8 (P is then at most
 //   2^8 and the sums are fp32, so nothing overflows).  S and P have two buffers each, so the MMAs
 //   of one unit run under the softmax of another.
-// * Roles: 4 softmax warps, 1 MMA warp, 1 TMA warp, 2 warps that gather Q, and 4 that widen an
-//   e4m3 cache to f16 (exact); the bf16 cache goes to the MMA as it lies in memory.
+// * Roles: 8 softmax warps, one warp each for the scores' MMAs, the values' MMAs, TMA and Q, and 4
+//   that widen an e4m3 cache to f16 (exact); the bf16 cache goes to the MMA as it lies in memory.
 // * P is rounded to the MMA's 16-bit type (bf16, or f16 with the e4m3 cache): half a step, 2^-9
 //   (2^-12) of each weight.  With the e4m3 cache q is carried as f16 times a power of two per row.
 //   S, O, maxima and sums are fp32.
@@ -49,7 +49,7 @@ using nvfp4_host::misaligned;
 using nvfp4_host::overlaps;
 
 constexpr int kRows = 128;  // rows of a tile: the MMA's M and tensor memory's lanes
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kQWarp = 10, kQWarps = 2;
+constexpr int kSoftmaxWarps = 8, kScoresWarp = 8, kTmaWarp = 9, kValuesWarp = 10, kQWarp = 11;
 constexpr int kWidenWarp = 12, kWidenWarps = 4;
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemMost = 232448;  // shared memory of a block
@@ -57,8 +57,9 @@ constexpr size_t kSmemMost = 232448;  // shared memory of a block
 // The small things in shared memory, ahead of the tiles.
 template <int NS, int NR, bool F8>
 struct Small {
-    uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[NR];
-    uint64_t q_full, q_free, s_full[2], p_full[2], pv_done, o_full, o_free, drained;
+    uint64_t full[NS], empty[NS];  // of the K places, then of the V places
+    uint64_t raw_full[NR], raw_empty[NR];
+    uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], o_full, o_free, drained[2];
     int64_t sums[20];
     int start[2][12];  // a Cursor: where the range begins; then, by turns, the softmax's next tile
     uint32_t tmem;
@@ -67,7 +68,8 @@ struct Small {
         float max[2][2][kRows];  // of a unit: [its parity][warpgroup][lane]
         float2 ml[2][kRows];     // of a row tile, maximum and sum: [warpgroup][lane]
     } row;
-    float q_scale[F8 ? 2 : 1][F8 ? kRows : 1];
+    // biased exponents of the f16 Q rows' scales.  Q may be two row tiles ahead of the softmax.
+    uint8_t q_scale[F8 ? 4 : 1][F8 ? kRows : 1];
 };
 
 template <int D, bool F8>
@@ -77,7 +79,7 @@ struct Cfg {
     static constexpr int kQBytes = kRows * D * 2;
     static constexpr int kTile = TK * D * 2;                // one K or V tile, 16-bit
     static constexpr int kRaw = F8 ? TK * D : 0;            // the same in e4m3
-    static constexpr int kThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kQWarp + kQWarps);
+    static constexpr int kThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kQWarp + 1);
     static constexpr size_t kHead = F8 ? 4096 : 3072;       // Small, in front of the tiles
     static constexpr int kStages =
         F8 ? (D == 64 ? 6 : D == 128 ? 4 : 3) : (int)((kSmemMost - kHead - kQBytes) / kTile);
@@ -85,10 +87,14 @@ struct Cfg {
         F8 ? (int)((kSmemMost - kHead - kQBytes - kStages * kTile) / (F8 ? kRaw : 1)) : 1;
     static constexpr size_t kSmem =
         kHead + kQBytes + (size_t)kStages * kTile + (F8 ? (size_t)kRawStages * kRaw : 0);
+    // Places of K and of V: rings of their own, since their readers go on independently (with one
+    // ring, a reader could take the phase of the other's tile for that of its own).
+    static constexpr int kKeyStages = kStages / 2, kValueStages = kStages - kKeyStages;
     using Shared = Small<kStages, kRawStages, F8>;
     // tensor memory columns: O, then two S, then two P (two 16-bit values per column)
     static constexpr int kS = D, kP = D + 2 * TK, kEnd = D + 2 * TK + TK;
     static_assert(kEnd <= kTmemCols, "tensor memory");
+    static_assert(kKeyStages >= 1 && kValueStages >= 2, "rings");
     static_assert(kSmem <= kSmemMost && sizeof(Shared) <= kHead, "shared memory");
 };
 
@@ -249,6 +255,20 @@ struct Cursor {
 __device__ __forceinline__ bool is_value(int i, int cnt) {
     return i + 1 == 2 * cnt || (i > 0 && (i & 1) == 0);
 }
+// A reader's or writer's place in a ring of N tiles, and the phase of its barriers.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase;
+    __device__ explicit Ring(uint32_t first) : phase(first) {}
+    __device__ __forceinline__ void step() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 struct Range {
     int64_t begin, end, total;
     int ctas;
@@ -339,6 +359,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                       const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<D, F8>;
     constexpr int TK = C::TK, NS = C::kStages, NR = C::kRawStages;
+    constexpr int NK = C::kKeyStages, NV = C::kValueStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     typename C::Shared& sm = *reinterpret_cast<typename C::Shared*>(smem_raw);
     uint8_t* const q_tile = smem_raw + C::kHead;
@@ -356,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == kMmaWarp) {
+    if (warp == kScoresWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sm.tmem)),
                      "r"(kTmemCols));
@@ -371,15 +392,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_init(&sm.raw_full[i], 1);
             mbar_init(&sm.raw_empty[i], kWidenWarps * 32);
         }
-        mbar_init(&sm.q_full, kQWarps * 32);
+        mbar_init(&sm.q_full, 32);
         mbar_init(&sm.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], kSoftmaxWarps);
+            mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.drained[i], 1);
         }
-        mbar_init(&sm.pv_done, 1);
         mbar_init(&sm.o_full, 1);
-        mbar_init(&sm.drained, 1);
         mbar_init(&sm.o_free, kSoftmaxWarps);
         sm.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -407,13 +428,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // and a group is a box per 64 values.  Keys past the end, and pages that do not exist, are
         // boxes outside the tensor, which arrive as zeros.  One elected lane issues all of a tile's
         // boxes: a divergent issue, a lane per box, took 95 cycles a box.
-        constexpr int N = F8 ? NR : NS, kMost = TK / 16;
+        constexpr int kMost = TK / 16;
         const int groups = TK / p.box, step = p.box * (F8 ? D : 128);  // bytes of a group (a panel's)
-        uint64_t* const fulls = F8 ? sm.raw_full : full;
-        uint64_t* const empties = F8 ? sm.raw_empty : empty;
-        uint8_t* const tiles = F8 ? raw : ring;
-        int slot = 0, it = 0;
-        uint32_t phase = 1;  // of `empties`: the first lap finds them free
+        Ring<NK> keys(1);  // (the first lap finds every place free)
+        Ring<NV> values(1);
+        Ring<NR> raws(1);
+        int it = 0, values_at = 0;
         while (left > 0 && ok) {
             const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
@@ -428,9 +448,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 place = key - col * p.block;
                 return row[col];
             };
-            auto load = [&](const CUtensorMap* map, int page, int place) {
-                ok = __all_sync(~0u, mbar_wait(&empties[slot], phase, stop_v));
+            auto load = [&](bool v, int page, int place) {
+                const int slot = F8 ? raws.slot : v ? NK + values.slot : keys.slot;
+                const uint32_t phase = F8 ? raws.phase : v ? values.phase : keys.phase;
+                uint64_t* const fulls = F8 ? sm.raw_full : full;
+                ok = __all_sync(
+                    ~0u, mbar_wait((F8 ? sm.raw_empty : empty) + slot, phase, stop_v));
                 if (!ok) return;
+                const CUtensorMap* const map = v ? &map_v : &map_k;
                 const int at = (unsigned)page < (unsigned)p.blocks ? page : p.outside;
                 int w[kMost], y[kMost];
 #pragma unroll
@@ -439,7 +464,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     y[i] = __shfl_sync(~0u, place, i);
                 }
                 const uint32_t fb = uniform(smem_u32(&fulls[slot]));
-                const uint32_t dst = uniform(smem_u32(tiles + slot * (F8 ? C::kRaw : C::kTile)));
+                const uint32_t dst = uniform(
+                    smem_u32(F8 ? raw + slot * C::kRaw : ring + slot * C::kTile));
                 const int head = uniform(cur.h);
                 if (elect_one()) {
                     mbar_expect_tx(fb, F8 ? C::kRaw : C::kTile);
@@ -457,18 +483,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     }
                 }
                 __syncwarp();
+                if (F8) raws.step();
+                else if (v) values.step();
+                else keys.step();
                 ++it;
-                if (++slot == N) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                values_at += v;
             };
             // pages are read ahead of their unit's first box
             int place0, place1, place2;
             int page0 = page_at(0, place0), page1 = page_at(1, place1), page2 = page_at(2, place2);
             for (int i = 0; i < 2 * cnt && ok; ++i) {
                 const bool v = is_value(i, cnt), head = v || i == 0;
-                load(v ? &map_v : &map_k, head ? page0 : page1, head ? place0 : place1);
+                load(v, head ? page0 : page1, head ? place0 : place1);
                 if (v) {
                     page0 = page1, place0 = place1;
                     page1 = page2, place1 = place2;
@@ -481,15 +507,27 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (!ok) code = 5;
         if (!ok) {  // a CTA that gives up leaves no copy in flight behind it
             volatile int none = 0;
-            for (int k = max(0, it - N); k < it; ++k)
-                mbar_wait(&fulls[k % N], (k / N) & 1, &none, 20000000ll);
+            auto drain = [&](uint64_t* b, int n, int count) {  // the last n of `count` copies
+                for (int k = max(0, count - n); k < count; ++k)
+                    mbar_wait(b + k % n, (k / n) & 1, &none, 20000000ll);
+            };
+            if (F8) {
+                drain(sm.raw_full, NR, it);
+            } else {
+                drain(full, NK, it - values_at);
+                drain(full + NK, NV, values_at);
+            }
         }
-    } else if (warp == kMmaWarp) {
-        // ---- MMAs: the warp waits together, one elected lane issues and commits
+    } else if (warp == kScoresWarp || warp == kValuesWarp) {
+        // ---- MMAs, one elected lane: a warp for S = Q K^T and one for O += P V, so that the next
+        // product waits in the tensor core's queue while a warp looks after its barriers.
+        // Unit g's scores need the weights of g - 2 formed (whose scores had their place).
+        const bool values = warp == kValuesWarp;
         constexpr uint32_t id_s = idesc_16(!F8, TK, false), id_o = idesc_16(!F8, D, true);
         const uint32_t q_low = uniform(smem_u32(q_tile) >> 4), ring_low = smem_u32(ring) >> 4;
-        int slot = 0, g = 0, item = 0;
-        uint32_t phase = 0;  // of the ring
+        int g = 0, item = 0;
+        Ring<NK> keys(0);
+        Ring<NV> vals(0);
         auto ready = [&](uint64_t* b, uint32_t parity) {
             ok = __all_sync(~0u, mbar_wait(b, parity, stop_v));
             return ok;
@@ -497,53 +535,49 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         while (left > 0 && ok) {
             const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
-            if (!ready(&sm.q_full, item & 1)) break;
-            // K0 K1 V0 K2 V1 ...: unit j's weights are formed while unit j+1's scores are
-            for (int j = -1; j < cnt; ++j) {
-                if (j + 1 < cnt) {  // S = Q K^T of unit j + 1
-                    if (!ready(&full[slot], phase)) break;
-                    const int b = (g + 1 + (j < 0 ? -1 : 0)) & 1;
+            if (!values) {
+                if (!ready(&sm.q_full, item & 1)) break;
+                for (int j = 0; j < cnt; ++j, ++g) {
+                    const int slot = keys.slot;
+                    if (!ready(&full[slot], keys.phase)) break;
+                    if (g >= 2 && !ready(&p_full[g & 1], ((g >> 1) - 1) & 1)) break;
                     const uint32_t low = uniform(ring_low + slot * (C::kTile >> 4));
-                    const uint32_t d = uniform(tmem + C::kS + b * TK);
+                    const uint32_t d = uniform(tmem + C::kS + (g & 1) * TK);
+                    tc_after_sync();
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             mma_ss(d, desc_at(q_low, 16, (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
                                    desc_at(low, 16, (kk >> 2) * (TK * 128) + (kk & 3) * 32), id_s,
                                    kk > 0);
-                        mma_commit(&s_full[b]);
+                        mma_commit(&s_full[g & 1]);
                         mma_commit(&empty[slot]);
-                        if (j + 2 == cnt) mma_commit(&sm.q_free);
+                        if (j + 1 == cnt) mma_commit(&sm.q_free);
                     }
                     __syncwarp();
-                    if (++slot == NS) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
+                    keys.step();
                 }
-                if (j >= 0) {  // O += P V of unit j
-                    if (!ready(&full[slot], phase)) break;
+            } else {
+                for (int j = 0; j < cnt; ++j, ++g) {
+                    const int slot = NK + vals.slot;
+                    if (!ready(&full[slot], vals.phase)) break;
                     if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
                     if (j == 0 && item > 0 && !ready(&sm.o_free, (item - 1) & 1)) break;
-                    tc_after_sync();
                     const uint32_t low = uniform(ring_low + slot * (C::kTile >> 4));
                     const uint32_t a = uniform(tmem + C::kP + (g & 1) * (TK / 2));
                     const uint32_t d = uniform(tmem);
+                    tc_after_sync();
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
                             mma_ts(d, a + kk * 8, desc_at(low, TK * 128, kk * 2048), id_o,
                                    kk > 0 || j > 0);
                         mma_commit(&empty[slot]);
-                        mma_commit(&sm.pv_done);
+                        mma_commit(&sm.pv_done[g & 1]);
                         if (j + 1 == cnt) mma_commit(&sm.o_full);
                     }
                     __syncwarp();
-                    ++g;
-                    if (++slot == NS) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
+                    vals.step();
                 }
             }
             ++item;
@@ -554,12 +588,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (!ok) {  // let the MMAs that were issued end before tensor memory is freed
             code = 6;
             volatile int none = 0;
-            if (elect_one()) mma_commit(&sm.drained);
-            mbar_wait(&sm.drained, 0, &none, 20000000ll);
+            if (elect_one()) mma_commit(&sm.drained[values]);
+            mbar_wait(&sm.drained[values], 0, &none, 20000000ll);
         }
-    } else if (warp >= kQWarp && warp < kQWarp + kQWarps) {
+    } else if (warp == kQWarp) {
         // ---- Q rows into the MMA's layout (K-major, 128-byte swizzle)
-        const int t = tid - kQWarp * 32;
         int item = 0;
         while (left > 0) {
             const int cnt = cur.take(left);
@@ -576,14 +609,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                        (int64_t)(cur.h * p.group + h) * p.q_head_stride;
             };
             if (!F8) {
-                for (int i = t; i < rows * (D / 8); i += kQWarps * 32) {
-                    const int r = i / (D / 8), c = i % (D / 8);
-                    const uint32_t dst = smem_u32(q_tile) + (c >> 3) * (kRows * 128) + r * 128 +
-                                         (((c & 7) ^ (r & 7)) << 4);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes per row, rows at once
+                const int c = lane % kLanes;
+                const uint32_t dst0 = smem_u32(q_tile) + (c >> 3) * (kRows * 128);
+#pragma unroll 4
+                for (int r = lane / kLanes; r < rows; r += kAtOnce)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
                                  "l"(src_of(r) + c * 8)
                                  : "memory");
-                }
                 asm volatile("cp.async.wait_all;" ::: "memory");
             } else {
                 // x 2^e with the row's largest magnitude in [2^14, 2^15), as f16.  D / 8 lanes take a
@@ -591,19 +625,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 // them, since a row alone is a memory latency.
                 constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
                 const int sub = lane / kLanes, c = lane % kLanes;
-                for (int r0 = (warp - kQWarp) * kAtOnce; r0 < rows;
-                     r0 += kQWarps * kAtOnce * kBatch) {
+                for (int r0 = 0; r0 < rows; r0 += kAtOnce * kBatch) {
                     uint4 v[kBatch];
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i * kQWarps * kAtOnce + sub;
+                        const int r = r0 + i * kAtOnce + sub;
                         v[i] = make_uint4(0, 0, 0, 0);
                         if (r < rows)
                             v[i] = *reinterpret_cast<const uint4*>(src_of(r) + c * 8);
                     }
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i * kQWarps * kAtOnce + sub;
+                        const int r = r0 + i * kAtOnce + sub;
                         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                         uint32_t big = 0;  // largest magnitude's bits; NaN and infinity lead
 #pragma unroll
@@ -626,8 +659,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         }
                         if (r < rows) {
                             if (c == 0)
-                                sm.q_scale[item & 1][r] =
-                                    __uint_as_float((uint32_t)(254 - up) << 23);
+                                sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
                             *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kRows * 128) + r * 128 +
                                                       (((c & 7) ^ (r & 7)) << 4)) =
                                 make_uint4(h[0], h[1], h[2], h[3]);
@@ -655,15 +687,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         const int first = (c >> 2) * (TK * 128) + key * 128 + (((u0 + swap) ^ (key & 7)) << 4);
         const int second =
             (c >> 2) * (TK * 128) + key * 128 + (((u0 + 1 - swap) ^ (key & 7)) << 4);
-        int rs = 0, ts = 0;
-        uint32_t rphase = 0, tphase = 1;
+        Ring<NR> raws(0);
+        Ring<NK> keys(1);
+        Ring<NV> values(1);
         while (left > 0 && ok) {
             const int cnt = cur.take(left);
             if (cnt <= 0) break;
             const int end = key_end(p, cur.q, cur.tile);
             for (int i = 0; i < 2 * cnt; ++i) {
-                if (!mbar_wait(&sm.raw_full[rs], rphase, stop_v) ||
-                    !mbar_wait(&empty[ts], tphase, stop_v)) {
+                const bool v = is_value(i, cnt);
+                const int rs = raws.slot, ts = v ? NK + values.slot : keys.slot;
+                if (!mbar_wait(&sm.raw_full[rs], raws.phase, stop_v) ||
+                    !mbar_wait(&empty[ts], v ? values.phase : keys.phase, stop_v)) {
                     ok = false;
                     break;
                 }
@@ -718,8 +753,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 fence_async_smem();
                 mbar_arrive(&sm.raw_empty[rs]);
                 mbar_arrive(&full[ts]);
-                if (++rs == NR) rs = 0, rphase ^= 1;
-                if (++ts == NS) ts = 0, tphase ^= 1;
+                raws.step();
+                if (v) values.step();
+                else keys.step();
             }
             left -= cur.lead + cnt;
             cur.next(p);
@@ -733,7 +769,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // on whatever is there) to the end of the range.
         const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        int g = 0, item = 0, ring_at = 0;
+        int g = 0, item = 0, values_at = 0;
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
         };
@@ -798,9 +834,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         const float f = rise ? exp2_approx((m - top) * c) : 1.f;
                         if (rise) m = top;
                         l *= f;
-                        // these scores came after PV of unit g - 2, and that of unit g waits for
-                        // this warp: the phase is g - 1 or its completion, no other
-                        wait(&sm.pv_done, (g - 1) & 1);
+                        wait(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
                         __syncwarp();
                         tc_after_sync();
 #pragma unroll 1
@@ -840,13 +874,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             for (int j = 0; j < cnt; ++j, ++g) {
                 const int page_next = page_at(j + 1);
                 wait(&s_full[g & 1], (g >> 1) & 1);
+                // P's place is free once unit g - 2 is through (and V's of that unit, so that the
+                // phase of a V place below is not taken for an earlier one's: NV >= 2)
+                if (g >= 2) wait(&sm.pv_done[g & 1], ((g >> 1) - 1) & 1);
                 tc_after_sync();
                 const int unit0 = (cur.u + j) * TK;
                 if (!F8 && unit0 + TK > end) {
                     // values past the end are whatever the page held: zeros, so that their weights
                     // of zero add nothing
-                    const int vi = ring_at + 2 * cnt - 1, slot = vi % NS;
-                    wait(&full[slot], (vi / NS) & 1);
+                    const int vi = values_at + cnt - 1, slot = NK + vi % NV;
+                    wait(&full[slot], (vi / NV) & 1);
                     const int from = max(end - unit0, 0);
                     uint8_t* const v = ring + slot * C::kTile;
                     for (int i = tid; i < (TK - from) * (D / 8); i += kSoftmaxWarps * 32) {
@@ -858,7 +895,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 }
                 __syncwarp();
                 // the scores are there, so the rows' scales are (q_full itself may be a phase on)
-                if (F8 && j == 0 && mine) c *= sm.q_scale[item & 1][row];
+                if (F8 && j == 0 && mine)
+                    c *= __uint_as_float((uint32_t)sm.q_scale[item & 3][row] << 23);
                 if (busy) weigh(j);
                 tc_before_sync();
                 __syncwarp();
@@ -922,7 +960,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             tc_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
-            ring_at += 2 * cnt;
+            values_at += cnt;
             left -= cur.lead + cnt;
             ++item;
             if (tid == 0 && cur.u == 0 && !whole) {  // the last row tile goes on in later CTAs
@@ -948,7 +986,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
     tc_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kScoresWarp) {
         tc_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols));
