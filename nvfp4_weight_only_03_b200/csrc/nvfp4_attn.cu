@@ -182,6 +182,13 @@ __device__ __forceinline__ void widen_nan(uint32_t w, uint32_t& even, uint32_t& 
         : "r"(x), "r"(0x1c001c00u));  // 2^-8 twice
 }
 constexpr float kWidened = 256.f;
+constexpr uint32_t kWidenedNan = 0x3f80;  // what widen makes of a NaN code, 480 / 256: above all others
+// The larger magnitude of each half (its sign is of no use).
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
 // ---- the order of the work ---------------------------------------------------------------
 
@@ -385,14 +392,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], F8 ? kWidenWarps * 32 : 1);
+            mbar_init(&full[i], F8 ? kWidenWarps : 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < NR; ++i) {
             mbar_init(&sm.raw_full[i], 1);
-            mbar_init(&sm.raw_empty[i], kWidenWarps * 32);
+            mbar_init(&sm.raw_empty[i], kWidenWarps);
         }
-        mbar_init(&sm.q_full, 32);
+        mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -422,22 +429,104 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     if (tid == 0) p.cuts[blockIdx.x].parts = 0;
     if (left == 0) {
         // nothing to do
-    } else if (warp == kTmaWarp) {
-        // ---- K and V tiles, in the order of the MMAs: K0 K1 V0 K2 V1 ... V(n-1).  A tile is
-        // TK / box groups of `box` keys of one page each (lane i knows group i's page and place),
-        // and a group is a box per 64 values.  Keys past the end, and pages that do not exist, are
-        // boxes outside the tensor, which arrive as zeros.  One elected lane issues all of a tile's
-        // boxes: a divergent issue, a lane per box, took 95 cycles a box.
+    } else if (warp == kTmaWarp || warp == kQWarp) {
+        // ---- what the products read.  bf16: one warp copies the K tiles, another gathers Q's rows
+        // and copies the V tiles (one warp alone was the kernel's bound with pages of 16 keys).  e4m3:
+        // one warp copies K and V tiles to where they are widened, in the order K0 K1 V0 K2 V1 ...
+        // V(n-1), and another gathers Q.  A tile is TK / box groups of `box` keys of one page each
+        // (lane i knows group i's page and place), and a group is a box per 64 values.  Keys past the
+        // end, and pages that do not exist, are boxes outside the tensor, which arrive as zeros.  One
+        // elected lane issues all of a tile's boxes: a divergent issue, a lane per box, took 95
+        // cycles a box.
         constexpr int kMost = TK / 16;
+        const bool second = warp == kQWarp;
         const int groups = TK / p.box, step = p.box * (F8 ? D : 128);  // bytes of a group (a panel's)
-        Ring<NK> keys(1);  // (the first lap finds every place free)
-        Ring<NV> values(1);
-        Ring<NR> raws(1);
-        int it = 0, values_at = 0;
+        const int places = F8 ? NR : second ? NV : NK, place0_at = !F8 && second ? NK : 0;
+        uint64_t* const fulls = F8 ? sm.raw_full : full + place0_at;
+        uint64_t* const empties = F8 ? sm.raw_empty : empty + place0_at;
+        const uint32_t room = smem_u32(F8 ? raw : ring + place0_at * C::kTile);
+        int slot = 0, it = 0, item = 0;
+        uint32_t phase = 1;  // (the first lap finds every place free)
+        // Q's rows in the MMA's layout (K-major, 128-byte swizzle)
+        auto gather = [&]() {
+            if (item > 0 &&
+                !(ok = __all_sync(~0u, mbar_wait(&sm.q_free, (item - 1) & 1, stop_v))))
+                return;
+            const int row0 = cur.tile * kRows;
+            const int rows = min(kRows, cur.q.n * p.group - row0);
+            auto src_of = [&](int r) {
+                const int tok = (int)div_by(row0 + r, p.by_group), h = (row0 + r) - tok * p.group;
+                return p.q + (int64_t)(cur.q.token0 + tok) * p.ldq +
+                       (int64_t)(cur.h * p.group + h) * p.q_head_stride;
+            };
+            if (!F8) {
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes per row, rows at once
+                const int c = lane % kLanes;
+                const uint32_t dst0 = smem_u32(q_tile) + (c >> 3) * (kRows * 128);
+#pragma unroll 4
+                for (int r = lane / kLanes; r < rows; r += kAtOnce)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                                 "l"(src_of(r) + c * 8)
+                                 : "memory");
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            } else {
+                // x 2^e with the row's largest magnitude in [2^14, 2^15), as f16.  D / 8 lanes take a
+                // row, 16 bytes each; a warp reads kBatch such groups of rows before it works on
+                // them, since a row alone is a memory latency.
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
+                const int sub = lane / kLanes, c = lane % kLanes;
+                for (int r0 = 0; r0 < rows; r0 += kAtOnce * kBatch) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = r0 + i * kAtOnce + sub;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (r < rows)
+                            v[i] = *reinterpret_cast<const uint4*>(src_of(r) + c * 8);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = r0 + i * kAtOnce + sub;
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t big = 0;  // largest magnitude's bits; NaN and infinity lead
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            big = max(big, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+                        for (int d = kLanes / 2; d; d >>= 1)
+                            big = max(big, __shfl_xor_sync(~0u, big, d));
+                        // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value
+                        // is below 2^-50 has scores of zero to fp32 either way
+                        const int up = min(127 + 14 + 127 - (int)(big >> 7), 127 + 64);
+                        const float mul = __uint_as_float((uint32_t)up << 23);
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {  // values 0, 2 and 1, 3 of four
+                            h[e] = pack16(true, __uint_as_float(w[e] << 16) * mul,
+                                          __uint_as_float(w[e + 1] << 16) * mul);
+                            h[e + 1] = pack16(true, __uint_as_float(w[e] & 0xffff0000u) * mul,
+                                              __uint_as_float(w[e + 1] & 0xffff0000u) * mul);
+                        }
+                        if (r < rows) {
+                            if (c == 0)
+                                sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
+                            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kRows * 128) + r * 128 +
+                                                      (((c & 7) ^ (r & 7)) << 4)) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full);
+        };
         while (left > 0 && ok) {
             const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
-            const int end = key_end(p, cur.q, cur.tile);
+            if (second) gather();
+            const int end = key_end(p, cur.q, cur.tile), head = uniform(cur.h);
             const int32_t* const row = p.table + cur.r * p.ld_table;
             // this lane's page and place in unit j of the range
             auto page_at = [&](int j, int& place) {
@@ -448,75 +537,61 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 place = key - col * p.block;
                 return row[col];
             };
-            auto load = [&](bool v, int page, int place) {
-                const int slot = F8 ? raws.slot : v ? NK + values.slot : keys.slot;
-                const uint32_t phase = F8 ? raws.phase : v ? values.phase : keys.phase;
-                uint64_t* const fulls = F8 ? sm.raw_full : full;
-                ok = __all_sync(
-                    ~0u, mbar_wait((F8 ? sm.raw_empty : empty) + slot, phase, stop_v));
-                if (!ok) return;
-                const CUtensorMap* const map = v ? &map_v : &map_k;
+            // pages are read ahead of their unit's first box
+            int place0, place1, place2;
+            int page0 = page_at(0, place0), page1 = page_at(1, place1), page2 = page_at(2, place2);
+            const int tiles = F8 ? (second ? 0 : 2 * cnt) : cnt;
+            for (int i = 0; i < tiles && ok; ++i) {
+                const bool v = F8 ? is_value(i, cnt) : second, first = !F8 || v || i == 0;
+                const int page = first ? page0 : page1, place = first ? place0 : place1;
                 const int at = (unsigned)page < (unsigned)p.blocks ? page : p.outside;
                 int w[kMost], y[kMost];
 #pragma unroll
-                for (int i = 0; i < kMost; ++i) {
-                    w[i] = __shfl_sync(~0u, at, i);
-                    y[i] = __shfl_sync(~0u, place, i);
+                for (int x = 0; x < kMost; ++x) {
+                    w[x] = __shfl_sync(~0u, at, x);
+                    y[x] = __shfl_sync(~0u, place, x);
                 }
-                const uint32_t fb = uniform(smem_u32(&fulls[slot]));
-                const uint32_t dst = uniform(
-                    smem_u32(F8 ? raw + slot * C::kRaw : ring + slot * C::kTile));
-                const int head = uniform(cur.h);
+                const CUtensorMap* const map = v ? &map_v : &map_k;
+                const uint32_t fb = uniform(smem_u32(fulls + slot));
+                const uint32_t dst = uniform(room + slot * (F8 ? C::kRaw : C::kTile));
+                ok = __all_sync(~0u, mbar_wait(empties + slot, phase, stop_v));
+                if (!ok) break;
                 if (elect_one()) {
                     mbar_expect_tx(fb, F8 ? C::kRaw : C::kTile);
 #pragma unroll
-                    for (int i = 0; i < kMost; ++i) {
-                        if (i >= groups) break;
+                    for (int x = 0; x < kMost; ++x) {
+                        if (x >= groups) break;
                         if (F8) {
-                            tma_load_4d(dst + i * step, map, 0, y[i], head, w[i], fb);
+                            tma_load_4d(dst + x * step, map, 0, y[x], head, w[x], fb);
                         } else {
 #pragma unroll
                             for (int pn = 0; pn < C::kPanels; ++pn)
-                                tma_load_4d(dst + pn * (TK * 128) + i * step, map, pn * 64,
-                                            y[i], head, w[i], fb);
+                                tma_load_4d(dst + pn * (TK * 128) + x * step, map, pn * 64, y[x],
+                                            head, w[x], fb);
                         }
                     }
                 }
                 __syncwarp();
-                if (F8) raws.step();
-                else if (v) values.step();
-                else keys.step();
                 ++it;
-                values_at += v;
-            };
-            // pages are read ahead of their unit's first box
-            int place0, place1, place2;
-            int page0 = page_at(0, place0), page1 = page_at(1, place1), page2 = page_at(2, place2);
-            for (int i = 0; i < 2 * cnt && ok; ++i) {
-                const bool v = is_value(i, cnt), head = v || i == 0;
-                load(v, head ? page0 : page1, head ? place0 : place1);
-                if (v) {
+                if (++slot == places) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                if (!F8 || v) {
                     page0 = page1, place0 = place1;
                     page1 = page2, place1 = place2;
-                    page2 = page_at(i / 2 + 2, place2);
+                    page2 = page_at((F8 ? i / 2 - 1 : i) + 3, place2);
                 }
             }
+            ++item;
             left -= cur.lead + cnt;
             cur.next(p);
         }
-        if (!ok) code = 5;
         if (!ok) {  // a CTA that gives up leaves no copy in flight behind it
+            code = second ? 7 : 5;
             volatile int none = 0;
-            auto drain = [&](uint64_t* b, int n, int count) {  // the last n of `count` copies
-                for (int k = max(0, count - n); k < count; ++k)
-                    mbar_wait(b + k % n, (k / n) & 1, &none, 20000000ll);
-            };
-            if (F8) {
-                drain(sm.raw_full, NR, it);
-            } else {
-                drain(full, NK, it - values_at);
-                drain(full + NK, NV, values_at);
-            }
+            for (int k = max(0, it - places); k < it; ++k)
+                mbar_wait(fulls + k % places, (k / places) & 1, &none, 20000000ll);
         }
     } else if (warp == kScoresWarp || warp == kValuesWarp) {
         // ---- MMAs, one elected lane: a warp for S = Q K^T and one for O += P V, so that the next
@@ -591,102 +666,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             if (elect_one()) mma_commit(&sm.drained[values]);
             mbar_wait(&sm.drained[values], 0, &none, 20000000ll);
         }
-    } else if (warp == kQWarp) {
-        // ---- Q rows into the MMA's layout (K-major, 128-byte swizzle)
-        int item = 0;
-        while (left > 0) {
-            const int cnt = cur.take(left);
-            if (cnt <= 0) break;
-            if (item > 0 && !mbar_wait(&sm.q_free, (item - 1) & 1, stop_v)) {
-                ok = false;
-                break;
-            }
-            const int row0 = cur.tile * kRows;
-            const int rows = min(kRows, cur.q.n * p.group - row0);
-            auto src_of = [&](int r) {
-                const int tok = (int)div_by(row0 + r, p.by_group), h = (row0 + r) - tok * p.group;
-                return p.q + (int64_t)(cur.q.token0 + tok) * p.ldq +
-                       (int64_t)(cur.h * p.group + h) * p.q_head_stride;
-            };
-            if (!F8) {
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes per row, rows at once
-                const int c = lane % kLanes;
-                const uint32_t dst0 = smem_u32(q_tile) + (c >> 3) * (kRows * 128);
-#pragma unroll 4
-                for (int r = lane / kLanes; r < rows; r += kAtOnce)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                                 "l"(src_of(r) + c * 8)
-                                 : "memory");
-                asm volatile("cp.async.wait_all;" ::: "memory");
-            } else {
-                // x 2^e with the row's largest magnitude in [2^14, 2^15), as f16.  D / 8 lanes take a
-                // row, 16 bytes each; a warp reads kBatch such groups of rows before it works on
-                // them, since a row alone is a memory latency.
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
-                const int sub = lane / kLanes, c = lane % kLanes;
-                for (int r0 = 0; r0 < rows; r0 += kAtOnce * kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i * kAtOnce + sub;
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (r < rows)
-                            v[i] = *reinterpret_cast<const uint4*>(src_of(r) + c * 8);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i * kAtOnce + sub;
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t big = 0;  // largest magnitude's bits; NaN and infinity lead
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            big = max(big, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-                        for (int d = kLanes / 2; d; d >>= 1)
-                            big = max(big, __shfl_xor_sync(~0u, big, d));
-                        // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value
-                        // is below 2^-50 has scores of zero to fp32 either way
-                        const int up = min(127 + 14 + 127 - (int)(big >> 7), 127 + 64);
-                        const float mul = __uint_as_float((uint32_t)up << 23);
-                        uint32_t h[4];
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {  // values 0, 2 and 1, 3 of four
-                            h[e] = pack16(true, __uint_as_float(w[e] << 16) * mul,
-                                          __uint_as_float(w[e + 1] << 16) * mul);
-                            h[e + 1] = pack16(true, __uint_as_float(w[e] & 0xffff0000u) * mul,
-                                              __uint_as_float(w[e + 1] & 0xffff0000u) * mul);
-                        }
-                        if (r < rows) {
-                            if (c == 0)
-                                sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
-                            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kRows * 128) + r * 128 +
-                                                      (((c & 7) ^ (r & 7)) << 4)) =
-                                make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                    }
-                }
-            }
-            fence_async_smem();
-            mbar_arrive(&sm.q_full);
-            ++item;
-            left -= cur.lead + cnt;
-            cur.next(p);
-        }
-        if (!ok) code = 7;
     } else if (F8 && warp >= kWidenWarp) {
-        // ---- e4m3 tiles to f16 in the MMA's layout.  A lane takes 16 codes of a key: two 16-byte
-        // pieces of its row; lanes 4..7 of 8 store theirs in the other order, so that 8 lanes
-        // always cover a panel's 128 bytes.  All of a thread's pieces have the same place in
-        // their rows.
-        const int t = tid - kWidenWarp * 32;
-        constexpr int kPer = D / 16, kThr = kWidenWarps * 32, kPieces = TK * kPer / kThr;
-        constexpr int kStep = kThr / kPer;  // keys from one piece of a thread to the next
-        static_assert(kStep % 8 == 0, "the swizzle of a thread's pieces is one");
-        const int key = t / kPer, c = t % kPer, u0 = (c & 3) * 2, swap = (lane >> 2) & 1;
-        const int first = (c >> 2) * (TK * 128) + key * 128 + (((u0 + swap) ^ (key & 7)) << 4);
-        const int second =
-            (c >> 2) * (TK * 128) + key * 128 + (((u0 + 1 - swap) ^ (key & 7)) << 4);
+        // ---- e4m3 tiles to f16 in the MMA's layout.  A piece is 16 codes of a key: two 16-byte units
+        // of its row.  Of 8 lanes, four take the four pieces of a panel of an even key and four those
+        // of the next panel of the odd key after it, so that neither the loads nor the stores, whose
+        // units are turned by the key's number, meet in a bank.
+        constexpr int kKeys = kWidenWarps * 8, P = C::kPanels;  // keys at once; panels of a key
+        constexpr int kPieces = TK / kKeys * P, kBatch = 4;
+        const int t = tid - kWidenWarp * 32, piece = t & 3, odd_key = (t >> 2) & 1;
+        const int key = (t >> 3) * 2 + odd_key;  // and kKeys, 2 kKeys ... further on
+        static_assert(kKeys % 8 == 0, "the swizzle of a thread's pieces is one");
+        const uint32_t unit0 = ((2 * piece) ^ (key & 7)) << 4, unit1 = unit0 ^ 16;
         Ring<NR> raws(0);
         Ring<NK> keys(1);
         Ring<NV> values(1);
@@ -702,57 +692,61 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     ok = false;
                     break;
                 }
-                const uint8_t* const src = raw + rs * C::kRaw + t * 16;
-                uint8_t* const dst = ring + ts * C::kTile;
-                // a value past the end must not meet a weight of zero as NaN or infinity: only the
-                // last tile of all, V(n-1), holds any
-                int valid = TK;
-                if (i + 1 == 2 * cnt) valid = end - (cur.u + cnt - 1) * TK;
-                constexpr int kBatch = 4;
+                const uint8_t* const src = raw + rs * C::kRaw + key * D + piece * 16;
+                uint8_t* const dst = ring + ts * C::kTile + key * 128;
+                // piece x of this thread: its key, and its panel
+                auto key_of = [&](int x) { return x / P * kKeys; };
+                auto panel_of = [&](int x) { return (x + odd_key) % P; };
+                uint32_t most = 0;  // largest magnitudes, in two halves
 #pragma unroll 1
-                for (int x = 0; x < kPieces; x += kBatch) {
+                for (int x0 = 0; x0 < kPieces; x0 += kBatch) {
                     uint4 w[kBatch];
-                    uint32_t nan = 0;
 #pragma unroll
                     for (int y = 0; y < kBatch; ++y)
-                        w[y] = *reinterpret_cast<const uint4*>(src + (x + y) * kThr * 16);
+                        w[y] = *reinterpret_cast<const uint4*>(src + key_of(x0 + y) * D +
+                                                               panel_of(x0 + y) * 64);
 #pragma unroll
                     for (int y = 0; y < kBatch; ++y) {
-                        if (key + (x + y) * kStep >= valid) w[y] = make_uint4(0, 0, 0, 0);
                         const uint32_t in[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
                         uint32_t out[8];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             widen(in[j], out[2 * j], out[2 * j + 1]);
-                            nan |= (in[j] & 0x7f7f7f7fu) + 0x01010101u;
+                            most = larger(larger(most, out[2 * j]), out[2 * j + 1]);
                         }
-                        const uint4 a = make_uint4(out[0], out[1], out[2], out[3]);
-                        const uint4 b = make_uint4(out[4], out[5], out[6], out[7]);
-                        uint8_t* const to = dst + (x + y) * kStep * 128;
-                        *reinterpret_cast<uint4*>(to + first) = swap ? b : a;
-                        *reinterpret_cast<uint4*>(to + second) = swap ? a : b;
+                        uint8_t* const to =
+                            dst + key_of(x0 + y) * 128 + panel_of(x0 + y) * (TK * 128);
+                        *reinterpret_cast<uint4*>(to + unit0) =
+                            make_uint4(out[0], out[1], out[2], out[3]);
+                        *reinterpret_cast<uint4*>(to + unit1) =
+                            make_uint4(out[4], out[5], out[6], out[7]);
                     }
-                    if (nan & 0x80808080u) {  // a NaN code: rare, and only cvt knows it
+                }
+                // What is rare is done over: NaN codes, which only cvt knows, and values past the end,
+                // which must not meet a weight of zero as NaN or infinity (only V(n-1) holds any).
+                const int valid = i + 1 == 2 * cnt ? end - (cur.u + cnt - 1) * TK : TK;
+                if (valid < TK || (most & 0x7fffu) >= kWidenedNan ||
+                    (most >> 16 & 0x7fffu) >= kWidenedNan) {
 #pragma unroll 1
-                        for (int y = 0; y < kBatch; ++y) {
-                            if (key + (x + y) * kStep >= valid) continue;
-                            uint8_t* const to = dst + (x + y) * kStep * 128;
-                            const uint32_t* const in =
-                                reinterpret_cast<const uint32_t*>(src + (x + y) * kThr * 16);
+                    for (int x = 0; x < kPieces; ++x) {
+                        const uint32_t* const in = reinterpret_cast<const uint32_t*>(
+                            src + key_of(x) * D + panel_of(x) * 64);
+                        uint8_t* const to = dst + key_of(x) * 128 + panel_of(x) * (TK * 128);
 #pragma unroll 1
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t even, odd;
-                                widen_nan(in[j], even, odd);
-                                const bool low = j < 2;  // which 16-byte piece
-                                *reinterpret_cast<uint2*>(to + (low != (swap != 0) ? first : second) +
-                                                          (j & 1) * 8) = make_uint2(even, odd);
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t even = 0, odd = 0;
+                            if (key + key_of(x) < valid) widen_nan(in[j], even, odd);
+                            *reinterpret_cast<uint2*>(to + (j < 2 ? unit0 : unit1) + (j & 1) * 8) =
+                                make_uint2(even, odd);
                         }
                     }
                 }
                 fence_async_smem();
-                mbar_arrive(&sm.raw_empty[rs]);
-                mbar_arrive(&full[ts]);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&full[ts]);
+                    mbar_arrive(&sm.raw_empty[rs]);
+                }
                 raws.step();
                 if (v) values.step();
                 else keys.step();
