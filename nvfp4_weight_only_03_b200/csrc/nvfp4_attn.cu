@@ -64,10 +64,8 @@ struct Small {
     int start[2][12];  // a Cursor: where the range begins; then, by turns, the softmax's next tile
     uint32_t tmem;
     int stop;
-    union {
-        float max[2][2][kRows];  // of a unit: [its parity][warpgroup][lane]
-        float2 ml[2][kRows];     // of a row tile, maximum and sum: [warpgroup][lane]
-    } row;
+    float row_max[2][kRows];  // a unit's reference maximum: [its parity][row]
+    float row_sum[2][kRows];  // a row tile's sum of weights: [warpgroup][row]
     // biased exponents of the f16 Q rows' scales.  Q may be two row tiles ahead of the softmax.
     uint8_t q_scale[F8 ? 4 : 1][F8 ? kRows : 1];
 };
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         mbar_init(&sm.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kSoftmaxWarps);
+            mbar_init(&p_full[i], kSoftmaxWarps / 2);
             mbar_init(&sm.pv_done[i], 1);
             mbar_init(&sm.drained[i], 1);
         }
@@ -756,8 +754,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         if (!ok) code = 8;
     } else if (warp < kSoftmaxWarps) {
-        // ---- softmax: thread = row = tensor memory lane.  Two warpgroups take half of a unit's
-        // keys each and share the row's maximum.
+        // ---- softmax: thread = row = tensor memory lane.  Two warpgroups take the units by turns, so
+        // that one waits for scores and finds their maximum while the other forms weights; the
+        // reference maximum is handed from unit to unit, and each keeps a sum of its own.
         // The warps meet at barriers, so they must all take the same way: one thread reads what
         // comes next for all of them, and after a wait that gave up they go on (without waiting,
         // on whatever is there) to the end of the range.
@@ -789,88 +788,99 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 return j >= cnt || lane >= TK / 16 || key >= end ? 0
                                                                      : table[div_by(key, p.by_block)];
             };
-            int page = page_at(0);  // read a unit ahead
+            int page = page_at((g ^ wg) & 1);  // of this warpgroup's first unit; read a turn ahead
             float m = -INFINITY, l = 0.f, c = p.c;
+            auto scale_of_q = [&]() {  // (where scores of the row tile have arrived)
+                return __uint_as_float((uint32_t)sm.q_scale[item & 3][F8 ? row : 0] << 23);
+            };
 
-            // one unit's weights for this thread's keys
+            // unit j's weights
             auto weigh = [&](int j) {
-                constexpr int W = TK / 2, kChunk = 32, kChunks = W / kChunk;  // keys per thread
-                const int col0 = wg * W;
-                const int key0 = (cur.u + j) * TK + col0;
-                uint32_t s[kChunks][kChunk];
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i)
-                    tmem_ld(tmem + lanes + C::kS + (g & 1) * TK + col0 + i * kChunk, s[i]);
-                const uint32_t holes =
-                    __ballot_sync(~0u, (unsigned)page >= (unsigned)p.blocks) >> (col0 / 16);
-                const int see = last - key0;  // keys 0..see of this thread's
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) tmem_wait_ld(s[i]);
-                if (holes || __any_sync(~0u, see < W - 1)) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        if (i > see || ((holes >> (i / 16)) & 1))
-                            s[i / kChunk][i % kChunk] = 0xff800000u;  // -inf
-                }
+                constexpr int kChunks = TK / 32;
+                const uint32_t from = tmem + lanes + C::kS + wg * TK;
+                const uint32_t to = tmem + lanes + C::kP + wg * (TK / 2);
+                const uint32_t holes = __ballot_sync(~0u, (unsigned)page >= (unsigned)p.blocks);
+                const int see = last - (cur.u + j) * TK;  // keys 0..see of the unit
+                const bool masked = holes || __any_sync(~0u, see < TK - 1);
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i / kChunk][i % kChunk]));
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                sm.row.max[g & 1][wg][row] = top;
-                bar_sync(1 + quarter, 64);
-                top = fmaxf(top, sm.row.max[g & 1][wg ^ 1][row]);
-                if (j == 0) {
-                    m = top;
-                } else {
-                    const bool rise = mine && (top - m) * c > 8.f;
-                    if (__any_sync(~0u, rise)) {
-                        const float f = rise ? exp2_approx((m - top) * c) : 1.f;
-                        if (rise) m = top;
-                        l *= f;
-                        wait(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
-                        __syncwarp();
-                        tc_after_sync();
 #pragma unroll 1
-                        for (int i = 0; i < D / 64; ++i) {  // this warpgroup's half of O
-                            uint32_t o[32];
-                            tmem_ld(tmem + lanes + wg * (D / 2) + i * 32, o);
-                            tmem_wait_ld(o);
+                for (int i = 0; i < kChunks; ++i) {
+                    uint32_t s[32];
+                    tmem_ld(from + i * 32, s);
+                    tmem_wait_ld(s);
+                    if (masked) {  // the second pass reads them masked
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st(tmem + lanes + wg * (D / 2) + i * 32, o);
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (i * 32 + e > see || ((holes >> (i * 2 + e / 16)) & 1))
+                                s[e] = 0xff800000u;  // -inf
+                        tmem_st(from + i * 32, s);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+                }
+                if (masked) tmem_wait_st();
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (g > 0) bar_sync(1 + quarter * 2 + (wg ^ 1), 64);
+                const float was = j > 0 ? sm.row_max[wg ^ 1][row] : top;
+                // the reference rises only when it has to: weights stay below 2^8
+                const bool rise = j > 0 && mine && (top - was) * c > 8.f;
+                const float now = rise ? top : was;
+                sm.row_max[wg][row] = now;
+                bar_arrive(1 + quarter * 2 + wg, 64);
+                if (l > 0.f) l *= exp2_approx((m - now) * c);
+                m = now;
+                if (__any_sync(~0u, rise)) {
+                    const float f = rise ? exp2_approx((was - top) * c) : 1.f;
+                    wait(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+                    __syncwarp();
+                    tc_after_sync();
+#pragma unroll 1
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_ld(tmem + lanes + i * 32, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st(tmem + lanes + i * 32, o);
                     }
                 }
                 const float mc = m == -INFINITY ? 0.f : m * c;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                // a chunk is read while the one before it is worked on
+                uint32_t s[2][32];
+                tmem_ld(from, s[0]);
+#pragma unroll 1
+                for (int i = 0; i < kChunks; i += 2) {
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    uint32_t w[kChunk / 2];
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_wait_ld(s[h]);
+                        if (h == 0 || i + 2 < kChunks) tmem_ld(from + (i + h + 1) * 32, s[h ^ 1]);
+                        uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < kChunk / 2; ++e) {
-                        const float a =
-                            exp2_approx(fmaf(__uint_as_float(s[i][2 * e]), c, -mc));
-                        const float b =
-                            exp2_approx(fmaf(__uint_as_float(s[i][2 * e + 1]), c, -mc));
-                        sum[(2 * e) & 3] += a;
-                        sum[(2 * e + 1) & 3] += b;
-                        w[e] = pack16(F8, a, b);
+                        for (int e = 0; e < 16; ++e) {
+                            const float a =
+                                exp2_approx(fmaf(__uint_as_float(s[h][2 * e]), c, -mc));
+                            const float b =
+                                exp2_approx(fmaf(__uint_as_float(s[h][2 * e + 1]), c, -mc));
+                            sum[(2 * e) & 3] += a;
+                            sum[(2 * e + 1) & 3] += b;
+                            w[e] = pack16(F8, a, b);
+                        }
+                        tmem_st(to + (i + h) * 16, w);
                     }
-                    tmem_st(tmem + lanes + C::kP + (g & 1) * (TK / 2) + (col0 + i * kChunk) / 2,
-                            w);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_st();
             };
 
             for (int j = 0; j < cnt; ++j, ++g) {
-                const int page_next = page_at(j + 1);
-                wait(&s_full[g & 1], (g >> 1) & 1);
+                if ((g & 1) != wg) continue;  // the other warpgroup's
+                const int page_next = page_at(j + 2);
+                wait(&s_full[wg], (g >> 1) & 1);
                 // P's place is free once unit g - 2 is through (and V's of that unit, so that the
                 // phase of a V place below is not taken for an earlier one's: NV >= 2)
-                if (g >= 2) wait(&sm.pv_done[g & 1], ((g >> 1) - 1) & 1);
+                if (g >= 2) wait(&sm.pv_done[wg], ((g >> 1) - 1) & 1);
                 tc_after_sync();
                 const int unit0 = (cur.u + j) * TK;
                 if (!F8 && unit0 + TK > end) {
@@ -880,7 +890,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     wait(&full[slot], (vi / NV) & 1);
                     const int from = max(end - unit0, 0);
                     uint8_t* const v = ring + slot * C::kTile;
-                    for (int i = tid; i < (TK - from) * (D / 8); i += kSoftmaxWarps * 32) {
+                    for (int i = row; i < (TK - from) * (D / 8); i += kRows) {
                         const int key = from + i / (D / 8), x = i % (D / 8);
                         *reinterpret_cast<uint4*>(v + (x >> 3) * (TK * 128) + key * 128 +
                                                   (x & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -888,13 +898,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     fence_async_smem();
                 }
                 __syncwarp();
-                // the scores are there, so the rows' scales are (q_full itself may be a phase on)
-                if (F8 && j == 0 && mine)
-                    c *= __uint_as_float((uint32_t)sm.q_scale[item & 3][row] << 23);
-                if (busy) weigh(j);
+                if (F8 && j < 2 && mine) c = p.c * scale_of_q();  // this warpgroup's first unit
+                if (busy) {
+                    weigh(j);
+                } else {
+                    if (g > 0) bar_sync(1 + quarter * 2 + (wg ^ 1), 64);
+                    bar_arrive(1 + quarter * 2 + wg, 64);
+                }
                 tc_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[g & 1]);
+                if (lane == 0) mbar_arrive(&p_full[wg]);
                 page = page_next;
             }
             wait(&sm.o_full, item & 1);
@@ -902,16 +915,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             tc_after_sync();
 
             // ---- O: divided by the sum and written, or left as a part
-            sm.row.ml[wg][row] = make_float2(m == -INFINITY ? m : m * c, l);
-            bar_sync(5, kSoftmaxWarps * 32);
-            const float total = l + sm.row.ml[wg ^ 1][row].y;
-            bar_sync(5, kSoftmaxWarps * 32);  // its place serves the next unit's maxima
+            bar_sync(9, kSoftmaxWarps * 32);
+            if (F8 && mine) c = p.c * scale_of_q();  // (also if it had no unit)
+            const float most = busy ? sm.row_max[(g - 1) & 1][row] : -INFINITY;  // the last unit's
+            sm.row_sum[wg][row] = l > 0.f ? l * exp2_approx((m - most) * c) : l;
+            bar_sync(9, kSoftmaxWarps * 32);
+            const float total = sm.row_sum[0][row] + sm.row_sum[1][row];
             const bool whole = cur.u == 0 && cnt == cur.n;
             const int which = cur.u == 0 ? 1 : 0;  // this CTA's cut at its end, or at its start
             const int64_t part0 = ((int64_t)blockIdx.x * 2 + which) * kRows;
             const float inv = total == 0.f ? 0.f : p.v_scale / total;
             if (!whole && mine && wg == 0)
-                p.part_ml[part0 + row] = make_float2(m == -INFINITY ? m : m * c, total);
+                p.part_ml[part0 + row] = make_float2(most == -INFINITY ? most : most * c, total);
             if (busy) {
                 uint16_t* const out =
                     p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +
