@@ -21,10 +21,11 @@
 //   memory; it is rescaled only when a row's maximum rose by more than 2^8 (P is then at most
 //   2^8 and the sums are fp32, so nothing overflows).  S and P have two buffers each, so the MMAs
 //   of one unit run under the softmax of another.
-// * Roles: 8 softmax warps, one warp each for the scores' MMAs, the values' MMAs, TMA and Q, and 4
-//   that widen an e4m3 cache to f16 (exact); the bf16 cache goes to the MMA as it lies in memory.
+// * Roles: 8 softmax warps, one warp each for the scores' MMAs, the values' MMAs, K, and Q and V, and 4
+//   that widen the V of an e4m3 cache to f16 (exact); all else goes to the MMA as it lies in memory.
 // * P is rounded to the MMA's 16-bit type (bf16, or f16 with the e4m3 cache): half a step, 2^-9
-//   (2^-12) of each weight.  With the e4m3 cache q is carried as f16 times a power of two per row.
+//   (2^-12) of each weight.  With the e4m3 cache K is read by 8-bit MMAs as it lies, q being carried
+//   as two e4m3 terms times a power of two per row (an error of at most 2^-17 of the row's largest).
 //   S, O, maxima and sums are fp32.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -55,9 +56,9 @@ constexpr int kTmemCols = 512;
 constexpr size_t kSmemMost = 232448;  // shared memory of a block
 
 // The small things in shared memory, ahead of the tiles.
-template <int NS, int NR, bool F8>
+template <int NK, int NV, int NR, bool F8>
 struct Small {
-    uint64_t full[NS], empty[NS];  // of the K places, then of the V places
+    uint64_t full[NK + NV], empty[NK + NV];  // of the K places, then of the V places
     uint64_t raw_full[NR], raw_empty[NR];
     uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], o_full, o_free, drained[2];
     int64_t sums[20];
@@ -66,33 +67,36 @@ struct Small {
     int stop;
     float row_max[2][kRows];  // a unit's reference maximum: [its parity][row]
     float row_sum[2][kRows];  // a row tile's sum of weights: [warpgroup][row]
-    // biased exponents of the f16 Q rows' scales.  Q may be two row tiles ahead of the softmax.
+    // biased exponents of the 8-bit Q rows' scales.  Q may be two row tiles ahead of the softmax.
     uint8_t q_scale[F8 ? 4 : 1][F8 ? kRows : 1];
 };
 
 template <int D, bool F8>
 struct Cfg {
-    static constexpr int TK = D == 256 ? 64 : 128;          // keys per unit
-    static constexpr int kPanels = D / 64;                  // 128-byte panels of a row
-    static constexpr int kQBytes = kRows * D * 2;
-    static constexpr int kTile = TK * D * 2;                // one K or V tile, 16-bit
-    static constexpr int kRaw = F8 ? TK * D : 0;            // the same in e4m3
+    static constexpr int TK = D == 256 ? 64 : 128;    // keys per unit
+    static constexpr int kQBytes = kRows * D * 2;     // bf16, or two 8-bit terms
+    static constexpr int kKey = TK * D * (F8 ? 1 : 2);  // a K tile
+    static constexpr int kVal = TK * D * 2;           // a V tile, 16-bit
+    static constexpr int kRaw = F8 ? TK * D : 0;      // the same in e4m3
+    static constexpr int kRow = F8 && D == 64 ? 64 : 128;  // bytes of a row of a panel of Q and K
+    static constexpr int kRowKeys = F8 ? kRow : 64;   // its values
+    static constexpr int kPanels = D / kRowKeys;      // panels of Q and K
     static constexpr int kThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kQWarp + 1);
-    static constexpr size_t kHead = F8 ? 4096 : 3072;       // Small, in front of the tiles
-    static constexpr int kStages =
-        F8 ? (D == 64 ? 6 : D == 128 ? 4 : 3) : (int)((kSmemMost - kHead - kQBytes) / kTile);
-    static constexpr int kRawStages =
-        F8 ? (int)((kSmemMost - kHead - kQBytes - kStages * kTile) / (F8 ? kRaw : 1)) : 1;
-    static constexpr size_t kSmem =
-        kHead + kQBytes + (size_t)kStages * kTile + (F8 ? (size_t)kRawStages * kRaw : 0);
-    // Places of K and of V: rings of their own, since their readers go on independently (with one
-    // ring, a reader could take the phase of the other's tile for that of its own).
-    static constexpr int kKeyStages = kStages / 2, kValueStages = kStages - kKeyStages;
-    using Shared = Small<kStages, kRawStages, F8>;
+    static constexpr size_t kHead = F8 ? 4096 : 3072;  // Small, in front of the tiles
+    // Places of K, of V and of V as it lies in an e4m3 cache.  K and V have rings of their own, since
+    // their readers go on independently (with one ring, a reader could take the phase of the
+    // other's tile for that of its own).
+    static constexpr int kStages = (int)((kSmemMost - kHead - kQBytes) / kVal);
+    static constexpr int NK = F8 ? (D == 64 ? 6 : D == 128 ? 4 : 3) : kStages / 2;
+    static constexpr int NV = F8 ? (D == 64 ? 4 : 2) : kStages - NK;
+    static constexpr int NR = F8 ? (D == 64 ? 6 : D == 128 ? 3 : 2) : 1;
+    static constexpr size_t kSmem = kHead + kQBytes + (size_t)NK * kKey + (size_t)NV * kVal +
+                                    (F8 ? (size_t)NR * kRaw : 0);
+    using Shared = Small<NK, NV, NR, F8>;
     // tensor memory columns: O, then two S, then two P (two 16-bit values per column)
     static constexpr int kS = D, kP = D + 2 * TK, kEnd = D + 2 * TK + TK;
     static_assert(kEnd <= kTmemCols, "tensor memory");
-    static_assert(kKeyStages >= 1 && kValueStages >= 2, "rings");
+    static_assert(NK >= 1 && NV >= 2, "rings");
     static_assert(kSmem <= kSmemMost && sizeof(Shared) <= kHead, "shared memory");
 };
 
@@ -163,9 +167,9 @@ __device__ __forceinline__ uint32_t pack16(bool f16, float lo, float hi) {
 
 // Four e4m3 codes (bytes 0..3) -> f16 values times 2^-8, exact, as the pairs {0, 2} and {1, 3}: a
 // code's exponent and mantissa, seven bits, moved to the same place below f16's exponent bias (15
-// against 7), subnormals included; the factor goes into the scores' and the output's scale.  Seven
-// shifts and masks; cvt has the rate of the exponentials and shares their pipe (measured: a verify
-// batch is 1.5 times as fast this way).  Q and O are put in the pairs' order where they are packed.
+// against 7), subnormals included; the factor goes into the output's scale.  Seven
+// shifts and masks; cvt has the rate of the exponentials and shares their pipe.  O comes out in the
+// pairs' order and is put right where it is written.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& even, uint32_t& odd) {
     even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
     odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
@@ -186,6 +190,18 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// Two values as e4m3 codes (the first in the low byte), and back.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
 // ---- the order of the work ---------------------------------------------------------------
@@ -255,11 +271,6 @@ struct Cursor {
     }
 };
 
-// The order in which the tiles of a row tile's `cnt` units go through the ring, K one unit ahead of
-// V: K0 K1 V0 K2 V1 ... K(cnt-1) V(cnt-2) V(cnt-1).
-__device__ __forceinline__ bool is_value(int i, int cnt) {
-    return i + 1 == 2 * cnt || (i > 0 && (i & 1) == 0);
-}
 // A reader's or writer's place in a ring of N tiles, and the phase of its barriers.
 template <int N>
 struct Ring {
@@ -363,13 +374,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     nvfp4_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<D, F8>;
-    constexpr int TK = C::TK, NS = C::kStages, NR = C::kRawStages;
-    constexpr int NK = C::kKeyStages, NV = C::kValueStages;
+    constexpr int TK = C::TK, NK = C::NK, NV = C::NV, NR = C::NR;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     typename C::Shared& sm = *reinterpret_cast<typename C::Shared*>(smem_raw);
     uint8_t* const q_tile = smem_raw + C::kHead;
-    uint8_t* const ring = q_tile + C::kQBytes;
-    uint8_t* const raw = ring + NS * C::kTile;
+    uint8_t* const key_ring = q_tile + C::kQBytes;
+    uint8_t* const val_ring = key_ring + NK * C::kKey;
+    uint8_t* const raw = val_ring + NV * C::kVal;
     uint64_t *const full = sm.full, *const empty = sm.empty, *const s_full = sm.s_full,
              *const p_full = sm.p_full;
     // (the tiles' swizzle wants 1024-byte alignment, which the block's only allocation has)
@@ -389,8 +400,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], F8 ? kWidenWarps : 1);
+        for (int i = 0; i < NK + NV; ++i) {
+            mbar_init(&full[i], F8 && i >= NK ? kWidenWarps : 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < NR; ++i) {
@@ -428,21 +439,25 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     if (left == 0) {
         // nothing to do
     } else if (warp == kTmaWarp || warp == kQWarp) {
-        // ---- what the products read.  bf16: one warp copies the K tiles, another gathers Q's rows
-        // and copies the V tiles (one warp alone was the kernel's bound with pages of 16 keys).  e4m3:
-        // one warp copies K and V tiles to where they are widened, in the order K0 K1 V0 K2 V1 ...
-        // V(n-1), and another gathers Q.  A tile is TK / box groups of `box` keys of one page each
-        // (lane i knows group i's page and place), and a group is a box per 64 values.  Keys past the
+        // ---- what the products read: one warp copies the K tiles, another gathers Q's rows and
+        // copies the V tiles (of an e4m3 cache, to where they are widened); one warp alone was the
+        // kernel's bound with pages of 16 keys.  A tile is TK / box groups of `box` keys of one page
+        // each (lane i knows group i's page and place), and a group is a box per panel.  Keys past the
         // end, and pages that do not exist, are boxes outside the tensor, which arrive as zeros.  One
         // elected lane issues all of a tile's boxes: a divergent issue, a lane per box, took 95
         // cycles a box.
         constexpr int kMost = TK / 16;
         const bool second = warp == kQWarp;
-        const int groups = TK / p.box, step = p.box * (F8 ? D : 128);  // bytes of a group (a panel's)
-        const int places = F8 ? NR : second ? NV : NK, place0_at = !F8 && second ? NK : 0;
-        uint64_t* const fulls = F8 ? sm.raw_full : full + place0_at;
-        uint64_t* const empties = F8 ? sm.raw_empty : empty + place0_at;
-        const uint32_t room = smem_u32(F8 ? raw : ring + place0_at * C::kTile);
+        const int groups = TK / p.box;
+        const int places = !second ? NK : F8 ? NR : NV;
+        uint64_t* const fulls = !second ? full : F8 ? sm.raw_full : full + NK;
+        uint64_t* const empties = !second ? empty : F8 ? sm.raw_empty : empty + NK;
+        const uint32_t room = smem_u32(!second ? key_ring : F8 ? raw : val_ring);
+        const int bytes = !second ? C::kKey : F8 ? C::kRaw : C::kVal;
+        const CUtensorMap* const map = second ? &map_v : &map_k;
+        // 128-byte (64-byte) rows of a panel, or, where V is widened, whole rows
+        const bool whole_rows = F8 && second;
+        const int step = p.box * (whole_rows ? D : C::kRow);  // bytes of a group (in a panel)
         int slot = 0, it = 0, item = 0;
         uint32_t phase = 1;  // (the first lap finds every place free)
         // Q's rows in the MMA's layout (K-major, 128-byte swizzle)
@@ -469,11 +484,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                                  : "memory");
                 asm volatile("cp.async.wait_all;" ::: "memory");
             } else {
-                // x 2^e with the row's largest magnitude in [2^14, 2^15), as f16.  D / 8 lanes take a
-                // row, 16 bytes each; a warp reads kBatch such groups of rows before it works on
+                // Q as two e4m3 terms of x = q 2^e, with the row's largest magnitude in [2^7, 2^8): the
+                // first is x rounded to its 4 bits, and what that leaves of bf16's 8 bits is at most 8
+                // of its last place, 4 bits again, so the two are exact down to e4m3's smallest step,
+                // 2^-9: an error of at most 2^-10, 2^-17 of the row's largest value.  D / 8 lanes take
+                // a row, 16 bytes each; a warp reads kBatch such groups of rows before it works on
                 // them, since a row alone is a memory latency.
                 constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
                 const int sub = lane / kLanes, c = lane % kLanes;
+                const int panel = c * 8 / C::kRowKeys, in_row = c * 8 % C::kRowKeys;
                 for (int r0 = 0; r0 < rows; r0 += kAtOnce * kBatch) {
                     uint4 v[kBatch];
 #pragma unroll
@@ -483,10 +502,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         if (r < rows)
                             v[i] = *reinterpret_cast<const uint4*>(src_of(r) + c * 8);
                     }
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < kBatch; ++i) {
                         const int r = r0 + i * kAtOnce + sub;
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        const uint4 x = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                         uint32_t big = 0;  // largest magnitude's bits; NaN and infinity lead
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -495,23 +515,30 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         for (int d = kLanes / 2; d; d >>= 1)
                             big = max(big, __shfl_xor_sync(~0u, big, d));
                         // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value
-                        // is below 2^-50 has scores of zero to fp32 either way
-                        const int up = min(127 + 14 + 127 - (int)(big >> 7), 127 + 64);
+                        // is below 2^-57 has scores of zero to fp32 either way.  An infinity times
+                        // 2^e - 2^e is NaN, as e4m3 has none.
+                        const int up = min(127 + 7 + 127 - (int)(big >> 7), 127 + 64);
                         const float mul = __uint_as_float((uint32_t)up << 23);
-                        uint32_t h[4];
+                        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-                        for (int e = 0; e < 4; e += 2) {  // values 0, 2 and 1, 3 of four
-                            h[e] = pack16(true, __uint_as_float(w[e] << 16) * mul,
-                                          __uint_as_float(w[e + 1] << 16) * mul);
-                            h[e + 1] = pack16(true, __uint_as_float(w[e] & 0xffff0000u) * mul,
-                                              __uint_as_float(w[e + 1] & 0xffff0000u) * mul);
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = __uint_as_float(w[e] << 16) * mul;
+                            const float b = __uint_as_float(w[e] & 0xffff0000u) * mul;
+                            const uint32_t h = e4m3_pair(a, b);
+                            const float2 f = e4m3_values(h);
+                            // (a - a is 0, or NaN where a is infinite)
+                            const uint32_t l = e4m3_pair(a - f.x + (a - a), b - f.y + (b - b));
+                            hi[e >> 1] |= h << (e & 1) * 16;
+                            lo[e >> 1] |= l << (e & 1) * 16;
                         }
                         if (r < rows) {
-                            if (c == 0)
-                                sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
-                            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (kRows * 128) + r * 128 +
-                                                      (((c & 7) ^ (r & 7)) << 4)) =
-                                make_uint4(h[0], h[1], h[2], h[3]);
+                            if (c == 0) sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
+                            // 16-byte units turned by the row, as TMA turns K's
+                            const int turn = C::kRow == 128 ? r & 7 : (r >> 1) & 3;
+                            uint8_t* const to = q_tile + panel * (kRows * C::kRow) + r * C::kRow +
+                                                (((in_row >> 4) ^ turn) << 4) + (in_row & 8);
+                            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(to + kRows * D) = make_uint2(lo[0], lo[1]);
                         }
                     }
                 }
@@ -538,34 +565,30 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             // pages are read ahead of their unit's first box
             int place0, place1, place2;
             int page0 = page_at(0, place0), page1 = page_at(1, place1), page2 = page_at(2, place2);
-            const int tiles = F8 ? (second ? 0 : 2 * cnt) : cnt;
-            for (int i = 0; i < tiles && ok; ++i) {
-                const bool v = F8 ? is_value(i, cnt) : second, first = !F8 || v || i == 0;
-                const int page = first ? page0 : page1, place = first ? place0 : place1;
-                const int at = (unsigned)page < (unsigned)p.blocks ? page : p.outside;
+            for (int i = 0; i < cnt; ++i) {
+                const int at = (unsigned)page0 < (unsigned)p.blocks ? page0 : p.outside;
                 int w[kMost], y[kMost];
 #pragma unroll
                 for (int x = 0; x < kMost; ++x) {
                     w[x] = __shfl_sync(~0u, at, x);
-                    y[x] = __shfl_sync(~0u, place, x);
+                    y[x] = __shfl_sync(~0u, place0, x);
                 }
-                const CUtensorMap* const map = v ? &map_v : &map_k;
                 const uint32_t fb = uniform(smem_u32(fulls + slot));
-                const uint32_t dst = uniform(room + slot * (F8 ? C::kRaw : C::kTile));
+                const uint32_t dst = uniform(room + slot * bytes);
                 ok = __all_sync(~0u, mbar_wait(empties + slot, phase, stop_v));
                 if (!ok) break;
                 if (elect_one()) {
-                    mbar_expect_tx(fb, F8 ? C::kRaw : C::kTile);
+                    mbar_expect_tx(fb, bytes);
 #pragma unroll
                     for (int x = 0; x < kMost; ++x) {
                         if (x >= groups) break;
-                        if (F8) {
+                        if (whole_rows) {
                             tma_load_4d(dst + x * step, map, 0, y[x], head, w[x], fb);
                         } else {
 #pragma unroll
                             for (int pn = 0; pn < C::kPanels; ++pn)
-                                tma_load_4d(dst + pn * (TK * 128) + x * step, map, pn * 64, y[x],
-                                            head, w[x], fb);
+                                tma_load_4d(dst + pn * (TK * C::kRow) + x * step, map,
+                                            pn * C::kRowKeys, y[x], head, w[x], fb);
                         }
                     }
                 }
@@ -575,11 +598,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     slot = 0;
                     phase ^= 1;
                 }
-                if (!F8 || v) {
-                    page0 = page1, place0 = place1;
-                    page1 = page2, place1 = place2;
-                    page2 = page_at((F8 ? i / 2 - 1 : i) + 3, place2);
-                }
+                page0 = page1, place0 = place1;
+                page1 = page2, place1 = place2;
+                page2 = page_at(i + 3, place2);
             }
             ++item;
             left -= cur.lead + cnt;
@@ -596,8 +617,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // product waits in the tensor core's queue while a warp looks after its barriers.
         // Unit g's scores need the weights of g - 2 formed (whose scores had their place).
         const bool values = warp == kValuesWarp;
-        constexpr uint32_t id_s = idesc_16(!F8, TK, false), id_o = idesc_16(!F8, D, true);
-        const uint32_t q_low = uniform(smem_u32(q_tile) >> 4), ring_low = smem_u32(ring) >> 4;
+        constexpr uint32_t id_s = F8 ? idesc_8(TK) : idesc_16(true, TK, false);
+        constexpr uint32_t id_o = idesc_16(!F8, D, true);
+        const uint32_t q_low = uniform(smem_u32(q_tile) >> 4);
         int g = 0, item = 0;
         Ring<NK> keys(0);
         Ring<NV> vals(0);
@@ -614,15 +636,24 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     const int slot = keys.slot;
                     if (!ready(&full[slot], keys.phase)) break;
                     if (g >= 2 && !ready(&p_full[g & 1], ((g >> 1) - 1) & 1)) break;
-                    const uint32_t low = uniform(ring_low + slot * (C::kTile >> 4));
+                    const uint32_t low = uniform((smem_u32(key_ring) + slot * C::kKey) >> 4);
                     const uint32_t d = uniform(tmem + C::kS + (g & 1) * TK);
                     tc_after_sync();
                     if (elect_one()) {
+                        // 32 bytes of a row per step: 16 values, or 32 of 8 bits
+                        constexpr int kSteps = F8 ? D / 32 : D / 16, kPer = C::kRow / 32;
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            mma_ss(d, desc_at(q_low, 16, (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
-                                   desc_at(low, 16, (kk >> 2) * (TK * 128) + (kk & 3) * 32), id_s,
-                                   kk > 0);
+                        for (int x = 0; x < (F8 ? 2 : 1) * kSteps; ++x) {
+                            const int kk = x % kSteps;  // (the second time: Q's second term)
+                            const uint64_t a =
+                                desc_at(q_low, 16, x / kSteps * (kRows * D) +
+                                                       kk / kPer * (kRows * C::kRow) + kk % kPer * 32,
+                                        C::kRow);
+                            const uint64_t b = desc_at(
+                                low, 16, kk / kPer * (TK * C::kRow) + kk % kPer * 32, C::kRow);
+                            if (F8) mma_ss_8(d, a, b, id_s, x > 0);
+                            else mma_ss(d, a, b, id_s, x > 0);
+                        }
                         mma_commit(&s_full[g & 1]);
                         mma_commit(&empty[slot]);
                         if (j + 1 == cnt) mma_commit(&sm.q_free);
@@ -632,11 +663,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 }
             } else {
                 for (int j = 0; j < cnt; ++j, ++g) {
-                    const int slot = NK + vals.slot;
-                    if (!ready(&full[slot], vals.phase)) break;
+                    const int slot = vals.slot;
+                    if (!ready(&full[NK + slot], vals.phase)) break;
                     if (!ready(&p_full[g & 1], (g >> 1) & 1)) break;
                     if (j == 0 && item > 0 && !ready(&sm.o_free, (item - 1) & 1)) break;
-                    const uint32_t low = uniform(ring_low + slot * (C::kTile >> 4));
+                    const uint32_t low = uniform((smem_u32(val_ring) + slot * C::kVal) >> 4);
                     const uint32_t a = uniform(tmem + C::kP + (g & 1) * (TK / 2));
                     const uint32_t d = uniform(tmem);
                     tc_after_sync();
@@ -645,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         for (int kk = 0; kk < TK / 16; ++kk)
                             mma_ts(d, a + kk * 8, desc_at(low, TK * 128, kk * 2048), id_o,
                                    kk > 0 || j > 0);
-                        mma_commit(&empty[slot]);
+                        mma_commit(&empty[NK + slot]);
                         mma_commit(&sm.pv_done[g & 1]);
                         if (j + 1 == cnt) mma_commit(&sm.o_full);
                     }
@@ -665,33 +696,32 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_wait(&sm.drained[values], 0, &none, 20000000ll);
         }
     } else if (F8 && warp >= kWidenWarp) {
-        // ---- e4m3 tiles to f16 in the MMA's layout.  A piece is 16 codes of a key: two 16-byte units
+        // ---- V tiles of an e4m3 cache to f16 in the MMA's layout (K goes to the MMA as it lies, against
+        // Q in two e4m3 terms; for P that would be three conversions per weight).  A piece is 16 codes of a key: two 16-byte units
         // of its row.  Of 8 lanes, four take the four pieces of a panel of an even key and four those
         // of the next panel of the odd key after it, so that neither the loads nor the stores, whose
         // units are turned by the key's number, meet in a bank.
-        constexpr int kKeys = kWidenWarps * 8, P = C::kPanels;  // keys at once; panels of a key
-        constexpr int kPieces = TK / kKeys * P, kBatch = 4;
+        constexpr int kKeys = kWidenWarps * 8, P = D / 64;  // keys at once; panels of a key
+        constexpr int kPieces = TK / kKeys * P, kBatch = kPieces < 4 ? kPieces : 4;
         const int t = tid - kWidenWarp * 32, piece = t & 3, odd_key = (t >> 2) & 1;
         const int key = (t >> 3) * 2 + odd_key;  // and kKeys, 2 kKeys ... further on
         static_assert(kKeys % 8 == 0, "the swizzle of a thread's pieces is one");
         const uint32_t unit0 = ((2 * piece) ^ (key & 7)) << 4, unit1 = unit0 ^ 16;
         Ring<NR> raws(0);
-        Ring<NK> keys(1);
         Ring<NV> values(1);
         while (left > 0 && ok) {
             const int cnt = cur.take(left);
             if (cnt <= 0) break;
             const int end = key_end(p, cur.q, cur.tile);
-            for (int i = 0; i < 2 * cnt; ++i) {
-                const bool v = is_value(i, cnt);
-                const int rs = raws.slot, ts = v ? NK + values.slot : keys.slot;
+            for (int i = 0; i < cnt; ++i) {
+                const int rs = raws.slot, ts = values.slot;
                 if (!mbar_wait(&sm.raw_full[rs], raws.phase, stop_v) ||
-                    !mbar_wait(&empty[ts], v ? values.phase : keys.phase, stop_v)) {
+                    !mbar_wait(&empty[NK + ts], values.phase, stop_v)) {
                     ok = false;
                     break;
                 }
                 const uint8_t* const src = raw + rs * C::kRaw + key * D + piece * 16;
-                uint8_t* const dst = ring + ts * C::kTile + key * 128;
+                uint8_t* const dst = val_ring + ts * C::kVal + key * 128;
                 // piece x of this thread: its key, and its panel
                 auto key_of = [&](int x) { return x / P * kKeys; };
                 auto panel_of = [&](int x) { return (x + odd_key) % P; };
@@ -722,7 +752,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 }
                 // What is rare is done over: NaN codes, which only cvt knows, and values past the end,
                 // which must not meet a weight of zero as NaN or infinity (only V(n-1) holds any).
-                const int valid = i + 1 == 2 * cnt ? end - (cur.u + cnt - 1) * TK : TK;
+                const int valid = end - (cur.u + i) * TK;
                 if (valid < TK || (most & 0x7fffu) >= kWidenedNan ||
                     (most >> 16 & 0x7fffu) >= kWidenedNan) {
 #pragma unroll 1
@@ -742,12 +772,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&full[ts]);
+                    mbar_arrive(&full[NK + ts]);
                     mbar_arrive(&sm.raw_empty[rs]);
                 }
                 raws.step();
-                if (v) values.step();
-                else keys.step();
+                values.step();
             }
             left -= cur.lead + cnt;
             cur.next(p);
@@ -886,10 +915,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 if (!F8 && unit0 + TK > end) {
                     // values past the end are whatever the page held: zeros, so that their weights
                     // of zero add nothing
-                    const int vi = values_at + cnt - 1, slot = NK + vi % NV;
-                    wait(&full[slot], (vi / NV) & 1);
+                    const int vi = values_at + cnt - 1, slot = vi % NV;
+                    wait(&full[NK + slot], (vi / NV) & 1);
                     const int from = max(end - unit0, 0);
-                    uint8_t* const v = ring + slot * C::kTile;
+                    uint8_t* const v = val_ring + slot * C::kVal;
                     for (int i = row; i < (TK - from) * (D / 8); i += kRows) {
                         const int key = from + i / (D / 8), x = i % (D / 8);
                         *reinterpret_cast<uint4*>(v + (x >> 3) * (TK * 128) + key * 128 +
@@ -1166,14 +1195,20 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
         const cuuint64_t strides[3] = {(cuuint64_t)kv.slot_stride * size,
                                        (cuuint64_t)kv.head_stride * size,
                                        (cuuint64_t)kv.block_stride * size};
-        const cuuint32_t boxes[4] = {(cuuint32_t)(f8 ? kv.dim : 64), (cuuint32_t)box, 1, 1};
+        // K, and V in bf16, panel by panel as the MMA reads them; V in e4m3 in whole rows
+        const bool panels = !f8 || i == 0;
+        const int row = f8 && kv.dim == 64 ? 64 : 128;
+        const cuuint32_t boxes[4] = {(cuuint32_t)(panels ? row / size : kv.dim), (cuuint32_t)box, 1,
+                                     1};
+        const CUtensorMapSwizzle swizzle = !panels      ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                           : row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                        : CU_TENSOR_MAP_SWIZZLE_64B;
         const cuuint32_t one[4] = {1, 1, 1, 1};
         // without pages nothing is read: every box then lies outside, on any valid address
         void* const at = const_cast<void*>(kv.blocks ? tensors[i] : workspace);
         if (encode(&maps[i], f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                    4, at, dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return NVFP4_ERR_LAUNCH;
     }
@@ -1201,7 +1236,7 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     p.box = box;
     const int64_t cap = a.table_columns * kv.block_size;
     p.capacity = (int)(cap > INT32_MAX - 1024 ? INT32_MAX - 1024 : cap);
-    p.c = a.scale * (f8 ? kv.k_scale * kWidened : 1.f) * 1.4426950408889634f;
+    p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;
     p.v_scale = f8 ? kv.v_scale * kWidened : 1.f;
     // a factor that left fp32's normal range would turn a masked score of -infinity into NaN
     if (!(p.c >= 1.1754944e-38f) || isinf(p.c)) return NVFP4_ERR_SHAPE;

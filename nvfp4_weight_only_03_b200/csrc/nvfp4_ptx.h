@@ -97,14 +97,17 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 
-// Shared-memory matrix descriptor, 128-byte swizzle, of the tile at 16 * low plus offset bytes.
-// K-major: rows of 128 bytes, 8-row atoms 1024 bytes apart (panel is 16, unused).  MN-major: 64
-// values of the M/N side per 128-byte row, 8 rows of the K side per atom (the next 8 another 1024
-// bytes on), the next 64 values `panel` bytes on.
-__device__ __forceinline__ uint64_t desc_at(uint32_t low, uint32_t panel, uint32_t offset) {
+// Shared-memory matrix descriptor of the tile at 16 * low plus offset bytes, swizzled over rows of
+// `row` bytes (128 or 64).  K-major: a row holds consecutive values of the K side, 8-row atoms follow
+// one another (panel is 16, unused).  MN-major: a row holds 64 values of the M/N side, 8 rows of
+// the K side are an atom, and the next 64 values lie `panel` bytes on.
+__device__ __forceinline__ uint64_t desc_at(uint32_t low, uint32_t panel, uint32_t offset,
+                                            uint32_t row = 128) {
     return (uint64_t)(low + (offset >> 4)) | ((uint64_t)((panel >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+           ((uint64_t)(8 * row >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)(row == 128 ? 2 : 4) << 61);
 }
+
 // Instruction descriptor of kind::f16: D fp32, A and B both bf16 or both f16, M = 128.
 __host__ __device__ constexpr uint32_t idesc_16(bool bf16, int n, bool b_mn_major) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u) |
@@ -116,6 +119,19 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 8-bit operands: descriptor (e4m3 both, K-major, M = 128, fp32 accumulators) and product.
+__host__ __device__ constexpr uint32_t idesc_8(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss_8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }

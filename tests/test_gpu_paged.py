@@ -9,7 +9,10 @@ sees, h the half step of a rounding (bf16 2^-8, f16 2^-11, fp32 2^-24):
                                weight is at least 1, so the sum of weights is, too)
   scores                       a sum of D products off by at most D 2^-23 sum|q k| (twice the
                                rounding of every partial sum) moves a weight by as much,
-                               relatively, in the numerator and in the sum: 2 delta A
+                               relatively, in the numerator and in the sum: 2 delta A.  With an
+                               e4m3 cache q is carried as two e4m3 terms of q 2^e, |q 2^e| < 2^8:
+                               off by at most half their smallest step, 2^-10, where the row's
+                               largest is at least 2^7: delta also has 2^-17 max|q| sum|k|
   exponent and sums            2^-20 (argument, ex2 and the rescaling), and 2^-23 per step of a
                                chain of n / 16 MMA steps and 128 additions, in both: times 2 A
 """
@@ -131,6 +134,9 @@ class Batch:
                 s = torch.where(see, s, -torch.inf)
                 delta = torch.where(see, mag, 0.0).amax(-1) if cap else q.new_zeros(m, G)
                 delta = delta * self.dim * 2.0 ** -23
+                if self.f8 and cap:
+                    delta = delta + 2.0 ** -17 * self.scale * q.abs().amax(-1) * \
+                        k.abs().sum(-1).nan_to_num(0.0).max()
                 w = torch.exp(s - s.amax(-1, keepdim=True).clamp(min=-1e300)) if cap else s
                 tot = w.sum(-1, keepdim=True)
                 w = torch.where(tot > 0, w / tot.clamp(min=1e-300), 0.0)
