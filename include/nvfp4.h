@@ -530,7 +530,7 @@ typedef struct {
     int32_t rank;
 } nvfp4_lora_t;
 
-/* Workspace bytes of nvfp4_lora_add (sums of A x over the ranges K is split into). */
+/* Workspace bytes of nvfp4_lora_add: A x of every row. */
 int nvfp4_lora_workspace_bytes(int m, int adapters, int rank, int64_t k, size_t* bytes);
 
 /* M = 0..NVFP4_MAX_ROWS rows.  out may be y itself (same leading dimension); otherwise it overlaps

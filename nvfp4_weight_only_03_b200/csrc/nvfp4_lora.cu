@@ -8,14 +8,16 @@
 //   memory straight into mma.sync fragments, 16 bytes per lane and load: k (and the rank) may be
 //   permuted as long as both operands are, so a lane's 8 consecutive values serve as the 4 pairs
 //   of two MMAs, and no shared-memory pass is needed.  tcgen05 would have to stage them.
-// * First kernel: weights are the 16 rows of the MMA, x rows its 8 columns; 8 warps split a CTA's
-//   K range and CTAs split K further when there are few groups; sums over warps and ranges are
-//   formed in a fixed order.  Second kernel: T rows are the MMA's 16 rows and the columns are
-//   output channels, permuted so that a lane ends up with 8 consecutive ones.
-// * T stays fp32 between the kernels and enters the second MMA as two bf16 values (high and
-//   remainder), so it is carried to 2^-17; the only other rounding is the output's.
-// * The second kernel is launched while the first runs and has its weights and y in registers
+// * First kernel: weights are the 16 rows of the MMA, x rows its 8 columns; a cluster of up to 8 CTAs
+//   takes (group, 16 ranks), splits K over its warps and adds their sums in order through distributed
+//   shared memory.  Second kernel: output channels are the MMA's rows, permuted so that a lane ends
+//   up with 4 consecutive ones, and T rows its columns; a warp per (group, 32 channels) and many warps,
+//   so that others load while one multiplies.
+// * T leaves the first kernel as two bf16 values (high and remainder), scaled, so it is carried to
+//   2^-17; the only other rounding is the output's.
+// * The second kernel is launched while the first runs and has its groups, its first weights and y
 //   before it waits for T.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -30,11 +32,13 @@ namespace {
 using nvfp4_host::misaligned;
 using nvfp4_host::overlaps;
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kDownWarps = 8, kDownThreads = kDownWarps * 32;
+constexpr int kWarps = 4, kThreads = kWarps * 32;  // of the second kernel
 constexpr int kMaxM = NVFP4_MAX_ROWS;
 constexpr int kMaxRank = NVFP4_LORA_MAX_RANK;
 constexpr int kChunkN = kWarps * 32;  // output channels per item of the second kernel
-constexpr int kColTiles = 4;          // tiles of 8 rows that share one pass over A
+constexpr int kColTiles = 2;          // tiles of 8 rows that share one pass over A
+constexpr int kStepK = 128;           // k of one step of a warp: 16 rows of A, 4 KB
 
 struct Params {
     const uint16_t* a;
@@ -50,8 +54,8 @@ struct Params {
     int64_t ldy;
     uint16_t* out;
     int64_t ldo;
-    float* t;  // [splits][m][rank16] partial sums of T
-    int m, adapters, rank, rank16, n, k, splits, chunk;  // chunk: k of one split, % 256 == 0
+    uint16_t* t;  // T: [m][2][rank32] bf16, values and remainders
+    int m, adapters, rank, rank16, rank32, n, k;
 };
 
 // Rows by adapter: `row` lists the rows group by group; group g is adapter[g], its rows are
@@ -59,49 +63,77 @@ struct Params {
 struct Groups {
     int count;
     int16_t adapter[kMaxM + 1], rank[kMaxM + 1], first[kMaxM + 2], row[kMaxM];
-    int16_t lead[kMaxM];  // the first row with this row's adapter; kMaxM without one
-    int32_t index[kMaxM];
+    int16_t lead[kMaxM + 1];  // by leading row (kMaxM: none): its group's first place in `row`
+    __align__(16) int32_t index[kMaxM];
 };
 
-// Thread t places row t: it counts the rows of earlier groups, and the earlier ones of its own.
+// Thread t (< kMaxM) places row t.  One pass over the indexes gives it the set of rows with its
+// adapter, as bits: the first of them leads the group, and prefix sums over the leaders' sizes place
+// the groups.
 __device__ __forceinline__ void find_groups(const Params& p, Groups& g) {
-    const int t = threadIdx.x;
-    int a = -1;
+    static_assert(kThreads >= kMaxM && kDownThreads >= kMaxM, "a thread per row");
+    __shared__ int32_t warp_sum[kMaxM / 32], warp_lead[kMaxM / 32];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    int a = -2;  // not a row
     if (t < p.m) {
         a = p.index[t];
         if (a < 0 || a >= p.adapters) a = -1;
-        g.index[t] = a;
     }
-    if (t == 0) g.count = 0;
+    if (t < kMaxM) g.index[t] = a;
     __syncthreads();
-    int lead = kMaxM;
-    if (t < p.m) {
-        if (a >= 0)
-            for (int i = t; i >= 0; --i)
-                if (g.index[i] == a) lead = i;
-        g.lead[t] = (int16_t)lead;
-    }
-    __syncthreads();
-    if (t < p.m) {
-        int group = 0, start = 0, before = 0, size = 0;
-        for (int i = 0; i < p.m; ++i) {
-            const int l = g.lead[i];
-            group += l == i && l < lead;
-            start += l < lead;
-            before += l == lead && i < t;
-            size += l == lead;
-        }
-        g.row[start + before] = (int16_t)t;
-        if (before == 0) {
-            int r = 0;
-            if (a >= 0) r = p.ranks ? min(max(p.ranks[a], 0), p.rank) : p.rank;
-            g.adapter[group] = (int16_t)a;
-            g.rank[group] = (int16_t)r;
-            g.first[group] = (int16_t)start;
-            g.first[group + 1] = (int16_t)(start + size);  // the next group's start, if there is one
-            atomicAdd(&g.count, 1);
+    uint32_t same[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w * 32 >= p.m) break;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const int4 v = *reinterpret_cast<const int4*>(&g.index[w * 32 + i]);
+            same[w] |= (v.x == a ? 1u << i : 0u) | (v.y == a ? 2u << i : 0u) |
+                       (v.z == a ? 4u << i : 0u) | (v.w == a ? 8u << i : 0u);
         }
     }
+    int lead = kMaxM, before = 0, size = 0;
+#pragma unroll
+    for (int w = 3; w >= 0; --w) {
+        if (same[w]) lead = w * 32 + __ffs(same[w]) - 1;
+        size += __popc(same[w]);
+        if (w <= warp) before += __popc(w < warp ? same[w] : same[w] & ((1u << lane) - 1));
+    }
+    // the rows without an adapter come last, whatever their first row is
+    const bool leads = a >= 0 && lead == t;
+    int sum = leads ? size : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(~0u, sum, d);
+        if (lane >= d) sum += v;
+    }
+    const uint32_t vote = __ballot_sync(~0u, leads);
+    if (lane == 31 && t < kMaxM) {
+        warp_sum[warp] = sum;
+        warp_lead[warp] = __popc(vote);
+    }
+    __syncthreads();
+    int start = sum - (leads ? size : 0), group = __popc(vote & ((1u << lane) - 1)), all = 0,
+        leaders = 0;
+#pragma unroll
+    for (int w = 0; w < kMaxM / 32; ++w) {
+        if (w < warp) start += warp_sum[w], group += warp_lead[w];
+        all += warp_sum[w], leaders += warp_lead[w];
+    }
+    const bool first_bare = a == -1 && before == 0;
+    if (first_bare) start = all, group = leaders;
+    if (leads || first_bare) {
+        int r = 0;
+        if (a >= 0) r = p.ranks ? min(max(p.ranks[a], 0), p.rank) : p.rank;
+        g.adapter[group] = (int16_t)a;
+        g.rank[group] = (int16_t)r;
+        g.first[group] = (int16_t)start;
+        g.first[group + 1] = (int16_t)(start + size);  // the next group's start, if there is one
+        g.lead[a >= 0 ? t : kMaxM] = (int16_t)start;
+    }
+    if (t == 0) g.count = leaders + (all < p.m);
+    __syncthreads();
+    if (t < p.m) g.row[g.lead[a >= 0 ? lead : kMaxM] + before] = (int16_t)t;
     __syncthreads();
 }
 
@@ -123,130 +155,135 @@ __device__ __forceinline__ uint4 load_stream(const uint16_t* p) {  // read once
 }
 
 // ---- T = A x -----------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads, 2) nvfp4_lora_down_kernel(const Params p) {
+__global__ void __launch_bounds__(kDownThreads, 3) nvfp4_lora_down_kernel(const Params p) {
     __shared__ Groups g;
-    __shared__ __align__(16) float part[kWarps][kColTiles][16][8];
+    __shared__ __align__(16) float part[kDownWarps][kColTiles][16][8];
+    __shared__ __align__(16) float sum[kColTiles * 128];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const auto cluster = cooperative_groups::this_cluster();
+    const int ctas = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
     find_groups(p, g);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
     const int blocks = p.rank16 / 16;
-    const int items = g.count * blocks * p.splits;
-    constexpr int kUnroll = 4;
+    const int item = blockIdx.x / ctas, blk = item % blocks, gi = item / blocks;
+    if (gi >= g.count) return;  // (the whole cluster)
+    const int rank = g.rank[gi], r0 = blk * 16;
+    if (r0 >= rank) return;
+    const int first = g.first[gi], rows = g.first[gi + 1] - first;
+    const uint16_t* const a = p.a + g.adapter[gi] * p.a_stride;
+    const float scale = p.scales[g.adapter[gi]];
+    // this lane's two rank rows; a row past the rank counts as zeros and is not read
+    const bool on0 = r0 + gr < rank, on1 = r0 + gr + 8 < rank;
+    const uint16_t* const a0 = a + (int64_t)(r0 + gr) * p.a_ld;
+    const uint16_t* const a1 = a0 + 8 * p.a_ld;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int split = it % p.splits, gb = it / p.splits, blk = gb % blocks, gi = gb / blocks;
-        const int rank = g.rank[gi], r0 = blk * 16;
-        if (r0 >= rank) continue;
-        const int first = g.first[gi], rows = g.first[gi + 1] - first;
-        const uint16_t* const a = p.a + g.adapter[gi] * p.a_stride;
-        // this lane's two rank rows; a row past the rank counts as zeros and is not read
-        const bool on0 = r0 + gr < rank, on1 = r0 + gr + 8 < rank;
-        const uint16_t* const a0 = a + (int64_t)(r0 + gr) * p.a_ld;
-        const uint16_t* const a1 = a0 + 8 * p.a_ld;
-        const int end = min((split + 1) * p.chunk, p.k);
-        for (int c0 = 0; c0 < rows; c0 += 8 * kColTiles) {
-            const int tiles = min((rows - c0 + 7) / 8, kColTiles);
-            const uint16_t* xr[kColTiles];
+    for (int c0 = 0; c0 < rows; c0 += 8 * kColTiles) {
+        const int tiles = min((rows - c0 + 7) / 8, kColTiles);
+        const uint16_t* xr[kColTiles];
 #pragma unroll
-            for (int c = 0; c < kColTiles; ++c) {
-                const int i = c0 + c * 8 + gr;
-                xr[c] = i < rows ? p.x + (int64_t)g.row[first + i] * p.ldx : nullptr;
-            }
-            float acc[kColTiles][4];
+        for (int c = 0; c < kColTiles; ++c) {
+            const int i = c0 + c * 8 + gr;
+            xr[c] = i < rows ? p.x + (int64_t)g.row[first + i] * p.ldx : nullptr;
+        }
+        float acc[kColTiles][4];
 #pragma unroll
-            for (int c = 0; c < kColTiles; ++c)
+        for (int c = 0; c < kColTiles; ++c)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
-            for (int k0 = split * p.chunk + warp * 32 + t * 8; k0 - t * 8 < end;
-                 k0 += kWarps * 32 * kUnroll) {
-                uint4 w0[kUnroll], w1[kUnroll], xv[kUnroll];
+            for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+        const int stride = ctas * kDownWarps * kStepK;
+        for (int k0 = (cta * kDownWarps + warp) * kStepK; k0 < p.k; k0 += stride) {
+            uint4 w0[4], w1[4], x[4];
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int kk = k0 + u * kWarps * 32;
-                    w0[u] = on0 && kk < end ? load_stream(a0 + kk) : zero;
-                    w1[u] = on1 && kk < end ? load_stream(a1 + kk) : zero;
-                }
-#pragma unroll
-                for (int c = 0; c < kColTiles; ++c) {
-                    if (c >= tiles) break;
-#pragma unroll
-                    for (int u = 0; u < kUnroll; ++u) {
-                        const int kk = k0 + u * kWarps * 32;
-                        xv[u] = xr[c] && kk < end
-                                    ? __ldg(reinterpret_cast<const uint4*>(xr[c] + kk))
-                                    : zero;
-                    }
-#pragma unroll
-                    for (int u = 0; u < kUnroll; ++u) {
-                        mma_bf16(acc[c], w0[u].x, w1[u].x, w0[u].y, w1[u].y, xv[u].x, xv[u].y);
-                        mma_bf16(acc[c], w0[u].z, w1[u].z, w0[u].w, w1[u].w, xv[u].z, xv[u].w);
-                    }
-                }
+            for (int u = 0; u < 4; ++u) {
+                const int k = k0 + u * 32 + t * 8;
+                w0[u] = on0 && k < p.k ? load_stream(a0 + k) : zero;
+                w1[u] = on1 && k < p.k ? load_stream(a1 + k) : zero;
             }
 #pragma unroll
             for (int c = 0; c < kColTiles; ++c) {
                 if (c >= tiles) break;
-                *reinterpret_cast<float2*>(&part[warp][c][gr][2 * t]) =
-                    make_float2(acc[c][0], acc[c][1]);
-                *reinterpret_cast<float2*>(&part[warp][c][gr + 8][2 * t]) =
-                    make_float2(acc[c][2], acc[c][3]);
-            }
-            __syncthreads();
-            for (int i = threadIdx.x; i < tiles * 128; i += kThreads) {
-                const int c = i >> 7, r = i & 15, col = (i >> 4) & 7;
-                if (c0 + c * 8 + col < rows) {
-                    float s = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) s += part[w][c][r][col];
-                    p.t[((int64_t)split * p.m + g.row[first + c0 + c * 8 + col]) * p.rank16 + r0 +
-                        r] = s;
+                for (int u = 0; u < 4; ++u) {
+                    const int k = k0 + u * 32 + t * 8;
+                    x[u] = xr[c] && k < p.k ? __ldg(reinterpret_cast<const uint4*>(xr[c] + k))
+                                            : zero;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    mma_bf16(acc[c], w0[u].x, w1[u].x, w0[u].y, w1[u].y, x[u].x, x[u].y);
+                    mma_bf16(acc[c], w0[u].z, w1[u].z, w0[u].w, w1[u].w, x[u].z, x[u].w);
                 }
             }
-            __syncthreads();
         }
+#pragma unroll
+        for (int c = 0; c < kColTiles; ++c) {
+            if (c >= tiles) break;
+            *reinterpret_cast<float2*>(&part[warp][c][gr][2 * t]) =
+                make_float2(acc[c][0], acc[c][1]);
+            *reinterpret_cast<float2*>(&part[warp][c][gr + 8][2 * t]) =
+                make_float2(acc[c][2], acc[c][3]);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < tiles * 128; i += kDownThreads) {
+            const float* const from = &part[0][0][0][0] + i;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kDownWarps; ++w) v += from[w * kColTiles * 128];
+            sum[i] = v;  // [tile][rank][row]
+        }
+        cluster.sync();
+        if (cta == 0) {
+            for (int i = threadIdx.x; i < tiles * 128; i += kDownThreads) {
+                const int r = i & 15, col = (i >> 4) & 7, c = i >> 7;
+                const int at = c * 128 + r * 8 + col;  // neighbours write neighbouring ranks
+                float v = 0.f;
+                for (int q = 0; q < ctas; ++q) v += cluster.map_shared_rank(sum, q)[at];
+                const int row = c0 + c * 8 + col;
+                if (row < rows) {
+                    v = r0 + r < rank ? v * scale : 0.f;
+                    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+                    const float rest = v - __bfloat162float(h);
+                    uint16_t* const to =
+                        p.t + (int64_t)g.row[first + row] * 2 * p.rank32 + r0 + r;
+                    to[0] = __bfloat16_as_ushort(h);
+                    to[p.rank32] = __bfloat16_as_ushort(
+                        __float2bfloat16_rn(isfinite(__bfloat162float(h)) ? rest : 0.f));
+                }
+            }
+        }
+        cluster.sync();  // before the sums are written again, or their CTA is gone
     }
 }
 
 // ---- out = y + B T -----------------------------------------------------------------------
 template <int STEPS>  // 32 ranks each
-__global__ void __launch_bounds__(kThreads, STEPS > 2 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, STEPS > 2 ? 3 : STEPS > 1 ? 5 : 6)
     nvfp4_lora_up_kernel(const Params p) {
     __shared__ Groups g;
-    constexpr int kR = STEPS * 32, kPad = kR + 8;  // a row's stride keeps 16-byte reads apart
-    extern __shared__ __align__(16) uint16_t t_smem[];
-    uint16_t* const hi = t_smem;                     // [m][kPad]
-    uint16_t* const lo = t_smem + p.m * kPad;
     find_groups(p, g);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
     const int chunks = (p.n + kChunkN - 1) / kChunkN;
-    const int64_t items = (int64_t)g.count * chunks;
-    const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
-    int loaded = -1;
-    bool waited = false;
+    const int items = g.count * chunks;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int64_t it = i0; it < i1; ++it) {
-        const int gi = (int)(it / chunks), n0 = (int)(it % chunks) * kChunkN + warp * 32;
+    bool waited = false;
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+        const int gi = it / chunks, n0 = (it - gi * chunks) * kChunkN + warp * 32;
         const int rank = g.rank[gi], first = g.first[gi], rows = g.first[gi + 1] - first;
-        // column c of tile j is channel n0 + (c / 2) * 8 + 2 j + c % 2: tile j's columns 2t, 2t+1
-        // are a lane's channels n0 + 8 t + 2 j + {0, 1}
-        uint4 w[4][STEPS];
-        const uint16_t* const b = p.b + (int64_t)max((int)g.adapter[gi], 0) * p.b_stride;
+        // row c + 8 h (c < 8) of tile j is channel n0 + 4 c + 2 j + h: a lane's rows c = gr are its
+        // channels n0 + 4 gr .. + 3
+        uint4 w[2][2][STEPS];
+        const int n = n0 + gr * 4;
+        const uint16_t* const b = p.b + (int64_t)max((int)g.adapter[gi], 0) * p.b_stride +
+                                  (int64_t)n * p.b_ld + t * 8;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + (gr >> 1) * 8 + 2 * j + (gr & 1);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int r = s * 32 + t * 8;
-                w[j][s] = n < p.n && r < rank ? load_stream(b + (int64_t)n * p.b_ld + r) : zero;
-            }
-        }
-        const int n_out = n0 + t * 8;
-        auto y_at = [&](int i) {
-            return i < rows && n_out < p.n
-                       ? *reinterpret_cast<const uint4*>(p.y + (int64_t)g.row[first + i] * p.ldy + n_out)
-                       : zero;
-        };
-        uint4 y0 = y_at(gr), y1 = y_at(gr + 8);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+                    w[j][h][s] = n < p.n && s * 32 + t * 8 < rank
+                                     ? load_stream(b + (2 * j + h) * p.b_ld + s * 32)
+                                     : zero;
         if (rank % 8) {  // ranks past the adapter's own within a lane's 8: zeros, whatever is there
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
@@ -254,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, STEPS > 2 ? 1 : 2)
                 if (left > 0 && left < 8) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint32_t* const v = &w[j][s].x;
+                        uint32_t* const v = &w[j >> 1][j & 1][s].x;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             v[e] &= (2 * e < left ? 0xffffu : 0u) |
@@ -263,95 +300,75 @@ __global__ void __launch_bounds__(kThreads, STEPS > 2 ? 1 : 2)
                 }
             }
         }
-        if (!waited) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            waited = true;
-        }
-        if (gi != loaded) {
-            __syncthreads();
-            const float scale = rank ? p.scales[g.adapter[gi]] : 0.f;
-            for (int i = threadIdx.x; i < rows * kR; i += kThreads) {
-                const int q = i / kR, r = i % kR;
-                float v = 0.f;
-                if (r < rank) {
-                    const float* src = p.t + (int64_t)g.row[first + q] * p.rank16 + r;
-                    for (int s = 0; s < p.splits; ++s) v += __ldcg(src + (int64_t)s * p.m * p.rank16);
-                    v *= scale;
-                }
-                const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                const float rest = v - __bfloat162float(h);
-                hi[q * kPad + r] = __bfloat16_as_ushort(h);
-                lo[q * kPad + r] = __bfloat16_as_ushort(
-                    __float2bfloat16_rn(isfinite(__bfloat162float(h)) ? rest : 0.f));
-            }
-            loaded = gi;
-            __syncthreads();
-        }
-        for (int m0 = 0; m0 < rows; m0 += 16) {
-            if (m0) y0 = y_at(m0 + gr), y1 = y_at(m0 + gr + 8);
-            float acc[4][4];
+        for (int m0 = 0; m0 < rows; m0 += 8) {
+            // a lane multiplies T of row gr and writes rows 2t and 2t + 1
+            const int left = rows - m0;
+            const int mul_row = gr < left ? g.row[first + m0 + gr] : 0;
+            int row[2];
+            uint2 y[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int e = 0; e < 2; ++e) {
+                row[e] = 2 * t + e < left && n < p.n ? g.row[first + m0 + 2 * t + e] : -1;
+                y[e] = make_uint2(0, 0);
+                if (row[e] >= 0)
+                    y[e] = *reinterpret_cast<const uint2*>(p.y + (int64_t)row[e] * p.ldy + n);
+            }
+            if (!waited) {  // T, from here on
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                waited = true;
+            }
+            float acc[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-            const bool on0 = m0 + gr < rows, on1 = m0 + gr + 8 < rows;
+            const uint16_t* const from = p.t + (int64_t)mul_row * 2 * p.rank32 + t * 8;
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                if (s * 32 >= rank) break;
+                // (16 ranks that the adapter does not reach were not written)
+                const bool live = gr < left && s * 32 + t * 8 < ((rank + 15) & ~15);
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    const uint16_t* const src = (part ? lo : hi) + (m0 + gr) * kPad + s * 32 + t * 8;
-                    const uint4 u = on0 ? *reinterpret_cast<const uint4*>(src) : zero;
-                    const uint4 v = on1 ? *reinterpret_cast<const uint4*>(src + 8 * kPad) : zero;
+                for (int half = 0; half < 2; ++half) {
+                    const uint4 v = live ? *reinterpret_cast<const uint4*>(
+                                               from + half * p.rank32 + s * 32)
+                                         : zero;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mma_bf16(acc[j], u.x, v.x, u.y, v.y, w[j][s].x, w[j][s].y);
-                        mma_bf16(acc[j], u.z, v.z, u.w, v.w, w[j][s].z, w[j][s].w);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 c = w[j][0][s], d = w[j][1][s];
+                        mma_bf16(acc[j], c.x, d.x, c.y, d.y, v.x, v.y);
+                        mma_bf16(acc[j], c.z, d.z, c.w, d.w, v.z, v.w);
                     }
                 }
             }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!(half ? on1 : on0) || n_out >= p.n) continue;
-                uint16_t* const dst =
-                    p.out + (int64_t)g.row[first + m0 + gr + half * 8] * p.ldo + n_out;
-                uint4 o = half ? y1 : y0;
+            for (int e = 0; e < 2; ++e) {
+                if (row[e] < 0) continue;
                 if (rank) {
-                    uint32_t* const v = &o.x;
+                    uint32_t* const v = &y[e].x;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float e0 = __uint_as_float(v[j] << 16) + acc[j][2 * half];
-                        const float e1 = __uint_as_float(v[j] & 0xffff0000u) + acc[j][2 * half + 1];
+                    for (int j = 0; j < 2; ++j) {  // channels 2j and 2j + 1
+                        const float e0 = __uint_as_float(v[j] << 16) + acc[j][e];
+                        const float e1 = __uint_as_float(v[j] & 0xffff0000u) + acc[j][2 + e];
                         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[j]) : "f"(e1), "f"(e0));
                     }
                 }
-                *reinterpret_cast<uint4*>(dst) = o;
+                *reinterpret_cast<uint2*>(p.out + (int64_t)row[e] * p.ldo + n) = y[e];
             }
         }
     }
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-struct Split {
-    int splits, chunk;
-};
-
-// K ranges: enough items of (group, 16 ranks, range) for three per SM, each range a multiple of
-// the 256 k that a CTA's warps take per step.  The group count is on the device; its bound is not.
-Split choose_split(int m, int adapters, int rank, int64_t k, int sms) {
-    const int64_t groups = m < adapters ? m : adapters;
-    const int64_t steps = (k + 255) / 256;
-    const int64_t per = groups * ((rank + 15) / 16);
-    int64_t want = (3 * sms + per - 1) / (per > 0 ? per : 1);
-    if (want > steps) want = steps;
-    if (want < 1) want = 1;
-    const int64_t each = (steps + want - 1) / want;
-    Split s;
-    s.chunk = (int)(each * 256);
-    s.splits = (int)((steps + each - 1) / each);
-    if (s.splits < 1) s.splits = 1;
-    return s;
+// CTAs of a cluster: enough items of (group, 16 ranks, part of K) for two per SM, no more than K has
+// steps for.  The group count is on the device; its bound is not.
+int choose_cluster(int m, int adapters, int rank, int64_t k, int sms) {
+    const int64_t items = (int64_t)(m < adapters ? m : adapters) * ((rank + 15) / 16);
+    int ctas = 1;
+    while (ctas < 8 && items * ctas < 2 * sms && 2 * ctas * kDownWarps * kStepK / 2 < k) ctas *= 2;
+    return ctas;
 }
+
+size_t t_bytes(int m, int rank) { return (size_t)m * 2 * ((rank + 31) / 32 * 32) * 2; }
 
 int check_shape(int m, int adapters, int rank, int64_t k) {
     if (m < 0 || m > NVFP4_MAX_ROWS) return NVFP4_ERR_ROWS;
@@ -363,26 +380,12 @@ int check_shape(int m, int adapters, int rank, int64_t k) {
 
 template <int STEPS>
 int launch_up(const Params& p, int sms, bool after_down, cudaStream_t stream) {
-    const size_t smem = (size_t)2 * p.m * (STEPS * 32 + 8) * 2;
-    static bool ready[64];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !ready[dev]) {
-        if (cudaFuncSetAttribute(nvfp4_lora_up_kernel<STEPS>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 2 * kMaxM * (STEPS * 32 + 8) * 2) != cudaSuccess) {
-            cudaGetLastError();
-            return NVFP4_ERR_LAUNCH;
-        }
-        ready[dev] = true;
-    }
     const int64_t groups = (p.m < p.adapters ? p.m : p.adapters) + 1;
     const int64_t items = groups * ((p.n + kChunkN - 1) / kChunkN);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)(items < 2 * sms ? items : 2 * sms));
+    cfg.gridDim = dim3((unsigned)(items < 6 * sms ? items : 6 * sms));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -410,8 +413,7 @@ int nvfp4_lora_workspace_bytes(int m, int adapters, int rank, int64_t k, size_t*
     nvfp4_host::EncodeFn encode;
     st = nvfp4_host::device(&dev, &sms, &encode);
     if (st != NVFP4_OK) return st;
-    const Split s = choose_split(m, adapters, rank, k, sms);
-    *bytes = (size_t)s.splits * m * ((rank + 15) / 16 * 16) * 4;
+    *bytes = t_bytes(m, rank);
     return NVFP4_OK;
 }
 
@@ -442,7 +444,6 @@ int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const v
     nvfp4_host::EncodeFn encode;
     st = nvfp4_host::device(&dev, &sms, &encode);
     if (st != NVFP4_OK) return st;
-    const Split s = choose_split(m, l.adapters, l.rank, k, sms);
     Params p;
     memset(&p, 0, sizeof(p));
     p.a = static_cast<const uint16_t*>(l.a);
@@ -466,18 +467,30 @@ int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const v
     p.rank16 = (l.rank + 15) / 16 * 16;
     p.n = (int)n;
     p.k = (int)k;
-    p.splits = s.splits;
-    p.chunk = s.chunk;
-    const size_t need = (size_t)s.splits * m * p.rank16 * 4;
+    p.rank32 = (l.rank + 31) / 32 * 32;
+    const size_t need = t_bytes(m, l.rank);
     if (need && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
         return NVFP4_ERR_WORKSPACE;
-    p.t = static_cast<float*>(workspace);
+    p.t = static_cast<uint16_t*>(workspace);
     if (any) {
         const int64_t groups = m < l.adapters ? m : l.adapters;
-        const int64_t items = groups * (p.rank16 / 16) * s.splits;
-        const int grid = (int)(items < 4 * sms ? items : 4 * sms);
-        nvfp4_lora_down_kernel<<<grid, kThreads, 0, stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_LAUNCH;
+        const int ctas = choose_cluster(m, l.adapters, l.rank, k, sms);
+        cudaLaunchConfig_t cfg;
+        memset(&cfg, 0, sizeof(cfg));
+        cfg.gridDim = dim3((unsigned)(groups * (p.rank16 / 16) * ctas));
+        cfg.blockDim = dim3(kDownThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = ctas;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, nvfp4_lora_down_kernel, p) != cudaSuccess) {
+            cudaGetLastError();
+            return NVFP4_ERR_LAUNCH;
+        }
     }
     if (p.rank <= 32) return launch_up<1>(p, sms, any, stream);
     if (p.rank <= 64) return launch_up<2>(p, sms, any, stream);
