@@ -500,9 +500,10 @@ typedef struct {
  * that its split of the keys cuts: 39 MB at dim 256 on a 148-SM B200). */
 int nvfp4_paged_attn_workspace_bytes(int dim, size_t* bytes);
 
-/* workspace: 16-byte aligned, the above bytes, zero-filled before first use (its first word is
- * the error word of nvfp4_workspace_error: 5..9, a bounded wait gave up and the results are
- * invalid).  Calls that may run at the same time need different workspaces.
+/* workspace: 16-byte aligned, the above bytes, zero-filled before first use; the words that have to
+ * be zero are so again after every call that completes.  Its first word is the error word of
+ * nvfp4_workspace_error (5..10: a bounded wait gave up and the results are invalid).  Calls that may
+ * run at the same time need different workspaces.
  * Errors: NVFP4_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _WORKSPACE, _ARCH, _LAUNCH. */
 int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cache,
                      void* workspace, size_t workspace_bytes, cudaStream_t stream);

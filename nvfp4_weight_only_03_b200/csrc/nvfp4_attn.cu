@@ -14,8 +14,9 @@
 // * Work: units of TK keys of one (request, kv head, row tile).  All units in order are cut into
 //   equal ranges, one per CTA (one CTA per SM), from the lengths in device memory: the host knows
 //   none of them, so a captured call serves every later length.  A tile that a range boundary
-//   cuts leaves (max, sum, O) in the workspace, and a second kernel joins the parts in order.
-//   No atomics: results are the same in every run.
+//   cuts leaves (max, sum, O) in the workspace, and a second kernel joins the parts in order (or,
+//   where all rows are few, the CTA that is last to leave its part).  Results are the same in every
+//   run.
 // * One pass over the cache: S = Q K^T in tensor memory, one thread per row keeps the running
 //   maximum and sum, P goes back to tensor memory as the A operand of O += P V.  O stays in tensor
 //   memory; it is rescaled only when a row's maximum rose by more than 2^8 (P is then at most
@@ -64,7 +65,7 @@ struct Small {
     int64_t sums[20];
     int start[2][12];  // a Cursor: where the range begins; then, by turns, the softmax's next tile
     uint32_t tmem;
-    int stop;
+    int stop, last;
     float row_max[2][kRows];  // a unit's reference maximum: [its parity][row]
     float row_sum[2][kRows];  // a row tile's sum of weights: [warpgroup][row]
     // biased exponents of the 8-bit Q rows' scales.  Q may be two row tiles ahead of the softmax.
@@ -145,6 +146,8 @@ struct Params {
     float c;           // scale * k_scale * log2(e)
     float v_scale;
     int32_t* error;
+    int join_here;     // rows are few: the last CTA of a cut row tile joins its parts itself
+    int32_t* arrived;  // [grid]: parts of CTA i's cut row tile written so far; zero between calls
     Cut* cuts;         // [grid]
     float2* part_ml;   // [grid][2][128]: maximum (log2 domain) and sum
     float* part_o;     // [grid][2][128][D]
@@ -367,11 +370,68 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
     return g;
 }
 
+// ---- joining the parts of a cut row tile: a warp per row, the parts in order -----------------
+// Part 0 lies with its CTA's cut at the end, the others with their cuts at the start.
+template <int D>
+__device__ __noinline__ void join_rows(const Params& p, int owner, const Cut& cut, int row, int step) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kPer = D / 32;
+    for (; row < cut.rows; row += step) {
+        auto at = [&](int i) { return ((int64_t)(owner + i) * 2 + (i == 0)) * kRows + row; };
+        float top = -INFINITY;
+        for (int i = lane; i < cut.parts; i += 32) top = fmaxf(top, __ldcg(&p.part_ml[at(i)].x));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        float acc[kPer], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+        if (top > -INFINITY) {
+#pragma unroll 4
+            for (int i = 0; i < cut.parts; ++i) {
+                const int64_t a = at(i);
+                const float2 ml = __ldcg(&p.part_ml[a]);
+                const float w = exp2_approx(ml.x - top);
+                const float2* const src =
+                    reinterpret_cast<const float2*>(p.part_o + a * D + lane * kPer);
+                sum = fmaf(w, ml.y, sum);
+                // a part that saw no key has a weight of zero and zeros to weigh
+#pragma unroll
+                for (int e = 0; e < kPer; e += 2) {
+                    const float2 v = __ldcg(src + e / 2);
+                    acc[e] = fmaf(w, v.x, acc[e]);
+                    acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+                }
+            }
+        }
+        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+        const int tok = (int)div_by(cut.row0 + row, p.by_group);
+        uint16_t* const out =
+            p.o + (int64_t)(cut.token0 + tok) * p.ldo +
+            (int64_t)(cut.head * p.group + cut.row0 + row - tok * p.group) * p.o_head_stride +
+            lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2)
+            *reinterpret_cast<uint32_t*>(out + e) = pack16(false, acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+constexpr int kJoinWarps = 8, kJoinSplit = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_attn_join_kernel(const __grid_constant__ Params p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int owner = blockIdx.x / kJoinSplit;
+    const Cut cut = p.cuts[owner];
+    if (cut.parts <= 0) return;
+    join_rows<D>(p, owner, cut, blockIdx.x % kJoinSplit * kJoinWarps + (threadIdx.x >> 5),
+                 kJoinSplit * kJoinWarps);
+}
+
 // ---- the kernel --------------------------------------------------------------------------
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
-    nvfp4_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_k,
+    nvfp4_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<D, F8>;
     constexpr int TK = C::TK, NK = C::NK, NV = C::NV, NR = C::NR;
@@ -999,20 +1059,38 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
             values_at += cnt;
-            left -= cur.lead + cnt;
             ++item;
-            if (tid == 0 && cur.u == 0 && !whole) {  // the last row tile goes on in later CTAs
-                const int64_t x = range.end - cnt + cur.n - 1;  // where its last unit counts
-                const int64_t e = div64((x + 1) * range.ctas + range.total - 1, range.total) - 1;
+            if (!whole && (cur.u == 0 || p.join_here)) {
+                // the CTA with unit x (as the ranges count) of this row tile's 0 .. n - 1 from `zero`
+                const int64_t zero = cur.u == 0 ? range.end - cnt : range.begin - cur.u;
+                auto cta_of = [&](int64_t x) {
+                    const int64_t e = div64((x + 1) * range.ctas + range.total - 1, range.total) - 1;
+                    return (int)min(max(e, (int64_t)0), (int64_t)range.ctas - 1);
+                };
+                const int owner = cur.u == 0 ? (int)blockIdx.x : cta_of(zero);
                 Cut cut;
                 memset(&cut, 0, sizeof(cut));
-                cut.parts = (int)min(e - blockIdx.x + 1, (int64_t)(range.ctas - blockIdx.x));
+                cut.parts = cta_of(zero + cur.n - 1) - owner + 1;
                 cut.token0 = cur.q.token0;
                 cut.row0 = row0;
                 cut.rows = rows;
                 cut.head = cur.h;
-                p.cuts[blockIdx.x] = cut;
+                if (!p.join_here) {  // the last row tile goes on in later CTAs
+                    if (tid == 0) p.cuts[blockIdx.x] = cut;
+                } else {
+                    __threadfence();
+                    bar_sync(9, kSoftmaxWarps * 32);
+                    if (tid == 0)
+                        sm.last = atomicAdd(&p.arrived[owner], 1) == cut.parts - 1;
+                    bar_sync(9, kSoftmaxWarps * 32);
+                    if (sm.last) {
+                        __threadfence();
+                        join_rows<D>(p, owner, cut, warp, kSoftmaxWarps);
+                        if (tid == 0) p.arrived[owner] = 0;
+                    }
+                }
             }
+            left -= cur.lead + cnt;
             cur = *reinterpret_cast<const Cursor<TK>*>(sm.start[item & 1]);
         }
         if (!ok) code = 9;
@@ -1031,61 +1109,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     }
 }
 
-// ---- joining the parts of cut row tiles: a warp per row, the parts in order ----------------
-constexpr int kJoinWarps = 8, kJoinSplit = 4;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_attn_join_kernel(const Params p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int owner = blockIdx.x / kJoinSplit;
-    const Cut cut = p.cuts[owner];
-    if (cut.parts <= 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kPer = D / 32;
-    for (int row = (blockIdx.x % kJoinSplit) * kJoinWarps + warp; row < cut.rows;
-         row += kJoinSplit * kJoinWarps) {
-        // part 0 lies with its CTA's cut at the end, the others with their cuts at the start
-        auto at = [&](int i) { return ((int64_t)(owner + i) * 2 + (i == 0)) * kRows + row; };
-        float top = -INFINITY;
-        for (int i = lane; i < cut.parts; i += 32) top = fmaxf(top, p.part_ml[at(i)].x);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        float acc[kPer], sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-        if (top > -INFINITY) {
-#pragma unroll 4
-            for (int i = 0; i < cut.parts; ++i) {
-                const int64_t a = at(i);
-                const float2 ml = p.part_ml[a];
-                const float w = exp2_approx(ml.x - top);
-                const float* const src = p.part_o + a * D + lane * kPer;
-                sum = fmaf(w, ml.y, sum);
-                // a part that saw no key has a weight of zero and zeros to weigh
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, src[e], acc[e]);
-            }
-        }
-        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-        const int grow = cut.row0 + row, tok = grow / p.group;
-        uint16_t* const out = p.o + (int64_t)(cut.token0 + tok) * p.ldo +
-                              (int64_t)(cut.head * p.group + grow - tok * p.group) * p.o_head_stride +
-                              lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2)
-            *reinterpret_cast<uint32_t*>(out + e) = pack16(false, acc[e] * inv, acc[e + 1] * inv);
-    }
-}
-
 // ---- host --------------------------------------------------------------------------------
 
 struct Layout {
-    size_t cuts, ml, o, total;
+    size_t arrived, cuts, ml, o, total;
 };
 
 Layout workspace_layout(int sms, int dim) {
     Layout w;
-    w.cuts = 512;
+    w.arrived = 512;
+    w.cuts = w.arrived + ((size_t)sms * 4 + 255) / 256 * 256;
     w.ml = w.cuts + (size_t)sms * sizeof(Cut);
     w.ml = (w.ml + 255) / 256 * 256;
     w.o = w.ml + (size_t)sms * 2 * kRows * sizeof(float2);
@@ -1119,6 +1152,7 @@ int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int 
     p.min_units = 1;
     nvfp4_attn_kernel<D, F8><<<grid, C::kThreads, C::kSmem, stream>>>(p, mk, mv);
     if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_LAUNCH;
+    if (p.join_here) return NVFP4_OK;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(grid * kJoinSplit);
@@ -1242,6 +1276,10 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     if (!(p.c >= 1.1754944e-38f) || isinf(p.c)) return NVFP4_ERR_SHAPE;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     p.error = reinterpret_cast<int32_t*>(ws);
+    p.arrived = reinterpret_cast<int32_t*>(ws + w.arrived);
+    // few rows at all: joining takes a CTA a microsecond or two, less than another launch does (with
+    // 8 x 6 rows in 37 parts it would be 12)
+    p.join_here = a.tokens * p.group <= 16;
     p.cuts = reinterpret_cast<Cut*>(ws + w.cuts);
     p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
     p.part_o = reinterpret_cast<float*>(ws + w.o);

@@ -169,18 +169,23 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
 }
 
 // ------------------------------------------------------------------------------------------
-// Append.  One 16-byte vector of 8 elements per thread and step, K and V in one launch; a
-// warp's lanes hold consecutive vectors of a token's row, so loads and stores are whole
-// sectors.  HBM bound, 4 bytes of traffic per element (3 with an 8-bit cache).  An e4m3
-// element is e4m3_rn(x / scale), saturated at 448: a true division, so the code is that of the
-// rounded quotient whatever the scale.
+// Append.  A warp per token and side (K or V); a lane moves pieces of 16 bytes of the cache (8 bf16
+// values, or 16 codes), so loads and stores are whole sectors and the slot is looked up once per
+// row.  HBM bound, 4 bytes of traffic per value (3 with an 8-bit cache).
+//
+// An e4m3 code is e4m3_rn(x / scale) of the fp32 quotient, saturated at 448.  The quotient is formed as
+// x * (1 / scale), which is off by at most 2 of its last places (three roundings of half a place):
+// that can change the code only next to a border between codes, in fp32 a value whose last 20
+// mantissa bits are 2^19 (e4m3 keeps 3 of the 23), and only from 2^-6 up, where codes keep three bits
+// whatever the exponent.  Values within 4 places of a border, or below 2^-6 but not zero, are
+// divided: one in 10^5 of the first kind.  (A division is ten instructions and was the bound.)
 constexpr int kAppendThreads = 256;
 
 struct AppendParams {
     const uint16_t* src[2];
     int64_t ld[2], head_stride[2];
     uint8_t* cache[2];
-    float scale[2];
+    float scale[2], inverse[2];  // inverse: 0 where 1 / scale is not a normal number
     const int32_t* slots;
     int64_t tokens, blocks, block_stride, slot_stride, cache_head_stride;
     int heads, dim, block;
@@ -189,38 +194,68 @@ struct AppendParams {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, float scale) {
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(r)
-        : "f"(__fdiv_rn(bf16_hi(w), scale)), "f"(__fdiv_rn(bf16_lo(w), scale)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Whether x * (1 / scale) may round to another code than x / scale.
+__device__ __forceinline__ bool near_border(float q) {
+    const uint32_t u = __float_as_uint(q) & 0x7fffffffu;
+    return (u & 0xfffffu) - 0x7fffcu <= 8u || (u < 0x3c800000u && u != 0);
+}
+
+// 8 bf16 values -> 8 codes.
+__device__ __forceinline__ uint2 quantise(uint4 v, float scale, float inverse) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float q[8];
+    bool again = inverse == 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = (i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) * inverse;
+        again |= near_border(q[i]);
+    }
+    if (again) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = __fdiv_rn(i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]), scale);
+    }
+    return make_uint2(e4m3_pair(q[0], q[1]) | e4m3_pair(q[2], q[3]) << 16,
+                      e4m3_pair(q[4], q[5]) | e4m3_pair(q[6], q[7]) << 16);
 }
 
 template <bool F8>
 __global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const AppendParams p) {
-    const int vecs = p.dim / 8, row = p.heads * vecs;  // vectors of a token's K (or V)
-    const int64_t all = p.tokens * row * 2;
-    const int64_t stride = (int64_t)gridDim.x * kAppendThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x; i < all; i += stride) {
-        const int64_t t = i / (2 * row);
-        const int in = (int)(i - t * 2 * row), which = in >= row;
-        const int j = in - which * row, h = j / vecs, c = j - h * vecs;
+    constexpr int kPiece = F8 ? 16 : 8;  // values
+    const int lane = threadIdx.x & 31;
+    const int per = p.dim / kPiece, pieces = p.heads * per;  // of a head, of a row
+    const int log_per = 31 - __clz(per);
+    const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
+    const int64_t me = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t i = me; i < 2 * p.tokens; i += warps) {
+        const int64_t t = i >> 1;
+        const int which = (int)(i & 1);
         const int32_t slot = p.slots[t];
-        const int64_t page = slot / p.block;
+        const int32_t page = slot / p.block;
         if (slot < 0 || page >= p.blocks) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(
-            p.src[which] + t * p.ld[which] + h * p.head_stride[which] + c * 8);
-        const int64_t at = page * p.block_stride + (int64_t)(slot - (int32_t)page * p.block) * p.slot_stride +
-                           h * p.cache_head_stride + c * 8;
-        if (F8) {
-            const float s = p.scale[which];
-            uint2 o;
-            o.x = e4m3_pair(v.x, s) | e4m3_pair(v.y, s) << 16;
-            o.y = e4m3_pair(v.z, s) | e4m3_pair(v.w, s) << 16;
-            *reinterpret_cast<uint2*>(p.cache[which] + at) = o;
-        } else {
-            *reinterpret_cast<uint4*>(p.cache[which] + 2 * at) = v;
+        const uint16_t* const src = p.src[which] + t * p.ld[which];
+        const int64_t at = page * p.block_stride + (int64_t)(slot - page * p.block) * p.slot_stride;
+        uint8_t* const dst = p.cache[which] + (F8 ? at : 2 * at);
+#pragma unroll 2
+        for (int j = lane; j < pieces; j += 32) {
+            const int h = j >> log_per, c = (j - (h << log_per)) * kPiece;
+            const uint4* const from =
+                reinterpret_cast<const uint4*>(src + h * p.head_stride[which] + c);
+            uint8_t* const to = dst + (F8 ? 1 : 2) * (h * p.cache_head_stride + c);
+            if (F8) {
+                const uint4 v = from[0], w = from[1];
+                const uint2 a = quantise(v, p.scale[which], p.inverse[which]);
+                const uint2 b = quantise(w, p.scale[which], p.inverse[which]);
+                *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
+            } else {
+                *reinterpret_cast<uint4*>(to) = from[0];
+            }
         }
     }
 }
@@ -365,6 +400,8 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     p.cache[1] = static_cast<uint8_t*>(c.v);
     p.scale[0] = c.k_scale;
     p.scale[1] = c.v_scale;
+    for (int i = 0; i < 2; ++i)
+        p.inverse[i] = p.scale[i] >= 1e-30f && p.scale[i] <= 1e30f ? 1.f / p.scale[i] : 0.f;
     p.slots = slots;
     p.tokens = tokens;
     p.blocks = c.blocks;
@@ -374,7 +411,7 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     p.heads = c.heads;
     p.dim = c.dim;
     p.block = c.block_size;
-    const int64_t want = (tokens * c.heads * (c.dim / 8) * 2 + kAppendThreads - 1) / kAppendThreads;
+    const int64_t want = (tokens * 2 * 32 + kAppendThreads - 1) / kAppendThreads;  // a warp per row
     const int grid = (int)(want > 8 * sms ? 8 * sms : want);
     if (c.type == NVFP4_KV_E4M3)
         nvfp4_append_kernel<true><<<grid, kAppendThreads, 0, stream>>>(p);

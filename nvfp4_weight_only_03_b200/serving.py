@@ -184,7 +184,7 @@ def _workspace(kind: str, need: int, index: int, st: int) -> torch.Tensor:
     the graph's own: two graphs never share one."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-        ws[:512].zero_()
+        ws[:2048].zero_()  # its words that have to be zero (one per SM, and the error word)
         return ws
     ws = _workspaces.get((kind, index, st))
     if ws is None or ws.numel() < need:
@@ -305,12 +305,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     n = lens.shape[0]
     cols, ld = _table_args(table, n, index)
     if out is None:
-        out = q.new_empty(shape)
-        ldo, ho = heads * dim, dim
-    else:
-        if out.shape != shape:
-            raise ValueError(f"out must be {list(shape)}")
-        ldo, ho = _heads(out, "out", index)
+        out = torch.empty_like(q)
+    elif out.shape != shape:
+        raise ValueError(f"out must be {list(shape)}")
+    ldo, ho = _heads(out, "out", index)
     st = _raw_stream(index)
     if ws is None:
         ws = _workspace("attn", paged_attention_workspace_bytes(dim), index, st)

@@ -287,6 +287,22 @@ def test_same_result_every_time_and_on_another_stream():
         assert torch.equal(o, want)
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("tokens", [1, 2])
+def test_few_rows_joined_in_the_kernel(tokens, f8):
+    # the parts of a tile are joined by the last CTA to leave one, over and over on one workspace
+    for k, n in enumerate((3, 130, 517, 4000, 30011)):
+        b = Batch(17 + k, [n], [tokens], 12, 2, 128, 16, f8)
+        ws = torch.zeros(nv.paged_attention_workspace_bytes(128), dtype=torch.uint8, device="cuda")
+        want = check_attention(b, ws=ws)
+        for _ in range(5):
+            assert torch.equal(b.call(ws=ws, check=False), want)
+        torch.cuda.synchronize()
+        assert int(ws[:1024].count_nonzero()) == 0
+        both = Batch(17 + k, [n] * 9, [tokens] * 9, 12, 2, 128, 16, f8)  # past the rule's limit
+        check_attention(both)
+
+
 def test_captured_call_serves_later_lengths():
     b = Batch(15, [200, 300], [1, 1], 8, 2, 128, 16)
     lens, out = ints([200, 300]), torch.empty_like(b.q)
@@ -337,6 +353,32 @@ def test_append(tokens, heads, dim, block, f8, layout):
         w[at // block, at % block] = new.contiguous().view(torch.uint8).view(len(at), heads, -1)
         got = cache.contiguous().view(torch.uint8).view(blocks, block, heads, -1)
         assert torch.equal(got, w)
+
+
+def test_append_rounds_the_true_quotient():
+    """Values whose quotient lies at a border between two codes, or a place beside it, for scales of
+    many magnitudes: the code is that of the fp32 quotient, not of a product with 1 / scale."""
+    codes = torch.arange(0x7F, dtype=torch.uint8).view(F8).double()  # every non-negative value
+    borders = (codes[1:] + codes[:-1]) / 2
+    for scale in (0.3, 1.0, 7.3e-5, 0.0123, 3.0e4, 1e-38, 3e38):
+        scale = torch.tensor(scale, dtype=torch.float32)
+        x = (borders * scale.double()).to(torch.bfloat16).view(torch.int16)
+        x = torch.cat([x - 1, x, x + 1, x | -0x8000]).view(torch.bfloat16)
+        x = torch.cat([x, torch.tensor([float("nan"), 448.0, -1e30, 0.0, -0.0, 1e-30, 2.0 ** -9,
+                                        2.0 ** -10]).bfloat16()])
+        n = -(-len(x) // 64)
+        rows = torch.zeros(n * 64, dtype=torch.bfloat16)
+        rows[:len(x)] = x
+        rows = rows.view(n, 1, 64).cuda()
+        kc, vc = (torch.zeros((n, 16, 1, 64), dtype=F8, device="cuda") for _ in range(2))
+        nv.kv_append(rows, rows, kc, vc, torch.arange(n, device="cuda", dtype=torch.int32) * 16,
+                     float(scale), float(scale))
+        q = rows.cpu().float().view(-1) / scale
+        want = torch.where(torch.isnan(q), q, q.clamp(-448, 448)).to(F8)
+        for c in (kc, vc):
+            got = c[:, 0, 0].reshape(-1).cpu()
+            same = got.view(torch.uint8) == want.view(torch.uint8)
+            assert (same | (torch.isnan(got.float()) & torch.isnan(want.float()))).all()
 
 
 # ---------------------------------------------------------------- the plan
