@@ -8,7 +8,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", f) for f in
         ("nvfp4_gemv.cu", "nvfp4_gemv_tc.cu", "nvfp4_paged.cu", "nvfp4_attn.cu",
-         "nvfp4_lora.cu")]
+         "nvfp4_lora.cu", "nvfp4_host.cu")]
 HDRS = [os.path.join(ROOT, "include", "nvfp4.h")] + \
        [os.path.join(HERE, "csrc", f) for f in
         ("nvfp4_tc.h", "nvfp4_prologue.h", "nvfp4_host.h", "nvfp4_ptx.h")]

@@ -67,7 +67,6 @@
 #include <string.h>
 
 #include "nvfp4.h"
-#include "nvfp4_host.h"
 #include "nvfp4_prologue.h"
 #include "nvfp4_tc.h"
 
@@ -1772,15 +1771,6 @@ int run_chain(const nvfp4_chain_op_t* ops, int count, int m, void* ws, size_t ws
 }
 
 }  // namespace
-
-int nvfp4_host::device(int* dev, int* sms, EncodeFn* encode) {
-    DeviceInfo* di = nullptr;
-    const int st = device_info(dev, &di);
-    if (st != NVFP4_OK) return st;
-    *sms = di->sms;
-    *encode = g_encode;
-    return NVFP4_OK;
-}
 
 // ------------------------------------------------------------------------------------------
 // Scratch of nvfp4_gemv_noalloc: the workspace of nvfp4_gemv (header, one hand-off word per CTA,

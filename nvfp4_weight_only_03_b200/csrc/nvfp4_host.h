@@ -1,4 +1,4 @@
-// Host-side helpers shared by the library's translation units (defined in nvfp4_gemv.cu).
+// Host-side helpers shared by the library's translation units (defined in nvfp4_host.cu).
 #ifndef NVFP4_HOST_H
 #define NVFP4_HOST_H
 

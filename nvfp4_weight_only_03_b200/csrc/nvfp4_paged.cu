@@ -173,19 +173,20 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
 // values, or 16 codes), so loads and stores are whole sectors and the slot is looked up once per
 // row.  HBM bound, 4 bytes of traffic per value (3 with an 8-bit cache).
 //
-// An e4m3 code is e4m3_rn(x / scale) of the fp32 quotient, saturated at 448.  The quotient is formed as
-// x * (1 / scale), which is off by at most 2 of its last places (three roundings of half a place):
-// that can change the code only next to a border between codes, in fp32 a value whose last 20
-// mantissa bits are 2^19 (e4m3 keeps 3 of the 23), and only from 2^-6 up, where codes keep three bits
-// whatever the exponent.  Values within 4 places of a border, or below 2^-6 but not zero, are
-// divided: one in 10^5 of the first kind.  (A division is ten instructions and was the bound.)
+// An e4m3 code is e4m3_rn(x / scale) of the fp32 quotient, saturated at 448.  A division per value was
+// the bound (a hundred instructions per eight values).  The quotient is formed from 1 / scale in two
+// fp32 terms, r and the rest of it, as q = fma(x, r, x * rest), which is off by little more than the
+// rounding itself, so within one place; Markstein's correction (IBM J. Res. Dev. 34, 1990: with r the
+// rounded reciprocal and q within a place, q + r (x - q scale) in two fused steps is the rounded
+// quotient) then makes it exact.  Infinities, NaN, and scales whose products might leave the normal
+// range are divided.
 constexpr int kAppendThreads = 256;
 
 struct AppendParams {
     const uint16_t* src[2];
     int64_t ld[2], head_stride[2];
     uint8_t* cache[2];
-    float scale[2], inverse[2];  // inverse: 0 where 1 / scale is not a normal number
+    float scale[2], inverse[2], rest[2];  // 1 / scale = inverse + rest; inverse 0: divide
     const int32_t* slots;
     int64_t tokens, blocks, block_stride, slot_stride, cache_head_stride;
     int heads, dim, block;
@@ -200,23 +201,21 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     return r;
 }
 
-// Whether x * (1 / scale) may round to another code than x / scale.
-__device__ __forceinline__ bool near_border(float q) {
-    const uint32_t u = __float_as_uint(q) & 0x7fffffffu;
-    return (u & 0xfffffu) - 0x7fffcu <= 8u || (u < 0x3c800000u && u != 0);
-}
-
 // 8 bf16 values -> 8 codes.
-__device__ __forceinline__ uint2 quantise(uint4 v, float scale, float inverse) {
+__device__ __forceinline__ uint2 quantise(uint4 v, float scale, float inverse, float rest) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0;  // bits 15 and 31: an exponent of all ones
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top |= (w[i] & 0x7f807f80u) + 0x00800080u;
+    const bool divide = inverse == 0.f || (top & 0x80008000u);
     float q[8];
-    bool again = inverse == 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        q[i] = (i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) * inverse;
-        again |= near_border(q[i]);
+        const float x = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+        const float a = fmaf(x, inverse, x * rest);
+        q[i] = fmaf(fmaf(-a, scale, x), inverse, a);
     }
-    if (again) {
+    if (divide) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             q[i] = __fdiv_rn(i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]), scale);
@@ -242,6 +241,7 @@ __global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const Appe
         const uint16_t* const src = p.src[which] + t * p.ld[which];
         const int64_t at = page * p.block_stride + (int64_t)(slot - page * p.block) * p.slot_stride;
         uint8_t* const dst = p.cache[which] + (F8 ? at : 2 * at);
+        const float scale = p.scale[which], inverse = p.inverse[which], rest = p.rest[which];
 #pragma unroll 2
         for (int j = lane; j < pieces; j += 32) {
             const int h = j >> log_per, c = (j - (h << log_per)) * kPiece;
@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const Appe
             uint8_t* const to = dst + (F8 ? 1 : 2) * (h * p.cache_head_stride + c);
             if (F8) {
                 const uint4 v = from[0], w = from[1];
-                const uint2 a = quantise(v, p.scale[which], p.inverse[which]);
-                const uint2 b = quantise(w, p.scale[which], p.inverse[which]);
+                const uint2 a = quantise(v, scale, inverse, rest);
+                const uint2 b = quantise(w, scale, inverse, rest);
                 *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
             } else {
                 *reinterpret_cast<uint4*>(to) = from[0];
@@ -401,7 +401,10 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     p.scale[0] = c.k_scale;
     p.scale[1] = c.v_scale;
     for (int i = 0; i < 2; ++i)
-        p.inverse[i] = p.scale[i] >= 1e-30f && p.scale[i] <= 1e30f ? 1.f / p.scale[i] : 0.f;
+        if (p.scale[i] >= 1e-15f && p.scale[i] <= 1e15f) {
+            p.inverse[i] = 1.f / p.scale[i];
+            p.rest[i] = (float)(1.0 / p.scale[i] - p.inverse[i]);
+        }
     p.slots = slots;
     p.tokens = tokens;
     p.blocks = c.blocks;
