@@ -93,13 +93,17 @@ def _nv():
 # the usual case (the tensors' device is current, no stream given) asks torch for plain numbers
 # only; any other enters the device and the stream and starts again.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+_I32, _BF16, _F8, _F32 = torch.int32, torch.bfloat16, torch.float8_e4m3fn, torch.float32
 
 
 def _elsewhere(first: torch.Tensor, stream) -> bool:
     """Whether the call has to enter another device or stream first."""
-    if not first.is_cuda:
+    index = first.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    return stream is not None or first.get_device() != torch.cuda.current_device()
+    return stream is not None or index != _current_device()
 
 
 @contextlib.contextmanager
@@ -120,7 +124,7 @@ def _same_device(index: int, name: str, t: torch.Tensor) -> None:
 
 def _ints(t: torch.Tensor, name: str, n: int, index: int) -> int:
     """Address of a contiguous int32 [n] on the call's device."""
-    if t.dtype != torch.int32:
+    if t.dtype is not _I32:
         raise TypeError(f"{name} must be int32")
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous [{n}], got {list(t.shape)}")
@@ -130,59 +134,63 @@ def _ints(t: torch.Tensor, name: str, n: int, index: int) -> int:
 
 
 def _table_args(table: torch.Tensor, rows: int, index: int):
-    if table.dtype != torch.int32:
+    if table.dtype is not _I32:
         raise TypeError("table must be int32")
-    shape = table.shape
-    if len(shape) != 2 or shape[0] != rows or (shape[1] > 1 and table.stride(1) != 1):
+    shape, stride = table.shape, table.stride()
+    if len(shape) != 2 or shape[0] != rows or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"table must be [{rows}][columns] with unit inner stride")
-    _same_device(index, "table", table)
+    if table.get_device() != index:
+        _same_device(index, "table", table)
     cols = shape[1]
-    return cols, table.stride(0) if rows > 1 else cols
+    return cols, stride[0] if rows > 1 else cols
 
 
 def _heads(t: torch.Tensor, name: str, index: int):
     """(token stride, head stride) of a bf16 [tokens][heads][dim] view."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be bfloat16")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or stride[2] != 1:
         raise ValueError(f"{name} must be [tokens][heads][dim] with unit inner stride")
-    _same_device(index, name, t)
-    head = stride[1] if shape[1] > 1 else shape[2]
-    return stride[0] if shape[0] > 1 else max(shape[1] * head, shape[2]), head
+    if t.get_device() != index:
+        _same_device(index, name, t)
+    n, h, d = shape
+    head = stride[1] if h > 1 else d
+    return stride[0] if n > 1 else max(h * head, d), head
 
 
 def _cache_args(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float, v_scale: float,
                 index: int) -> KvCacheStruct:
     dtype = k_cache.dtype
-    if (dtype != torch.bfloat16 and dtype != torch.float8_e4m3fn) or v_cache.dtype != dtype:
+    if (dtype is not _BF16 and dtype is not _F8) or v_cache.dtype is not dtype:
         raise TypeError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
     shape = k_cache.shape
     if len(shape) != 4 or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must be [blocks][block_size][heads][dim]")
     blocks, block, heads, dim = shape
-    stride = k_cache.stride()
-    same = stride == v_cache.stride()
+    stride, other = k_cache.stride(), v_cache.stride()
     page, slot, head, one = stride
+    same = stride == other
     if heads == 1 or blocks <= 1 or not same:  # the stride of a single head or page says nothing
         def used(st):
             return (st[0] if blocks > 1 else block * st[1], st[1], st[2] if heads > 1 else dim,
                     st[3])
         page, slot, head, one = used(stride)
-        same = used(v_cache.stride()) == (page, slot, head, one)
+        same = used(other) == (page, slot, head, one)
     if one != 1 or not same:
         raise ValueError("k_cache and v_cache must have the same strides, the inner one 1")
-    _same_device(index, "k_cache", k_cache)
-    _same_device(index, "v_cache", v_cache)
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        _same_device(index, "k_cache", k_cache)
+        _same_device(index, "v_cache", v_cache)
     return KvCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(),
-                         KV_BF16 if dtype == torch.bfloat16 else KV_E4M3, heads, dim, block,
-                         blocks, page, slot, head, k_scale, v_scale)
+                         KV_BF16 if dtype is _BF16 else KV_E4M3, heads, dim, block, blocks, page,
+                         slot, head, k_scale, v_scale)
 
 
 def _workspace(kind: str, need: int, index: int, st: int) -> torch.Tensor:
     """The cached workspace of (device, current stream), or, while a graph is captured, one of
     the graph's own: two graphs never share one."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
         ws[:2048].zero_()  # its words that have to be zero (one per SM, and the error word)
         return ws
@@ -331,23 +339,26 @@ _attn_bytes: dict = {}
 
 def paged_attention_workspace_bytes(dim: int) -> int:
     """Bytes of a paged_attention workspace for this head dim on the current device."""
-    key = (torch.cuda.current_device(), dim)
-    if key not in _attn_bytes:
+    key = (_current_device(), dim)
+    need = _attn_bytes.get(key)
+    if need is None:
         b = ctypes.c_size_t()
         nv = _nv()
         nv._check(nv.lib().nvfp4_paged_attn_workspace_bytes(dim, ctypes.byref(b)),
                   "nvfp4_paged_attn_workspace_bytes")
-        _attn_bytes[key] = int(b.value)
-    return _attn_bytes[key]
+        need = _attn_bytes[key] = int(b.value)
+    return need
 
 
 def _rows(t: torch.Tensor, name: str, m: int, n: int, index: int) -> int:
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be bfloat16")
-    if t.shape != (m, n) or (n > 1 and t.stride(1) != 1):
+    stride = t.stride()
+    if t.shape != (m, n) or (n > 1 and stride[1] != 1):
         raise ValueError(f"{name} must be [{m}][{n}] with unit inner stride, got {list(t.shape)}")
-    _same_device(index, name, t)
-    return t.stride(0) if m > 1 else n
+    if t.get_device() != index:
+        _same_device(index, name, t)
+    return stride[0] if m > 1 else n
 
 
 _lora_bytes: dict = {}
@@ -355,14 +366,17 @@ _lora_bytes: dict = {}
 
 def lora_workspace_bytes(m: int, adapters: int, rank: int, k: int) -> int:
     """Bytes of a lora_add workspace on the current device."""
-    key = (torch.cuda.current_device(), m, adapters, rank, k)
-    if key not in _lora_bytes:
+    key = (m, adapters, rank, k)
+    need = _lora_bytes.get(key)
+    if need is None:
         b = ctypes.c_size_t()
         nv = _nv()
         nv._check(nv.lib().nvfp4_lora_workspace_bytes(m, adapters, rank, k, ctypes.byref(b)),
                   "nvfp4_lora_workspace_bytes")
-        _lora_bytes[key] = int(b.value)
-    return _lora_bytes[key]
+        if len(_lora_bytes) > 4096:
+            _lora_bytes.clear()
+        need = _lora_bytes[key] = int(b.value)
+    return need
 
 
 def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -383,34 +397,34 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if x.dim() == 1:
         x = x.unsqueeze(0)
     dev = y.get_device()
-    for name, t in (("a", a), ("b", b)):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be bfloat16")
-        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be 3-D with unit inner stride")
-        _same_device(dev, name, t)
+    if a.dtype is not _BF16 or b.dtype is not _BF16:
+        raise TypeError("a and b must be bfloat16")
+    sa, sb, shape = a.stride(), b.stride(), b.shape
+    if len(sa) != 3 or len(sb) != 3:
+        raise ValueError("a must be [adapters][rank][K] and b [adapters][N][rank]")
     s, rank, k = a.shape
-    n = b.shape[1]
-    if b.shape != (s, n, rank):
-        raise ValueError(f"b must be [{s}][N][{rank}], got {list(b.shape)}")
+    n = shape[1]
+    if shape != (s, n, rank):
+        raise ValueError(f"b must be [{s}][N][{rank}], got {list(shape)}")
+    if (k > 1 and sa[2] != 1) or (rank > 1 and sb[2] != 1):
+        raise ValueError("a and b must have unit inner strides")
+    if a.get_device() != dev or b.get_device() != dev or scales.get_device() != dev:
+        for name, t in (("a", a), ("b", b), ("scales", scales)):
+            _same_device(dev, name, t)
     m = y.shape[0]
     ldy, ldx = _rows(y, "y", m, n, dev), _rows(x, "x", m, k, dev)
-    if scales.dtype != torch.float32:
+    if scales.dtype is not _F32:
         raise TypeError("scales must be float32")
     if scales.shape != (s,) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous [{s}]")
-    _same_device(dev, "scales", scales)
     if out is None:
-        out = y.new_empty((m, n))
-        ldo = n
-    else:
-        ldo = _rows(out, "out", m, n, dev)
+        out = torch.empty_like(y)
+    ldo = _rows(out, "out", m, n, dev)
     st = _raw_stream(dev)
     if ws is None:
         ws = _workspace("lora", lora_workspace_bytes(m, s, rank, k), dev, st)
     else:
         _same_device(dev, "ws", ws)
-    sa, sb = a.stride(), b.stride()
     l = LoraStruct(a.data_ptr(), sa[0] if s > 1 else rank * k, sa[1] if rank > 1 else k,
                    b.data_ptr(), sb[0] if s > 1 else n * rank, sb[1] if n > 1 else rank,
                    scales.data_ptr(), None if ranks is None else _ints(ranks, "ranks", s, dev),
