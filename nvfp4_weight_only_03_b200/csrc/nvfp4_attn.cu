@@ -83,7 +83,7 @@ struct Cfg {
     static constexpr int kRowKeys = F8 ? kRow : 64;   // its values
     static constexpr int kPanels = D / kRowKeys;      // panels of Q and K
     static constexpr int kThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kQWarp + 1);
-    static constexpr size_t kHead = F8 ? 4096 : 3072;  // Small, in front of the tiles
+    static constexpr size_t kHead = F8 ? 4096 : 3 * 1024;  // Small, in front of the tiles
     // Places of K, of V and of V as it lies in an e4m3 cache.  K and V have rings of their own, since
     // their readers go on independently (with one ring, a reader could take the phase of the
     // other's tile for that of its own).
