@@ -66,6 +66,7 @@ struct Small {
     int start[2][12];  // a Cursor: where the range begins; then, by turns, the softmax's next tile
     uint32_t tmem;
     int stop, last;
+    int partly[8];  // item + 1 where V of a key that not all rows see is not finite; [item's place]
     float row_max[2][kRows];  // a unit's reference maximum: [its parity][row]
     float row_sum[2][kRows];  // a row tile's sum of weights: [warpgroup][row]
     // biased exponents of the 8-bit Q rows' scales.  Q may be two row tiles ahead of the softmax.
@@ -142,6 +143,8 @@ struct Params {
     Divisor by_group, by_block;
     int outside;       // a page index past the tensor: its boxes arrive as zeros
     int capacity;      // keys that a table row can hold
+    const void* v;     // the cache's values and strides (elements), for what is read without TMA
+    int64_t block_stride, slot_stride, head_stride;
     int min_units;     // fewest units worth a CTA of their own
     float c;           // scale * k_scale * log2(e)
     float v_scale;
@@ -231,6 +234,11 @@ __device__ __forceinline__ int key_end(const Params& p, const Request& q, int ti
     const int rows = min((tile + 1) * kRows, q.n * p.group);
     const int last = (int)div_by(rows - 1, p.by_group);
     return min(max(q.len - q.n + last + 1, 0), p.capacity);
+}
+
+// Keys from this one on are seen by some rows of the row tile only: its first row's position + 1.
+__device__ __forceinline__ int key_open(const Params& p, const Request& q, int tile) {
+    return max(q.len - q.n + (int)div_by(tile * kRows, p.by_group) + 1, 0);
 }
 
 template <int TK>
@@ -370,6 +378,35 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
     return g;
 }
 
+// ---- V that is not finite -------------------------------------------------------------------
+// In the product a weight of zero times an infinity or NaN is NaN, and a key that comes after a
+// row's own position has such a weight.  So where V of a key that only some rows of the row tile see
+// is not finite, the product gets a zero in its place, and the rows that see it get the value
+// itself here: it decides their result whatever the weights are.  One thread, its row's columns
+// col .. col + cols - 1, behind the result (out) or the part that it wrote.
+template <bool F8>
+__device__ __noinline__ void add_not_finite(const Params& p, const int32_t* table, int head, int key,
+                                            int key_to, int col, int cols, uint16_t* out, float* part) {
+    for (; key < key_to; ++key) {
+        const int c = (int)div_by(key, p.by_block), page = table[c];
+        if ((unsigned)page >= (unsigned)p.blocks) continue;
+        const int64_t at = page * p.block_stride + (key - c * p.block) * p.slot_stride +
+                           head * p.head_stride;
+        for (int i = col; i < col + cols; ++i) {
+            float v;
+            if (F8)
+                v = (static_cast<const uint8_t*>(p.v)[at + i] & 0x7f) == 0x7f ? NAN : 0.f;
+            else
+                v = __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.v)[at + i] << 16);
+            if (isfinite(v)) continue;
+            if (part)
+                part[i] += v;
+            else
+                out[i] = (uint16_t)pack16(false, __uint_as_float((uint32_t)out[i] << 16) + v, 0.f);
+        }
+    }
+}
+
 // ---- joining the parts of a cut row tile: a warp per row, the parts in order -----------------
 // Part 0 lies with its CTA's cut at the end, the others with their cuts at the start.
 template <int D>
@@ -479,6 +516,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.o_free, kSoftmaxWarps);
         sm.stop = 0;
+        for (int i = 0; i < 8; ++i) sm.partly[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&map_k);
         prefetch_map(&map_v);
@@ -769,10 +807,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         const uint32_t unit0 = ((2 * piece) ^ (key & 7)) << 4, unit1 = unit0 ^ 16;
         Ring<NR> raws(0);
         Ring<NV> values(1);
+        int item = 0;  // (at most NV <= 4 ahead of the softmax warps')
         while (left > 0 && ok) {
             const int cnt = cur.take(left);
             if (cnt <= 0) break;
-            const int end = key_end(p, cur.q, cur.tile);
+            const int end = key_end(p, cur.q, cur.tile), open = key_open(p, cur.q, cur.tile);
             for (int i = 0; i < cnt; ++i) {
                 const int rs = raws.slot, ts = values.slot;
                 if (!mbar_wait(&sm.raw_full[rs], raws.phase, stop_v) ||
@@ -810,8 +849,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                             make_uint4(out[4], out[5], out[6], out[7]);
                     }
                 }
-                // What is rare is done over: NaN codes, which only cvt knows, and values past the end,
-                // which must not meet a weight of zero as NaN or infinity (only V(n-1) holds any).
+                // What is rare is done over: NaN codes, which only cvt knows and which are zeros here
+                // if not all rows see the key, and values past the end, which are zeros.
                 const int valid = end - (cur.u + i) * TK;
                 if (valid < TK || (most & 0x7fffu) >= kWidenedNan ||
                     (most >> 16 & 0x7fffu) >= kWidenedNan) {
@@ -823,7 +862,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 #pragma unroll 1
                         for (int j = 0; j < 4; ++j) {
                             uint32_t even = 0, odd = 0;
-                            if (key + key_of(x) < valid) widen_nan(in[j], even, odd);
+                            if (key + key_of(x) < valid) {
+                                uint32_t codes = in[j];
+                                if ((cur.u + i) * TK + key + key_of(x) >= open) {
+                                    const uint32_t nan =
+                                        ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                    codes &= ~((nan >> 7) * 0xffu);
+                                    if (nan) sm.partly[item & 7] = item + 1;
+                                }
+                                widen_nan(codes, even, odd);
+                            }
                             *reinterpret_cast<uint2*>(to + (j < 2 ? unit0 : unit1) + (j & 1) * 8) =
                                 make_uint2(even, odd);
                         }
@@ -838,6 +886,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 raws.step();
                 values.step();
             }
+            ++item;
             left -= cur.lead + cnt;
             cur.next(p);
         }
@@ -851,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // on whatever is there) to the end of the range.
         const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        int g = 0, item = 0, values_at = 0;
+        int g = 0, item = 0;
         auto wait = [&](uint64_t* b, uint32_t parity) {
             if (ok && !mbar_wait(b, parity, stop_v)) ok = false;
         };
@@ -868,7 +917,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const bool busy = quarter * 32 < rows;  // this warp has rows
             const bool mine = row < rows;  // lanes past the rows compute on whatever is there
             const int tok = (int)div_by(row0 + row, p.by_group);
-            const int end = key_end(p, cur.q, cur.tile);
+            const int end = key_end(p, cur.q, cur.tile), open = key_open(p, cur.q, cur.tile);
             // the last key this row sees
             const int last = mine ? min(cur.q.len - cur.q.n + tok, end - 1) : INT32_MAX;
             const int32_t* const table = p.table + cur.r * p.ld_table;
@@ -972,17 +1021,34 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 if (g >= 2) wait(&sm.pv_done[wg], ((g >> 1) - 1) & 1);
                 tc_after_sync();
                 const int unit0 = (cur.u + j) * TK;
-                if (!F8 && unit0 + TK > end) {
-                    // values past the end are whatever the page held: zeros, so that their weights
-                    // of zero add nothing
-                    const int vi = values_at + cnt - 1, slot = vi % NV;
-                    wait(&full[NK + slot], (vi / NV) & 1);
-                    const int from = max(end - unit0, 0);
+                if (!F8 && unit0 + TK > min(open, end)) {
+                    // Values past the end are whatever the page held: zeros, so that their weights
+                    // of zero add nothing.  Those that not all rows see: zeros where not finite.
+                    const int slot = g % NV;
+                    wait(&full[NK + slot], (g / NV) & 1);
+                    const int from = max(min(open, end) - unit0, 0);
                     uint8_t* const v = val_ring + slot * C::kVal;
+#pragma unroll 1
                     for (int i = row; i < (TK - from) * (D / 8); i += kRows) {
                         const int key = from + i / (D / 8), x = i % (D / 8);
-                        *reinterpret_cast<uint4*>(v + (x >> 3) * (TK * 128) + key * 128 +
-                                                  (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        uint4* const at = reinterpret_cast<uint4*>(
+                            v + (x >> 3) * (TK * 128) + key * 128 + (x & 7) * 16);
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (unit0 + key < end) {
+                            w = *at;
+                            uint32_t* const ww = &w.x;
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {  // an exponent of all ones
+                                const uint32_t bad =
+                                    ((ww[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                                any |= bad;
+                                ww[e] &= ~((bad >> 15) * 0xffffu);
+                            }
+                            if (!any) continue;
+                            sm.partly[item & 7] = item + 1;
+                        }
+                        *at = w;
                     }
                     fence_async_smem();
                 }
@@ -1055,10 +1121,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     }
                 }
             }
+            if (mine && sm.partly[item & 7] == item + 1)
+                add_not_finite<F8>(
+                    p, table, cur.h, max(open, cur.u * TK), min(last + 1, (cur.u + cnt) * TK),
+                    wg * (D / 2), D / 2,
+                    p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +
+                        (int64_t)(cur.h * p.group + (row0 + row) - tok * p.group) * p.o_head_stride,
+                    whole ? nullptr : p.part_o + (part0 + row) * D);
             tc_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
-            values_at += cnt;
             ++item;
             if (!whole && (cur.u == 0 || p.join_here)) {
                 // the CTA with unit x (as the ranges count) of this row tile's 0 .. n - 1 from `zero`
@@ -1268,6 +1340,10 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     p.blocks = (int)kv.blocks;
     p.outside = kv.blocks ? (int)kv.blocks : 1;
     p.box = box;
+    p.v = kv.v;
+    p.block_stride = kv.block_stride;
+    p.slot_stride = kv.slot_stride;
+    p.head_stride = kv.head_stride;
     const int64_t cap = a.table_columns * kv.block_size;
     p.capacity = (int)(cap > INT32_MAX - 1024 ? INT32_MAX - 1024 : cap);
     p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;

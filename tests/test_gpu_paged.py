@@ -251,6 +251,37 @@ def test_nan_of_a_visible_token_reaches_its_rows_and_no_others(f8):
 
 
 @pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim,len_,new,block", [
+    (24, 4, 256, 300, 8, 16), (12, 2, 128, 700, 200, 16), (7, 1, 64, 150, 150, 48),
+    (24, 4, 256, 9000, 100, 64), (5, 5, 128, 333, 333, 32)])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them_and_no_others(heads, kv_heads, dim,
+                                                                               len_, new, block,
+                                                                               f8):
+    b = Batch(30, [70, len_, 33], [3, new, 33], heads, kv_heads, dim, block, f8)
+    want = b.call()
+    first, keys = len_ - new, [len_ - new + 1, len_ - new // 2, len_ - 1]
+    seen = torch.zeros(new, dim, dtype=torch.bool, device="cuda")
+    for i, key in enumerate(keys):  # a key of the new ones, each in dimensions of its own
+        page = int(b.table[1, key // block])
+        dims = slice(dim // 4 * i + 3, dim // 4 * i + 6)
+        if f8:
+            b.vc.view(torch.uint8)[page, key % block, :, dims] = 0x7F if i else 0xFF
+        else:
+            b.vc[page, key % block, :, dims] = (float("nan"), float("inf"), -float("inf"))[i]
+        seen[key - first:, dims] = True
+    out = b.call()
+    mine = slice(3, 3 + new)
+    assert torch.equal(out[:3], want[:3]) and torch.equal(out[3 + new:], want[3 + new:])
+    hit = seen[:, None].expand(new, heads, dim)
+    assert not torch.isfinite(out[mine][hit]).any()
+    assert torch.equal(out[mine][~hit], want[mine][~hit])
+    if not f8:
+        d = dim // 4 + 4
+        assert (out[mine][keys[1] - first:, :, d] == float("inf")).all()
+        assert (out[mine][keys[2] - first:, :, 2 * (dim // 4) + 4] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_many_requests_and_long_context(f8):
     rng = np.random.default_rng(9)
     lens = [int(x) for x in rng.integers(1, 400, 300)]
