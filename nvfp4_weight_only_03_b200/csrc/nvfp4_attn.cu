@@ -153,7 +153,7 @@ struct Params {
     int32_t* arrived;  // [grid]: parts of CTA i's cut row tile written so far; zero between calls
     Cut* cuts;         // [grid]
     float2* part_ml;   // [grid][2][128]: maximum (log2 domain) and sum
-    float* part_o;     // [grid][2][128][D]
+    float* part_o;     // [grid][2][D / 4][128][4]: a warp's rows side by side
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -400,68 +400,89 @@ __device__ __noinline__ void add_not_finite(const Params& p, const int32_t* tabl
                 v = __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.v)[at + i] << 16);
             if (isfinite(v)) continue;
             if (part)
-                part[i] += v;
+                part[i / 4 * (kRows * 4) + i % 4] += v;
             else
                 out[i] = (uint16_t)pack16(false, __uint_as_float((uint32_t)out[i] << 16) + v, 0.f);
         }
     }
 }
 
-// ---- joining the parts of a cut row tile: a warp per row, the parts in order -----------------
-// Part 0 lies with its CTA's cut at the end, the others with their cuts at the start.
+// Row `row` (of all the request's) of the cursor's head.
+template <int TK>
+__device__ __forceinline__ const uint16_t* q_row(const Params& p, const Cursor<TK>& cur, int row) {
+    const int tok = (int)div_by(row, p.by_group);
+    return p.q + (int64_t)(cur.q.token0 + tok) * p.ldq +
+           (int64_t)(cur.h * p.group + row - tok * p.group) * p.q_head_stride;
+}
+
+// ---- joining the parts of a cut row tile, in their order -------------------------------------
+// Part 0 lies with its CTA's cut at the end, the others with their cuts at the start.  A thread
+// takes 8 columns of a row, its neighbours those of the next rows, as the parts lie.
 template <int D>
-__device__ __noinline__ void join_rows(const Params& p, int owner, const Cut& cut, int row, int step) {
-    const int lane = threadIdx.x & 31;
-    constexpr int kPer = D / 32;
-    for (; row < cut.rows; row += step) {
-        auto at = [&](int i) { return ((int64_t)(owner + i) * 2 + (i == 0)) * kRows + row; };
-        float top = -INFINITY;
-        for (int i = lane; i < cut.parts; i += 32) top = fmaxf(top, __ldcg(&p.part_ml[at(i)].x));
+__device__ __noinline__ void join_rows(const Params& p, int owner, const Cut& cut, int item, int step) {
+    for (; item < cut.rows * (D / 8); item += step) {
+        const int oct = item / cut.rows, row = item - oct * cut.rows;
+        auto at = [&](int i) { return ((int64_t)(owner + i) * 2 + (i == 0)) * kRows; };
+        float acc[8], sum = 0.f, top = -INFINITY;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        float acc[kPer], sum = 0.f;
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        constexpr int kSome = 8;  // parts read at once: the loads' latency is what this takes
+#pragma unroll 1
+        for (int i0 = 0; i0 < cut.parts; i0 += kSome) {
+            float2 ml[kSome];
+            float4 u[kSome], v[kSome];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-        if (top > -INFINITY) {
-#pragma unroll 4
-            for (int i = 0; i < cut.parts; ++i) {
-                const int64_t a = at(i);
-                const float2 ml = __ldcg(&p.part_ml[a]);
-                const float w = exp2_approx(ml.x - top);
-                const float2* const src =
-                    reinterpret_cast<const float2*>(p.part_o + a * D + lane * kPer);
-                sum = fmaf(w, ml.y, sum);
-                // a part that saw no key has a weight of zero and zeros to weigh
-#pragma unroll
-                for (int e = 0; e < kPer; e += 2) {
-                    const float2 v = __ldcg(src + e / 2);
-                    acc[e] = fmaf(w, v.x, acc[e]);
-                    acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+            for (int j = 0; j < kSome; ++j) {
+                ml[j] = make_float2(-INFINITY, 0.f);
+                u[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + j < cut.parts) {
+                    const int64_t a = at(i0 + j);
+                    const float4* const src =
+                        reinterpret_cast<const float4*>(p.part_o + a * D) + oct * 2 * kRows + row;
+                    ml[j] = __ldcg(&p.part_ml[a + row]);
+                    u[j] = __ldcg(src), v[j] = __ldcg(src + kRows);
                 }
+            }
+            const float was = top;
+#pragma unroll
+            for (int j = 0; j < kSome; ++j) top = fmaxf(top, ml[j].x);
+            // (parts that saw no key have a weight of zero and zeros to weigh)
+            const float ref = top == -INFINITY ? 0.f : top, f = exp2_approx(was - ref);
+            sum *= f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+            for (int j = 0; j < kSome; ++j) {
+                const float w = exp2_approx(ml[j].x - ref);
+                sum = fmaf(w, ml[j].y, sum);
+                acc[0] = fmaf(w, u[j].x, acc[0]), acc[1] = fmaf(w, u[j].y, acc[1]);
+                acc[2] = fmaf(w, u[j].z, acc[2]), acc[3] = fmaf(w, u[j].w, acc[3]);
+                acc[4] = fmaf(w, v[j].x, acc[4]), acc[5] = fmaf(w, v[j].y, acc[5]);
+                acc[6] = fmaf(w, v[j].z, acc[6]), acc[7] = fmaf(w, v[j].w, acc[7]);
             }
         }
         const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
         const int tok = (int)div_by(cut.row0 + row, p.by_group);
-        uint16_t* const out =
+        uint4 o;
+        uint32_t* const oo = &o.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oo[e] = pack16(false, acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        *reinterpret_cast<uint4*>(
             p.o + (int64_t)(cut.token0 + tok) * p.ldo +
             (int64_t)(cut.head * p.group + cut.row0 + row - tok * p.group) * p.o_head_stride +
-            lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2)
-            *reinterpret_cast<uint32_t*>(out + e) = pack16(false, acc[e] * inv, acc[e + 1] * inv);
+            oct * 8) = o;
     }
 }
 
-constexpr int kJoinWarps = 8, kJoinSplit = 4;
+constexpr int kJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) nvfp4_attn_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinThreads) nvfp4_attn_join_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int owner = blockIdx.x / kJoinSplit;
-    const Cut cut = p.cuts[owner];
+    const Cut cut = p.cuts[blockIdx.y];
     if (cut.parts <= 0) return;
-    join_rows<D>(p, owner, cut, blockIdx.x % kJoinSplit * kJoinWarps + (threadIdx.x >> 5),
-                 kJoinSplit * kJoinWarps);
+    join_rows<D>(p, blockIdx.y, cut, blockIdx.x * kJoinThreads + threadIdx.x,
+                 gridDim.x * kJoinThreads);
 }
 
 // ---- the kernel --------------------------------------------------------------------------
@@ -505,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_init(&sm.raw_full[i], 1);
             mbar_init(&sm.raw_empty[i], kWidenWarps);
         }
-        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_full, F8 ? kWidenWarps : 1);
         mbar_init(&sm.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -537,7 +558,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     if (left == 0) {
         // nothing to do
     } else if (warp == kTmaWarp || warp == kQWarp) {
-        // ---- what the products read: one warp copies the K tiles, another gathers Q's rows and
+        // ---- what the products read: one warp copies the K tiles, another gathers Q's rows (bf16) and
         // copies the V tiles (of an e4m3 cache, to where they are widened); one warp alone was the
         // kernel's bound with pages of 16 keys.  A tile is TK / box groups of `box` keys of one page
         // each (lane i knows group i's page and place), and a group is a box per panel.  Keys past the
@@ -558,89 +579,33 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         const int step = p.box * (whole_rows ? D : C::kRow);  // bytes of a group (in a panel)
         int slot = 0, it = 0, item = 0;
         uint32_t phase = 1;  // (the first lap finds every place free)
-        // Q's rows in the MMA's layout (K-major, 128-byte swizzle)
+        // Q's rows in the MMA's layout (K-major, 128-byte swizzle): a lane finds the address of a row
+        // in 32, D / 8 lanes copy it
         auto gather = [&]() {
             if (item > 0 &&
                 !(ok = __all_sync(~0u, mbar_wait(&sm.q_free, (item - 1) & 1, stop_v))))
                 return;
             const int row0 = cur.tile * kRows;
             const int rows = min(kRows, cur.q.n * p.group - row0);
-            auto src_of = [&](int r) {
-                const int tok = (int)div_by(row0 + r, p.by_group), h = (row0 + r) - tok * p.group;
-                return p.q + (int64_t)(cur.q.token0 + tok) * p.ldq +
-                       (int64_t)(cur.h * p.group + h) * p.q_head_stride;
-            };
-            if (!F8) {
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes per row, rows at once
-                const int c = lane % kLanes;
-                const uint32_t dst0 = smem_u32(q_tile) + (c >> 3) * (kRows * 128);
+            constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes per row, rows at once
+            const int c = lane % kLanes, sub = lane / kLanes;
+            const uint32_t dst0 = smem_u32(q_tile) + (c >> 3) * (kRows * 128);
+            for (int r0 = 0; r0 < rows; r0 += 32) {
+                const uint16_t* const mine = q_row(p, cur, row0 + min(r0 + lane, rows - 1));
+                const int some = min(32, rows - r0);
 #pragma unroll 4
-                for (int r = lane / kLanes; r < rows; r += kAtOnce)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                                 "l"(src_of(r) + c * 8)
-                                 : "memory");
-                asm volatile("cp.async.wait_all;" ::: "memory");
-            } else {
-                // Q as two e4m3 terms of x = q 2^e, with the row's largest magnitude in [2^7, 2^8): the
-                // first is x rounded to its 4 bits, and what that leaves of bf16's 8 bits is at most 8
-                // of its last place, 4 bits again, so the two are exact down to e4m3's smallest step,
-                // 2^-9: an error of at most 2^-10, 2^-17 of the row's largest value.  D / 8 lanes take
-                // a row, 16 bytes each; a warp reads kBatch such groups of rows before it works on
-                // them, since a row alone is a memory latency.
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
-                const int sub = lane / kLanes, c = lane % kLanes;
-                const int panel = c * 8 / C::kRowKeys, in_row = c * 8 % C::kRowKeys;
-                for (int r0 = 0; r0 < rows; r0 += kAtOnce * kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i * kAtOnce + sub;
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (r < rows)
-                            v[i] = *reinterpret_cast<const uint4*>(src_of(r) + c * 8);
-                    }
-#pragma unroll 1
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i * kAtOnce + sub;
-                        const uint4 x = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t big = 0;  // largest magnitude's bits; NaN and infinity lead
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            big = max(big, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-                        for (int d = kLanes / 2; d; d >>= 1)
-                            big = max(big, __shfl_xor_sync(~0u, big, d));
-                        // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value
-                        // is below 2^-57 has scores of zero to fp32 either way.  An infinity times
-                        // 2^e - 2^e is NaN, as e4m3 has none.
-                        const int up = min(127 + 7 + 127 - (int)(big >> 7), 127 + 64);
-                        const float mul = __uint_as_float((uint32_t)up << 23);
-                        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = __uint_as_float(w[e] << 16) * mul;
-                            const float b = __uint_as_float(w[e] & 0xffff0000u) * mul;
-                            const uint32_t h = e4m3_pair(a, b);
-                            const float2 f = e4m3_values(h);
-                            // (a - a is 0, or NaN where a is infinite)
-                            const uint32_t l = e4m3_pair(a - f.x + (a - a), b - f.y + (b - b));
-                            hi[e >> 1] |= h << (e & 1) * 16;
-                            lo[e >> 1] |= l << (e & 1) * 16;
-                        }
-                        if (r < rows) {
-                            if (c == 0) sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
-                            // 16-byte units turned by the row, as TMA turns K's
-                            const int turn = C::kRow == 128 ? r & 7 : (r >> 1) & 3;
-                            uint8_t* const to = q_tile + panel * (kRows * C::kRow) + r * C::kRow +
-                                                (((in_row >> 4) ^ turn) << 4) + (in_row & 8);
-                            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2*>(to + kRows * D) = make_uint2(lo[0], lo[1]);
-                        }
-                    }
+                for (int i = 0; i < some; i += kAtOnce) {
+                    const int r = r0 + i + sub;
+                    const uint16_t* const src = reinterpret_cast<const uint16_t*>(
+                        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine), i + sub));
+                    if (r < rows)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                                     "l"(src + c * 8)
+                                     : "memory");
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_full);
@@ -648,7 +613,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         while (left > 0 && ok) {
             const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
-            if (second) gather();
+            if (!F8 && second) {
+                gather();
+                if (!ok) break;
+            }
             const int end = key_end(p, cur.q, cur.tile), head = uniform(cur.h);
             const int32_t* const row = p.table + cur.r * p.ld_table;
             // this lane's page and place in unit j of the range
@@ -794,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_wait(&sm.drained[values], 0, &none, 20000000ll);
         }
     } else if (F8 && warp >= kWidenWarp) {
-        // ---- V tiles of an e4m3 cache to f16 in the MMA's layout (K goes to the MMA as it lies, against
+        // ---- with an e4m3 cache: Q in two e4m3 terms, and V tiles to f16 in the MMA's layout (K goes to the MMA as it lies, against
         // Q in two e4m3 terms; for P that would be three conversions per weight).  A piece is 16 codes of a key: two 16-byte units
         // of its row.  Of 8 lanes, four take the four pieces of a panel of an even key and four those
         // of the next panel of the odd key after it, so that neither the loads nor the stores, whose
@@ -808,9 +776,77 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         Ring<NR> raws(0);
         Ring<NV> values(1);
         int item = 0;  // (at most NV <= 4 ahead of the softmax warps')
+        // Q as two e4m3 terms of x = q 2^e, with the row's largest magnitude in [2^7, 2^8): the first
+        // is x rounded to its 4 bits, and what that leaves of bf16's 8 bits is at most 8 of its last
+        // place, 4 bits again, so the two are exact down to e4m3's smallest step, 2^-9: an error of at
+        // most 2^-10, 2^-17 of the row's largest value.  D / 8 lanes take a row, 16 bytes each; a
+        // warp reads kSome such groups of rows at once, since a row alone is a memory latency and
+        // a chain of conversions.  (One warp alone took 45 us for 128 rows at D = 256.)
+        auto split_q = [&]() {
+            constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSome = 4;
+            const int row0 = cur.tile * kRows;
+            const int rows = min(kRows, cur.q.n * p.group - row0);
+            const int sub = lane / kLanes, c = lane % kLanes;
+            const int panel = c * 8 / C::kRowKeys, in_row = c * 8 % C::kRowKeys;
+#pragma unroll 1
+            for (int r0 = (warp - kWidenWarp) * kAtOnce * kSome; r0 < rows;
+                 r0 += kWidenWarps * kAtOnce * kSome) {
+                uint4 v[kSome];
+#pragma unroll
+                for (int i = 0; i < kSome; ++i) {
+                    const int r = min(r0 + i * kAtOnce + sub, rows - 1);
+                    v[i] = __ldg(reinterpret_cast<const uint4*>(q_row(p, cur, row0 + r) + c * 8));
+                }
+#pragma unroll
+                for (int i = 0; i < kSome; ++i) {
+                    const int r = r0 + i * kAtOnce + sub;
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t two = 0;  // largest magnitudes' bits; NaN and infinity lead
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) two = __vmaxu2(two, w[e] & 0x7fff7fffu);
+                    uint32_t big = max(two & 0xffffu, two >> 16);
+#pragma unroll
+                    for (int d = kLanes / 2; d; d >>= 1)
+                        big = max(big, __shfl_xor_sync(~0u, big, d));
+                    // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value is
+                    // below 2^-57 has scores of zero to fp32 either way.  An infinity times
+                    // 2^e - 2^e is NaN, as e4m3 has none.
+                    const int up = min(127 + 7 + 127 - (int)(big >> 7), 127 + 64);
+                    const float mul = __uint_as_float((uint32_t)up << 23);
+                    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = __uint_as_float(w[e] << 16) * mul;
+                        const float b = __uint_as_float(w[e] & 0xffff0000u) * mul;
+                        const uint32_t h = e4m3_pair(a, b);
+                        const float2 f = e4m3_values(h);
+                        // (a - a is 0, or NaN where a is infinite)
+                        const uint32_t l = e4m3_pair(a - f.x + (a - a), b - f.y + (b - b));
+                        hi[e >> 1] |= h << (e & 1) * 16;
+                        lo[e >> 1] |= l << (e & 1) * 16;
+                    }
+                    if (r < rows) {
+                        if (c == 0) sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
+                        // 16-byte units turned by the row, as TMA turns K's
+                        const int turn = C::kRow == 128 ? r & 7 : (r >> 1) & 3;
+                        uint8_t* const to = q_tile + panel * (kRows * C::kRow) + r * C::kRow +
+                                            (((in_row >> 4) ^ turn) << 4) + (in_row & 8);
+                        *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2*>(to + kRows * D) = make_uint2(lo[0], lo[1]);
+                    }
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full);
+        };
         while (left > 0 && ok) {
-            const int cnt = cur.take(left);
+            const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
+            if (item > 0 && !mbar_wait(&sm.q_free, (item - 1) & 1, stop_v)) ok = false;
+            __syncwarp();
+            if (!__all_sync(~0u, ok)) break;
+            split_q();
             const int end = key_end(p, cur.q, cur.tile), open = key_open(p, cur.q, cur.tile);
             for (int i = 0; i < cnt; ++i) {
                 const int rs = raws.slot, ts = values.slot;
@@ -1113,10 +1149,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                             *reinterpret_cast<uint4*>(out + col + e * 8) = w;
                         }
                     } else if (mine) {
-                        float* const dst = p.part_o + (part0 + row) * D + col;
+                        uint4* const dst = reinterpret_cast<uint4*>(p.part_o + part0 * D) +
+                                           col / 4 * kRows + row;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(dst + e * 4) = make_uint4(
+                            dst[e * kRows] = make_uint4(
                                 o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
                     }
                 }
@@ -1127,7 +1164,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     wg * (D / 2), D / 2,
                     p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +
                         (int64_t)(cur.h * p.group + (row0 + row) - tok * p.group) * p.o_head_stride,
-                    whole ? nullptr : p.part_o + (part0 + row) * D);
+                    whole ? nullptr : p.part_o + part0 * D + row * 4);
             tc_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
@@ -1157,7 +1194,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     bar_sync(9, kSoftmaxWarps * 32);
                     if (sm.last) {
                         __threadfence();
-                        join_rows<D>(p, owner, cut, warp, kSoftmaxWarps);
+                        join_rows<D>(p, owner, cut, tid, kSoftmaxWarps * 32);
                         if (tid == 0) p.arrived[owner] = 0;
                     }
                 }
@@ -1227,8 +1264,12 @@ int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int 
     if (p.join_here) return NVFP4_OK;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(grid * kJoinSplit);
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    // a thread for 8 columns of a row, by the average request's rows (16 blocks for each CTA, most of
+    // which have no cut, are a microsecond of launching)
+    const int64_t each = ((int64_t)p.tokens * p.group + p.requests - 1) / p.requests;
+    const int rows = each < kRows ? (int)each : kRows;
+    cfg.gridDim = dim3((rows * (D / 8) + kJoinThreads - 1) / kJoinThreads, grid);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
