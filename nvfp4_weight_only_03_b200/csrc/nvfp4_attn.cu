@@ -146,6 +146,10 @@ struct Params {
     const void* v;     // the cache's values and strides (elements), for what is read without TMA
     int64_t block_stride, slot_stride, head_stride;
     int min_units;     // fewest units worth a CTA of their own
+    // What beginning and ending a row tile costs, in units: Q's rows, the first scores and the epilogue
+    // pass without overlap.  The split counts it, or a CTA with many short row tiles would be the
+    // last by far.
+    int tile_cost;
     float c;           // scale * k_scale * log2(e)
     float v_scale;
     int32_t* error;
@@ -246,15 +250,10 @@ __device__ __forceinline__ int units_of(const Params& p, const Request& q, int t
     return max(1, (key_end(p, q, tile) + TK - 1) / TK);  // 1: rows without keys are written too
 }
 
-// What beginning and ending a row tile costs, in units: Q's rows, the first scores and the
-// epilogue pass without overlap, about as long as two units take.  The split counts it, or a CTA
-// with many short row tiles would be the last by far.
-constexpr int kTileCost = 2;
-
 template <int TK>
 struct Cursor {
     int r, h, tile, tiles, u, n;  // unit u of the row tile's n
-    int lead;                     // how much of kTileCost counts here: all, unless a cut fell in it
+    int lead;                     // how much of tile_cost counts here: all, unless a cut fell in it
     Request q;
     // Units of this row tile in a range with `left` to go; none: the range is done.
     __device__ __forceinline__ int take(int left) const {
@@ -266,7 +265,7 @@ struct Cursor {
     }
     __device__ __forceinline__ void next(const Params& p) {  // the next row tile
         u = 0;
-        lead = kTileCost;
+        lead = p.tile_cost;
         if (++tile == tiles) {
             tile = 0;
             if (++h == p.kv_heads) {
@@ -318,7 +317,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
         const Request q = request_of(p, r);
         const int tiles = row_tiles(p, q);
         int64_t s = 0;
-        for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + kTileCost;
+        for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + p.tile_cost;
         mine += s * p.kv_heads;
     }
     int64_t incl = mine;
@@ -351,7 +350,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
             const Request q = request_of(p, r);
             const int tiles = row_tiles(p, q);
             int64_t s = 0;
-            for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + kTileCost;
+            for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + p.tile_cost;
             if (at >= s * p.kv_heads) {
                 at -= s * p.kv_heads;
                 continue;
@@ -362,10 +361,10 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
             c.h = (int)div64(at, s);
             at -= c.h * s;
             c.tile = 0;
-            while (at >= units_of<TK>(p, q, c.tile) + kTileCost)
-                at -= units_of<TK>(p, q, c.tile++) + kTileCost;
-            c.lead = (int)max((int64_t)kTileCost - at, (int64_t)0);
-            c.u = (int)max(at - kTileCost, (int64_t)0);
+            while (at >= units_of<TK>(p, q, c.tile) + p.tile_cost)
+                at -= units_of<TK>(p, q, c.tile++) + p.tile_cost;
+            c.lead = (int)max((int64_t)p.tile_cost - at, (int64_t)0);
+            c.u = (int)max(at - p.tile_cost, (int64_t)0);
             c.enter(p);
             *start = c;
             break;
@@ -593,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             for (int r0 = 0; r0 < rows; r0 += 32) {
                 const uint16_t* const mine = q_row(p, cur, row0 + min(r0 + lane, rows - 1));
                 const int some = min(32, rows - r0);
-#pragma unroll 4
+#pragma unroll 8
                 for (int i = 0; i < some; i += kAtOnce) {
                     const int r = r0 + i + sub;
                     const uint16_t* const src = reinterpret_cast<const uint16_t*>(
@@ -788,15 +787,24 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const int rows = min(kRows, cur.q.n * p.group - row0);
             const int sub = lane / kLanes, c = lane % kLanes;
             const int panel = c * 8 / C::kRowKeys, in_row = c * 8 % C::kRowKeys;
-#pragma unroll 1
-            for (int r0 = (warp - kWidenWarp) * kAtOnce * kSome; r0 < rows;
-                 r0 += kWidenWarps * kAtOnce * kSome) {
-                uint4 v[kSome];
+            constexpr int kStep = kWidenWarps * kAtOnce * kSome;
+            uint4 ahead[kSome];
+            auto read = [&](int r0) {
 #pragma unroll
                 for (int i = 0; i < kSome; ++i) {
                     const int r = min(r0 + i * kAtOnce + sub, rows - 1);
-                    v[i] = __ldg(reinterpret_cast<const uint4*>(q_row(p, cur, row0 + r) + c * 8));
+                    ahead[i] =
+                        __ldg(reinterpret_cast<const uint4*>(q_row(p, cur, row0 + r) + c * 8));
                 }
+            };
+            int r0 = (warp - kWidenWarp) * kAtOnce * kSome;
+            read(r0);
+#pragma unroll 1
+            for (; r0 < rows; r0 += kStep) {
+                uint4 v[kSome];
+#pragma unroll
+                for (int i = 0; i < kSome; ++i) v[i] = ahead[i];
+                read(r0 + kStep);
 #pragma unroll
                 for (int i = 0; i < kSome; ++i) {
                     const int r = r0 + i * kAtOnce + sub;
@@ -1258,7 +1266,8 @@ int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int 
         }
         ready[dev] = true;
     }
-    p.min_units = 1;
+    p.min_units = 2;
+    p.tile_cost = F8 && D == 256 ? 7 : 4;
     nvfp4_attn_kernel<D, F8><<<grid, C::kThreads, C::kSmem, stream>>>(p, mk, mv);
     if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_LAUNCH;
     if (p.join_here) return NVFP4_OK;
