@@ -192,7 +192,8 @@ def _workspace(kind: str, need: int, index: int, st: int) -> torch.Tensor:
     the graph's own: two graphs never share one."""
     if _capturing():
         ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-        ws[:2048].zero_()  # its words that have to be zero (one per SM, and the error word)
+        if kind == "attn":
+            ws[:2048].zero_()  # its words that have to be zero (one per SM, and the error word)
         return ws
     ws = _workspaces.get((kind, index, st))
     if ws is None or ws.numel() < need:

@@ -21,6 +21,8 @@ import pytest
 import torch
 
 import nvfp4_weight_only_03_b200 as nv
+import synth
+from gpu_util import dev_weight
 
 pytestmark = pytest.mark.gpu
 
@@ -514,3 +516,88 @@ def test_steps_of_a_batch_from_empty_tables(f8):
         check_attention(b)
         lens, head = plan.lens, plan.head
         assert plan.missing.item() == 0
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_attention_half_of_a_layer_captured(f8):
+    """One step of a decode loop as a graph: plan, the q, k, v and gate projections (adapters on q),
+    cache rows, attention, the gated output projection.  Replayed over steps, each result is that
+    of the calls made one by one, and the attention's that of the plain form."""
+    heads, kv_heads, dim, block, k, n = 8, 2, 64, 16, 512, 4
+    g = torch.Generator(device="cuda").manual_seed(33)
+    W = [dev_weight(synth.nvfp4_weight(70 + i, 0, rows, k)) for i, rows in
+         enumerate((heads * dim, kv_heads * dim, kv_heads * dim, heads * dim))]
+    wo = dev_weight(synth.nvfp4_weight(75, 0, k, heads * dim))
+    rank, adapters = 16, 3
+    a = (torch.randn((adapters, rank, k), generator=g, device="cuda") * k ** -0.5).bfloat16()
+    b = (torch.randn((adapters, heads * dim, rank), generator=g, device="cuda") * 0.1).bfloat16()
+    lora = nv.Lora(a, b, ints([0, 2, -1, 1]), torch.tensor([1.0, 0.5, 2.0], device="cuda"))
+    blocks, scale = 24, 0.05 if f8 else 1.0
+    kc, vc = make_cache(g, blocks, block, kv_heads, dim, f8)
+    table = torch.full((n, 5), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(blocks, generator=g, device="cuda").to(torch.int32)
+    lens, head, new = ints([0] * n), ints([0]), ints([1] * n)
+    x = torch.zeros((n, k), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        plan = nv.paged_plan(lens, new, table, free, head, block, tokens=n)
+        q, kk, v, gate = nv.gemv_multi(W, x, lora=[lora, None, None, None])
+        q = q.view(n, heads, dim)
+        nv.kv_append(kk.view(n, kv_heads, dim), v.view(n, kv_heads, dim), kc, vc, plan.slots,
+                     scale, scale)
+        o = nv.paged_attention(q, kc, vc, table, plan.starts, plan.lens, k_scale=scale,
+                               v_scale=scale)
+        y = nv.gemv(*wo, o.view(n, -1), prologue=nv.SigmoidGate(gate))
+        lens.copy_(plan.lens)
+        head.copy_(plan.head)
+        return plan, q, o, y
+
+    step()  # (loads the kernels)
+    for t in (lens, head):
+        t.zero_()
+    table.fill_(-1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan, q, o, y = step()
+    for i in range(40):
+        x.copy_(torch.randn((n, k), generator=g, device="cuda").bfloat16())
+        graph.replay()
+        assert lens.tolist() == [i + 1] * n and plan.missing.item() == 0
+        if i % 13:
+            continue
+        t = Batch.__new__(Batch)
+        t.lens, t.new, t.f8, t.dim, t.heads, t.kv_heads = [i + 1] * n, [1] * n, f8, dim, heads, \
+            kv_heads
+        t.kc, t.vc, t.k_scale, t.v_scale, t.table = kc, vc, scale, scale, table
+        t.q, t.tokens, t.starts, t.scale = q, n, plan.starts, dim ** -0.5
+        t.block, t.blocks, t.cols = block, blocks, table.shape[1]
+        assert torch.equal(check_attention(t), o)
+        q2, _, _, gate = nv.gemv_multi(W, x, lora=[lora, None, None, None])
+        assert torch.equal(q2.view_as(q), q)
+        assert torch.equal(nv.gemv(*wo, o.view(n, -1), prologue=nv.SigmoidGate(gate)), y)
+
+
+def test_two_graphs_at_once():
+    """Two captured calls replayed on two streams, over and over: each has a workspace of its own."""
+    batches = [Batch(50, [5000], [1], 24, 4, 256, 16), Batch(51, [900, 3100], [40, 8], 12, 2, 256, 32)]
+    want = [b.call() for b in batches]
+    graphs, outs = [], []
+    for b in batches:
+        lens, out = ints(b.lens), torch.empty_like(b.q)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            nv.paged_attention(b.q, b.kc, b.vc, b.table, b.starts, lens, scale=b.scale, out=out)
+        graphs.append((graph, lens))
+        outs.append(out)
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for (graph, _), stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert torch.equal(out, w)
