@@ -470,6 +470,14 @@ def test_plan(requests, block):
     check_plan(lens, new, block, 541, pages + 9, 4, sum(new) + 7)
 
 
+@pytest.mark.parametrize("requests", [2561, 3050, 3071, nv.MAX_REQUESTS])
+def test_plan_of_many_requests(requests):
+    rng = np.random.default_rng(requests)
+    lens, new = rng.integers(0, 60, requests), rng.integers(0, 3, requests)
+    check_plan([int(v) for v in lens], [int(v) for v in new], 16, 5, 4 * requests, 2,
+               int(new.sum()) + 9)
+
+
 def test_plan_runs_out():
     check_plan([10, 0, 30, 16], [10, 50, 3, 1], 16, 3, 4, 2, 70)   # list spent, table too short
     check_plan([10, 0, 30, 16], [10, 50, 3, 1], 16, 9, 2, 2, 64)   # nothing left
