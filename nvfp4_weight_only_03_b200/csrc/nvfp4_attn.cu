@@ -503,13 +503,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     // (the tiles' swizzle wants 1024-byte alignment, which the block's only allocation has)
     if (smem_u32(smem_raw) & 1023u) {
         if (threadIdx.x == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             atomicCAS(p.error, 0, 10);
             p.cuts[blockIdx.x].parts = 0;
         }
         return;
     }
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == kScoresWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sm.tmem)),
@@ -541,6 +541,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         prefetch_map(&map_k);
         prefetch_map(&map_v);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_before_sync();
     Cursor<TK>* const start = reinterpret_cast<Cursor<TK>*>(sm.start[0]);
     static_assert(sizeof(Cursor<TK>) <= sizeof(sm.start[0]) && C::kThreads / 32 <= 20, "Small");
@@ -1268,28 +1270,16 @@ int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int 
     }
     p.min_units = 2;
     p.tile_cost = F8 && D == 256 ? 7 : 4;
-    nvfp4_attn_kernel<D, F8><<<grid, C::kThreads, C::kSmem, stream>>>(p, mk, mv);
-    if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_LAUNCH;
-    if (p.join_here) return NVFP4_OK;
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
+    const int st = nvfp4_host::launch_behind(nvfp4_attn_kernel<D, F8>, grid, C::kThreads, C::kSmem, 0,
+                                             stream, p, mk, mv);
+    if (st != NVFP4_OK || p.join_here) return st;
     // a thread for 8 columns of a row, by the average request's rows (16 blocks for each CTA, most of
     // which have no cut, are a microsecond of launching)
     const int64_t each = ((int64_t)p.tokens * p.group + p.requests - 1) / p.requests;
     const int rows = each < kRows ? (int)each : kRows;
-    cfg.gridDim = dim3((rows * (D / 8) + kJoinThreads - 1) / kJoinThreads, grid);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, nvfp4_attn_join_kernel<D>, p) != cudaSuccess) {
-        cudaGetLastError();
-        return NVFP4_ERR_LAUNCH;
-    }
-    return NVFP4_OK;
+    return nvfp4_host::launch_behind(
+        nvfp4_attn_join_kernel<D>, dim3((rows * (D / 8) + kJoinThreads - 1) / kJoinThreads, grid),
+        kJoinThreads, 0, 0, stream, p);
 }
 
 }  // namespace

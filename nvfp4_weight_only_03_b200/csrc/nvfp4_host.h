@@ -28,6 +28,29 @@ inline bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
     return a && b && na && nb && pa < pb + nb && pb < pa + na;
 }
 
+// Launches a kernel whose blocks may be set up while the work before it on the stream ends; it waits
+// (griddepcontrol.wait) before it reads or writes anything.  cluster 0: no cluster.
+template <typename... P, typename... A>
+int launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                  cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return NVFP4_OK;
+    cudaGetLastError();
+    return NVFP4_ERR_LAUNCH;
+}
+
 // Clears a failed launch's error and turns it into a status.
 inline int launched() { return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH; }
 

@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(kDownThreads, 3) nvfp4_lora_down_kernel(const 
     __shared__ Groups g;
     __shared__ __align__(16) float part[kDownWarps][kColTiles][16][8];
     __shared__ __align__(16) float sum[kColTiles * 128];
+    // (the second kernel reads y and the index as soon as it may start: not before this one may)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const auto cluster = cooperative_groups::this_cluster();
     const int ctas = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
@@ -475,22 +477,10 @@ int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const v
     if (any) {
         const int64_t groups = m < l.adapters ? m : l.adapters;
         const int ctas = choose_cluster(m, l.adapters, l.rank, k, sms);
-        cudaLaunchConfig_t cfg;
-        memset(&cfg, 0, sizeof(cfg));
-        cfg.gridDim = dim3((unsigned)(groups * (p.rank16 / 16) * ctas));
-        cfg.blockDim = dim3(kDownThreads);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = ctas;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, nvfp4_lora_down_kernel, p) != cudaSuccess) {
-            cudaGetLastError();
-            return NVFP4_ERR_LAUNCH;
-        }
+        st = nvfp4_host::launch_behind(nvfp4_lora_down_kernel,
+                                       dim3((unsigned)(groups * (p.rank16 / 16) * ctas)),
+                                       kDownThreads, 0, ctas, stream, p);
+        if (st != NVFP4_OK) return st;
     }
     if (p.rank <= 32) return launch_up<1>(p, sms, any, stream);
     if (p.rank <= 64) return launch_up<2>(p, sms, any, stream);

@@ -14,7 +14,6 @@
 
 namespace {
 
-using nvfp4_host::launched;
 using nvfp4_host::misaligned;
 using nvfp4_host::overlaps;
 
@@ -82,6 +81,7 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
     int64_t* const first = sums + p.requests;
     __shared__ int64_t warp_sum[3][kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int64_t carry_tok = 0, carry_page = 0, lost = 0;
     for (int base = 0; base < p.requests; base += kPlanThreads) {
         const int r = base + tid;
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const Appe
     const int log_per = 31 - __clz(per);
     const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
     const int64_t me = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t i = me; i < 2 * p.tokens; i += warps) {
         const int64_t t = i >> 1;
         const int which = (int)(i & 1);
@@ -355,8 +356,7 @@ int nvfp4_paged_plan(const nvfp4_paged_plan_t* plan, cudaStream_t stream) {
     }
     const int64_t want = (a.tokens + a.requests + kPlanThreads - 1) / kPlanThreads;
     const int grid = (int)(want < 1 ? 1 : want > sms ? sms : want);
-    nvfp4_plan_kernel<<<grid, kPlanThreads, smem, stream>>>(p);
-    return launched();
+    return nvfp4_host::launch_behind(nvfp4_plan_kernel, grid, kPlanThreads, smem, 0, stream, p);
 }
 
 int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const void* v, int64_t ldv,
@@ -416,11 +416,9 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     p.block = c.block_size;
     const int64_t want = (tokens * 2 * 32 + kAppendThreads - 1) / kAppendThreads;  // a warp per row
     const int grid = (int)(want > 8 * sms ? 8 * sms : want);
-    if (c.type == NVFP4_KV_E4M3)
-        nvfp4_append_kernel<true><<<grid, kAppendThreads, 0, stream>>>(p);
-    else
-        nvfp4_append_kernel<false><<<grid, kAppendThreads, 0, stream>>>(p);
-    return launched();
+    return nvfp4_host::launch_behind(
+        c.type == NVFP4_KV_E4M3 ? nvfp4_append_kernel<true> : nvfp4_append_kernel<false>, grid,
+        kAppendThreads, 0, 0, stream, p);
 }
 
 }  // extern "C"
