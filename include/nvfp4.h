@@ -477,7 +477,8 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
  * with kv head h / (heads / cache->heads), key j at slot j % block_size of page
  * table[r][j / block_size].  Keys whose page is not in 0..blocks-1, or lies beyond table_columns,
  * are not there; a token that sees no key gives zeros.  Rows of o behind the last token stay as
- * they were.  What cache slots hold that no token sees has no effect, whatever it is.
+ * they were.  What cache slots hold that a token does not see has no effect on it, whatever it is
+ * (keys or values that are infinite or NaN reach the tokens that see them, and no others).
  *   q, o: bf16, head h of token t at q + t*ldq + h*q_head_stride; 16-byte aligned, strides
  *   multiples of 8 and >= dim; o may not overlap q.   heads % cache->heads == 0
  *   scale: > 0 (scale * k_scale a normal fp32 number) */

@@ -9,7 +9,7 @@
 // * Rows: the query heads that share a kv head are rows of one matrix product, row g of a request
 //   being (token g / G, head g % G); 128 rows are a tile (the MMA's M), so a key or value row
 //   leaves HBM once per tile and kv head.  A decode step fills 6 of the 128 rows: the tensor
-//   cores have the time (512 cycles of MMA against some 2500 of HBM per 64 KB of cache), and one
+//   cores have the time (1024 cycles of MMA against some 2800 of HBM per 64 KB of cache), and one
 //   kernel serves every row count.
 // * Work: units of TK keys of one (request, kv head, row tile).  All units in order are cut into
 //   equal ranges, one per CTA (one CTA per SM), from the lengths in device memory: the host knows
@@ -22,12 +22,21 @@
 //   memory; it is rescaled only when a row's maximum rose by more than 2^8 (P is then at most
 //   2^8 and the sums are fp32, so nothing overflows).  S and P have two buffers each, so the MMAs
 //   of one unit run under the softmax of another.
-// * Roles: 8 softmax warps, one warp each for the scores' MMAs, the values' MMAs, K, and Q and V, and 4
-//   that widen the V of an e4m3 cache to f16 (exact); all else goes to the MMA as it lies in memory.
-// * P is rounded to the MMA's 16-bit type (bf16, or f16 with the e4m3 cache): half a step, 2^-9
-//   (2^-12) of each weight.  With the e4m3 cache K is read by 8-bit MMAs as it lies, q being carried
+// * Roles: 8 softmax warps, one warp each for the scores' MMAs, the values' MMAs, K, and Q and V; with
+//   an e4m3 cache 4 more that widen V to f16 (exact) and split Q.  All else goes to the MMA as it lies
+//   in memory.  The roles share the instruction cache, so an instruction costs 4 to 10 cycles: uniform
+//   operands, elected lanes and short loops decide the time more than their count of operations.
+// * P is rounded to the MMA's 16-bit type (bf16, or f16 with the e4m3 cache): half a step, 2^-8
+//   (2^-11) of each weight.  With the e4m3 cache K is read by 8-bit MMAs as it lies, q being carried
 //   as two e4m3 terms times a power of two per row (an error of at most 2^-17 of the row's largest).
 //   S, O, maxima and sums are fp32.
+// * Measured (B200, calls of a captured graph): 64 requests of up to 8192 keys, 24 heads on 4 of
+//   256, one token each: 167 us, 6.0 TB/s, 93% of the copy rate; one request of 131072 keys: 103 us,
+//   80% (parts of its 4 heads' single row tiles are joined by one CTA each); 16 requests x 8 tokens,
+//   e4m3, 32 heads on 8 of 128: 96 us, 46% (widening V and the one softmax warp that has rows);
+//   2048 tokens over 16384 keys: 680 us, 1140 TFLOP/s, 67% of the matrix rate (shared memory, out
+//   of which Q is read again for every unit).  The least call is some 8 us: lengths, first pages,
+//   keys, scores, weights and values follow on one another, each with its latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -129,7 +138,10 @@ inline Divisor divisor_of(uint32_t d) {
     }
     return r;
 }
-__device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
+// a / b, neither negative.  A 64-bit division takes half a microsecond.
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b) {
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 
 struct Params {
     const uint16_t* q;
@@ -337,7 +349,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
     before += incl - mine;
     Range g;
     g.total = total;
-    const int64_t most = (total + p.min_units - 1) / p.min_units;
+    const int64_t most = div64(total + p.min_units - 1, p.min_units);
     g.ctas = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
     g.begin = g.end = 0;
     if ((int)blockIdx.x < g.ctas) {
@@ -763,9 +775,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             mbar_wait(&sm.drained[values], 0, &none, 20000000ll);
         }
     } else if (F8 && warp >= kWidenWarp) {
-        // ---- with an e4m3 cache: Q in two e4m3 terms, and V tiles to f16 in the MMA's layout (K goes to the MMA as it lies, against
-        // Q in two e4m3 terms; for P that would be three conversions per weight).  A piece is 16 codes of a key: two 16-byte units
-        // of its row.  Of 8 lanes, four take the four pieces of a panel of an even key and four those
+        // ---- with an e4m3 cache: Q in two e4m3 terms, and V tiles to f16 in the MMA's layout (K goes
+        // to the MMA as it lies; for P the two terms would be three conversions per weight).  A piece is
+        // 16 codes of a key: two 16-byte units of its row.  Of 8 lanes, four take the four pieces of a panel of an even key and four those
         // of the next panel of the odd key after it, so that neither the loads nor the stores, whose
         // units are turned by the key's number, meet in a bank.
         constexpr int kKeys = kWidenWarps * 8, P = D / 64;  // keys at once; panels of a key

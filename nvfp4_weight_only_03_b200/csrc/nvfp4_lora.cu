@@ -3,7 +3,8 @@
 //   out[m] = bf16( y[m] + scale_a * B_a (A_a x[m]) ),   a = index[m];  out[m] = y[m] without one
 //
 // * Two kernels: the first forms T = A x (rank values per row), the second adds B T.  Rows that
-//   share an adapter form a group, found from `index` by every CTA itself (at most 128 rows), so each adapter leaves HBM once and the host needs no copy of the index.
+//   share an adapter form a group, found from `index` by every CTA itself (at most 128 rows), so
+//   each adapter leaves HBM once and the host needs no copy of the index.
 // * HBM bound: rank * (K + N) bf16 per adapter against a few rows.  The weights go from global
 //   memory straight into mma.sync fragments, 16 bytes per lane and load: k (and the rank) may be
 //   permuted as long as both operands are, so a lane's 8 consecutive values serve as the 4 pairs
@@ -17,6 +18,11 @@
 //   2^-17; the only other rounding is the output's.
 // * The second kernel is launched while the first runs and has its groups, its first weights and y
 //   before it waits for T.
+// * Measured (B200, calls of a captured graph): 128 rows over 48 adapters of rank 64, 10240 x 5120:
+//   27.6 us, 3.4 TB/s, 52% of the copy rate (two kernels of 5 and 9 us of traffic, each with its
+//   start and its last wave); one row of rank 16: 5.5 us, latency alone.  One kernel with a cluster
+//   per 16 rows of a group for both products took 36.5 and 8.2 us: eight SMs per adapter draw too
+//   little.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

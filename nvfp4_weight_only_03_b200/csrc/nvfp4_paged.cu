@@ -29,7 +29,8 @@ using nvfp4_host::overlaps;
 // and then takes its share of the tokens and of the new pages, finding a token's (a page's)
 // request by binary search.  Nothing is read that another CTA writes: an entry that this call
 // fills is taken from the free list again instead of from the table.  Latency bound: the chain
-// is lengths -> sums -> search -> table -> slot.
+// is lengths -> sums -> search -> table -> slot: 4.2 us for 32 requests, 6.6 us for 1024 with 10200
+// tokens (B200).
 constexpr int kPlanThreads = 512;
 
 struct PlanParams {
@@ -171,7 +172,8 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
 // ------------------------------------------------------------------------------------------
 // Append.  A warp per token and side (K or V); a lane moves pieces of 16 bytes of the cache (8 bf16
 // values, or 16 codes), so loads and stores are whole sectors and the slot is looked up once per
-// row.  HBM bound, 4 bytes of traffic per value (3 with an 8-bit cache).
+// row.  HBM bound, 4 bytes of traffic per value (3 with an 8-bit cache).  Measured (B200): 8192 tokens
+// of 4 heads of 256 into an e4m3 cache 12.7 us, 55% of the copy rate; 128 tokens, bf16, 2.5 us.
 //
 // An e4m3 code is e4m3_rn(x / scale) of the fp32 quotient, saturated at 448.  A division per value was
 // the bound (a hundred instructions per eight values).  The quotient is formed from 1 / scale in two
