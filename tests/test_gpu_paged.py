@@ -292,6 +292,11 @@ def test_many_requests_and_long_context(f8):
     check_attention(Batch(11, [3001, 2500], [500, 333], 12, 2, 128, 16, f8))
 
 
+@pytest.mark.parametrize("lens,new", [([6001], [600]), ([2200, 700, 4100], [500, 700, 31])])
+def test_chunks_with_many_units_per_row_tile(lens, new):
+    check_attention(Batch(40, lens, new, 24, 4, 256, 32))
+
+
 def test_rows_behind_the_last_token_stay():
     b = Batch(12, [40, 50], [3, 1], 8, 2, 128, 16, pad=5)
     out = torch.full_like(b.q, 7.0)
