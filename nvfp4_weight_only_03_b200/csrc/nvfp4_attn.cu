@@ -1362,11 +1362,16 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
                                            : row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                                         : CU_TENSOR_MAP_SWIZZLE_64B;
         const cuuint32_t one[4] = {1, 1, 1, 1};
+        // L2 fetches no more of a line than the head's row has: the next head's is another CTA's, later
+        const CUtensorMapL2promotion promotion = kv.dim * size >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                                 : kv.dim * size >= 128
+                                                     ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                     : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
         // without pages nothing is read: every box then lies outside, on any valid address
         void* const at = const_cast<void*>(kv.blocks ? tensors[i] : workspace);
         if (encode(&maps[i], f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                    4, at, dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   swizzle, promotion,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return NVFP4_ERR_LAUNCH;
     }

@@ -19,8 +19,8 @@
 // * The second kernel is launched while the first runs and has its groups, its first weights and y
 //   before it waits for T.
 // * Measured (B200, calls of a captured graph): 128 rows over 48 adapters of rank 64, 10240 x 5120:
-//   27.6 us, 3.4 TB/s, 52% of the copy rate (two kernels of 5 and 9 us of traffic, each with its
-//   start and its last wave); one row of rank 16: 5.5 us, latency alone.  One kernel with a cluster
+//   23.9 us, 3.9 TB/s, 60% of the copy rate (two kernels of 5 and 9 us of traffic, each with its
+//   start and its last wave); one row of rank 16: 5.4 us, latency alone.  One kernel with a cluster
 //   per 16 rows of a group for both products took 36.5 and 8.2 us: eight SMs per adapter draw too
 //   little.
 #include <cooperative_groups.h>
@@ -264,8 +264,12 @@ __global__ void __launch_bounds__(kDownThreads, 3) nvfp4_lora_down_kernel(const 
 }
 
 // ---- out = y + B T -----------------------------------------------------------------------
+// CTAs that an SM holds at once (more than that at rank 64, in a second wave: 27.4 us, not 23.9).
+template <int STEPS>
+constexpr int kUp = STEPS == 1 ? 6 : STEPS == 2 ? 5 : 3;
+
 template <int STEPS>  // 32 ranks each
-__global__ void __launch_bounds__(kThreads, STEPS > 2 ? 3 : STEPS > 1 ? 5 : 6)
+__global__ void __launch_bounds__(kThreads, kUp<STEPS>)
     nvfp4_lora_up_kernel(const Params p) {
     __shared__ Groups g;
     find_groups(p, g);
@@ -392,7 +396,7 @@ int launch_up(const Params& p, int sms, bool after_down, cudaStream_t stream) {
     const int64_t items = groups * ((p.n + kChunkN - 1) / kChunkN);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)(items < 6 * sms ? items : 6 * sms));
+    cfg.gridDim = dim3((unsigned)(items < kUp<STEPS> * sms ? items : kUp<STEPS> * sms));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
