@@ -464,7 +464,8 @@ int nvfp4_paged_plan(const nvfp4_paged_plan_t* plan, cudaStream_t stream);
  * negative or past the last page are skipped.  An e4m3 cache stores e4m3_rn(x / scale) of the
  * fp32 quotient, saturated at +-448 (NaN stays NaN).  Slots that occur twice leave, value by
  * value, one of their rows.
- *   k, v 16-byte aligned;  strides >= dim and multiples of 8;  the cache overlaps no input.
+ *   k, v 16-byte aligned;  strides >= dim and multiples of 8;  the cache overlaps no input, and its
+ *   K and V are not one.
  * Errors: NVFP4_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARCH, _LAUNCH. */
 int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const void* v, int64_t ldv,
                     int64_t v_head_stride, int64_t tokens, const int32_t* slots,
@@ -480,7 +481,7 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
  * they were.  What cache slots hold that a token does not see has no effect on it, whatever it is
  * (keys or values that are infinite or NaN reach the tokens that see them, and no others).
  *   q, o: bf16, head h of token t at q + t*ldq + h*q_head_stride; 16-byte aligned, strides
- *   multiples of 8 and >= dim; o may not overlap q.   heads % cache->heads == 0
+ *   multiples of 8 and >= dim; o overlaps nothing that the call reads.   heads % cache->heads == 0
  *   scale: > 0 (scale * k_scale a normal fp32 number) */
 typedef struct {
     const void* q;
@@ -536,7 +537,7 @@ typedef struct {
 int nvfp4_lora_workspace_bytes(int m, int adapters, int rank, int64_t k, size_t* bytes);
 
 /* M = 0..NVFP4_MAX_ROWS rows.  out may be y itself (same leading dimension); otherwise it overlaps
- * neither y nor x.  workspace: 16-byte aligned, the above bytes, of any content; it holds no error
+ * nothing that the call reads.  workspace: 16-byte aligned, the above bytes, of any content; it holds no error
  * word (nothing in the call waits).  Calls that may run at the same time need different ones.
  * Errors: NVFP4_ERR_NULL, _SHAPE, _ROWS, _ALIGN, _ALIAS, _WORKSPACE, _ARCH, _LAUNCH. */
 int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const void* y,

@@ -1329,9 +1329,15 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
         misaligned(a.lens, 4) || misaligned(a.table, 4) || a.ldq % 8 || a.q_head_stride % 8 ||
         a.ldo % 8 || a.o_head_stride % 8)
         return NVFP4_ERR_ALIGN;
-    const uint64_t qb = 2ull * ((a.tokens - 1) * a.ldq + (a.heads - 1) * a.q_head_stride + kv.dim);
-    const uint64_t ob = 2ull * ((a.tokens - 1) * a.ldo + (a.heads - 1) * a.o_head_stride + kv.dim);
-    if (overlaps(a.o, ob, a.q, qb)) return NVFP4_ERR_ALIAS;
+    using nvfp4_host::span;
+    const uint64_t ob = 2 * span(1, 0, a.tokens, a.ldo, a.heads, a.o_head_stride, kv.dim);
+    const uint64_t cb = kv.blocks ? nvfp4_host::cache_bytes(kv) : 0;
+    if (overlaps(a.o, ob, a.q, 2 * span(1, 0, a.tokens, a.ldq, a.heads, a.q_head_stride, kv.dim)) ||
+        overlaps(a.o, ob, kv.k, cb) || overlaps(a.o, ob, kv.v, cb) ||
+        overlaps(a.o, ob, a.table, 4 * span(1, 0, 1, 0, a.requests, a.ld_table, a.table_columns)) ||
+        overlaps(a.o, ob, a.starts, 4ull * a.requests + 4) ||
+        overlaps(a.o, ob, a.lens, 4ull * a.requests))
+        return NVFP4_ERR_ALIAS;
     if (!workspace || misaligned(workspace, 16)) return NVFP4_ERR_WORKSPACE;
     int dev, sms;
     nvfp4_host::EncodeFn encode;
@@ -1339,6 +1345,7 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     if (st != NVFP4_OK) return st;
     const Layout w = workspace_layout(sms, kv.dim);
     if (workspace_bytes < w.total) return NVFP4_ERR_WORKSPACE;
+    if (overlaps(a.o, ob, workspace, w.total)) return NVFP4_ERR_ALIAS;
 
     const bool f8 = kv.type == NVFP4_KV_E4M3;
     const int tk = kv.dim == 256 ? 64 : 128;
@@ -1401,8 +1408,8 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     p.block_stride = kv.block_stride;
     p.slot_stride = kv.slot_stride;
     p.head_stride = kv.head_stride;
-    const int64_t cap = a.table_columns * kv.block_size;
-    p.capacity = (int)(cap > INT32_MAX - 1024 ? INT32_MAX - 1024 : cap);
+    const int64_t cap = a.table_columns * kv.block_size;  // (below 2^51)
+    p.capacity = (int)(cap > INT32_MAX - 8192 ? INT32_MAX - 8192 : cap);
     p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;
     p.v_scale = f8 ? kv.v_scale * kWidened : 1.f;
     // a factor that left fp32's normal range would turn a masked score of -infinity into NaN

@@ -28,6 +28,20 @@ inline bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
     return a && b && na && nb && pa < pb + nb && pb < pa + na;
 }
 
+// Elements from the first to the last of [n0][n1][n2][inner] with these strides, at most 2^60.
+inline uint64_t span(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2,
+                     int64_t inner) {
+    const unsigned __int128 n = (unsigned __int128)(n0 - 1) * s0 + (unsigned __int128)(n1 - 1) * s1 +
+                                (unsigned __int128)(n2 - 1) * s2 + inner;
+    return n >> 60 ? 1ull << 60 : (uint64_t)n;
+}
+
+// Bytes that K (or V) of a cache with at least one page takes.
+inline uint64_t cache_bytes(const nvfp4_kv_cache_t& c) {
+    return (c.type == NVFP4_KV_E4M3 ? 1ull : 2ull) * span(c.blocks, c.block_stride, c.block_size,
+                                                          c.slot_stride, c.heads, c.head_stride, c.dim);
+}
+
 // Launches a kernel whose blocks may be set up while the work before it on the stream ends; it waits
 // (griddepcontrol.wait) before it reads or writes anything.  cluster 0: no cluster.
 template <typename... P, typename... A>

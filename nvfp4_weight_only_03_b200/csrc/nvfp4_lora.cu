@@ -448,10 +448,18 @@ int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const v
         misaligned(l.ranks, 4) || ldx % 8 || ldy % 8 || ldo % 8 || l.a_ld % 8 || l.b_ld % 8 ||
         l.a_stride % 8 || l.b_stride % 8)
         return NVFP4_ERR_ALIGN;
-    const uint64_t ob = 2ull * ((uint64_t)(m - 1) * ldo + n), yb = 2ull * ((uint64_t)(m - 1) * ldy + n);
+    using nvfp4_host::span;
+    const uint64_t ob = 2 * span(1, 0, 1, 0, m, ldo, n), yb = 2 * span(1, 0, 1, 0, m, ldy, n);
     // in place is y itself, row for row
     if (overlaps(out, ob, y, yb) && !(out == y && (ldo == ldy || m == 1))) return NVFP4_ERR_ALIAS;
-    if (any && overlaps(out, ob, x, 2ull * ((uint64_t)(m - 1) * ldx + k))) return NVFP4_ERR_ALIAS;
+    if (overlaps(out, ob, l.index, 4ull * m) || overlaps(out, ob, workspace, t_bytes(m, l.rank)))
+        return NVFP4_ERR_ALIAS;
+    if (any && (overlaps(out, ob, x, 2 * span(1, 0, 1, 0, m, ldx, k)) ||
+                overlaps(out, ob, l.a, 2 * span(1, 0, l.adapters, l.a_stride, l.rank, l.a_ld, k)) ||
+                overlaps(out, ob, l.b, 2 * span(1, 0, l.adapters, l.b_stride, n, l.b_ld, l.rank)) ||
+                overlaps(out, ob, l.scales, 4ull * l.adapters) ||
+                overlaps(out, ob, l.ranks, 4ull * l.adapters)))
+        return NVFP4_ERR_ALIAS;
     int dev, sms;
     nvfp4_host::EncodeFn encode;
     st = nvfp4_host::device(&dev, &sms, &encode);

@@ -314,7 +314,7 @@ int nvfp4_paged_plan(const nvfp4_paged_plan_t* plan, cudaStream_t stream) {
     const uint64_t rb = 4ull * a.requests, tb = 4ull * a.tokens;
     const uint64_t bytes[] = {
         rb, rb,
-        a.requests ? 4ull * ((uint64_t)(a.requests - 1) * a.ld_table + a.table_columns) : 0,
+        a.requests ? 4 * nvfp4_host::span(1, 0, 1, 0, a.requests, a.ld_table, a.table_columns) : 0,
         4ull * a.free_count, 4, rb + 4, rb, tb, a.request ? tb : 0, a.positions ? tb : 0, 4, 4};
     const int inputs[] = {0, 1, 3, 4}, outputs[] = {2, 5, 6, 7, 8, 9, 10, 11};
     for (int i = 0; i < 8; ++i) {
@@ -375,13 +375,11 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 4) || ldk % 8 || ldv % 8 ||
         k_head_stride % 8 || v_head_stride % 8)
         return NVFP4_ERR_ALIGN;
-    const int size = c.type == NVFP4_KV_E4M3 ? 1 : 2;
-    const uint64_t cache_bytes = (uint64_t)size * ((c.blocks - 1) * c.block_stride +
-                                                   (c.block_size - 1) * c.slot_stride +
-                                                   (c.heads - 1) * c.head_stride + c.dim);
-    const uint64_t kb = 2ull * ((tokens - 1) * ldk + (c.heads - 1) * k_head_stride + c.dim);
-    const uint64_t vb = 2ull * ((tokens - 1) * ldv + (c.heads - 1) * v_head_stride + c.dim);
+    const uint64_t cache_bytes = nvfp4_host::cache_bytes(c);
+    const uint64_t kb = 2 * nvfp4_host::span(1, 0, tokens, ldk, c.heads, k_head_stride, c.dim);
+    const uint64_t vb = 2 * nvfp4_host::span(1, 0, tokens, ldv, c.heads, v_head_stride, c.dim);
     const void* caches[2] = {c.k, c.v};
+    if (c.k == c.v) return NVFP4_ERR_ALIAS;  // (they may lie in one buffer, page by page)
     for (const void* dst : caches)
         if (overlaps(dst, cache_bytes, k, kb) || overlaps(dst, cache_bytes, v, vb) ||
             overlaps(dst, cache_bytes, slots, 4ull * tokens))

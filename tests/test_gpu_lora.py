@@ -159,3 +159,16 @@ def test_beside_the_projection():
     assert torch.equal(q, want) and torch.equal(p, base)
     with pytest.raises(ValueError):  # the adapters' x is the prologue's result, kept in the call
         nv.gemv(W, S, g, x, lora=lora, prologue=nv.SigmoidGate(x))
+    one = nv.Lora(a, b, ints([2]), scales)  # a row as a vector, as gemv takes it
+    assert torch.equal(nv.gemv(W, S, g, x[1], lora=one).view(-1), want[1])
+
+
+def test_another_stream():
+    y, x, a, b, scales = inputs(8, 5, 264, 520, 3, 24)
+    index = ints([0, 2, 1, -1, 2])
+    want = nv.lora_add(y, x, a, b, index, scales)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    out = nv.lora_add(y, x, a, b, index, scales, stream=stream)
+    stream.synchronize()
+    assert torch.equal(out, want)

@@ -297,6 +297,13 @@ def test_chunks_with_many_units_per_row_tile(lens, new):
     check_attention(Batch(40, lens, new, 24, 4, 256, 32))
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(1, 1, 64), (160, 1, 64), (258, 2, 128), (128, 1, 256)])
+def test_head_groups(heads, kv_heads, dim, f8):
+    # a group of more than 128 heads is several row tiles of a token
+    check_attention(Batch(60, [77, 130, 300, 9], [1, 5, 1, 9], heads, kv_heads, dim, 16, f8))
+
+
 def test_rows_behind_the_last_token_stay():
     b = Batch(12, [40, 50], [3, 1], 8, 2, 128, 16, pad=5)
     out = torch.full_like(b.q, 7.0)

@@ -111,6 +111,7 @@ def test_append_refuses_a_cache(L, kw, status):
     (dict(k=at(0) + 8), ALIGN), (dict(slots=at(2) + 2), ALIGN), (dict(ldk=516), ALIGN),
     (dict(hk=132), ALIGN),
     (dict(k=at(20) + 1024), ALIAS), (dict(v=at(21) - 16), ALIAS), (dict(slots=at(20)), ALIAS),
+    (dict(cache=dict(v=at(20))), ALIAS), (dict(ldk=2 ** 62), ALIAS),  # (reaches everything)
 ])
 def test_append_refuses(L, kw, status):
     assert append(L, **kw) == status
@@ -155,7 +156,9 @@ def test_attention_refuses_a_cache(L, kw, status):
     (dict(table=None), NULL),
     (dict(q=at(0) + 8), ALIGN), (dict(o=at(1) + 4), ALIGN), (dict(ldq=1028), ALIGN),
     (dict(o_head_stride=132), ALIGN), (dict(table=at(2) + 2), ALIGN),
-    (dict(o=at(0)), ALIAS), (dict(o=at(0) + 1024), ALIAS),
+    (dict(o=at(0)), ALIAS), (dict(o=at(0) + 1024), ALIAS), (dict(o=at(20) + 64), ALIAS),
+    (dict(o=at(21)), ALIAS), (dict(o=at(2)), ALIAS), (dict(o=at(3)), ALIAS), (dict(o=at(4)), ALIAS),
+    (dict(ldo=2 ** 61), ALIAS), (dict(ldq=2 ** 61), ALIAS),
     (dict(ws=None), WORKSPACE), (dict(ws=at(5) + 8), WORKSPACE),
 ])
 def test_attention_refuses(L, kw, status):
@@ -199,6 +202,8 @@ def lora(L, x=at(5), ldx=256, y=at(6), ldy=512, out=at(7), ldo=512, m=3, n=512, 
     (dict(ldx=260), ALIGN), (dict(b_ld=20), ALIGN), (dict(a_stride=4100), ALIGN),
     (dict(index=at(4) + 2), ALIGN), (dict(ranks=at(3) + 1), ALIGN),
     (dict(out=at(6) + 1024), ALIAS), (dict(out=at(6), ldo=520), ALIAS), (dict(out=at(5)), ALIAS),
+    (dict(out=at(0) + 4096), ALIAS), (dict(out=at(1)), ALIAS), (dict(out=at(2)), ALIAS),
+    (dict(out=at(3)), ALIAS), (dict(out=at(4)), ALIAS), (dict(ldo=2 ** 61), ALIAS),
 ])
 def test_lora_refuses(L, kw, status):
     assert lora(L, **kw) == status
