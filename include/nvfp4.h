@@ -29,6 +29,9 @@
  *   o[m][n] = bf16_rn( silu(g_gate * acc_gate) * (g_up * acc_up) ),  silu(t) = t / (1 + e^-t)
  * in fp32 -- the SiLU(gate)*up that the GB10 plan runs as a separate "moe_silu_mul" launch.
  *
+ * The operators between a decode step's projections (block tables, paged cache, attention, adapters)
+ * are declared at the end, with guarantees of their own.
+ *
  * Guarantees:
  *   - Row invariance: output row m is bitwise identical for every M in 1..128 given the same
  *     x row, weights, N, K and device (the kernel's work split depends on N, K and the SM

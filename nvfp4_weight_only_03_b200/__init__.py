@@ -12,6 +12,13 @@ missing or the device is not a B200 the calls raise.
     o, d = gemv_chain([ChainOp.dual(wg, sg, gg, wu, su, gu, x=x),    # one launch: gate_up ...
                        ChainOp.single([(wd, sd, gd)], x_from=0)])   # ... feeding down
 
+Between the projections (serving.py):
+
+    plan = paged_plan(lens, new, table, free, head, block_size, tokens=T)  # block tables, slots
+    kv_append(k, v, k_cache, v_cache, plan.slots)                          # rows into the cache
+    o = paged_attention(q, k_cache, v_cache, table, plan.starts, plan.lens)
+    y = gemv(w, s, g, x, lora=Lora(a, b, index, scales))                   # adapters beside it
+
 w: uint8 [N][K/2] packed e2m1 (low nibble = even k), s: uint8 [N][K/16] e4m3 scale codes,
 g: float global scale, x: bfloat16 [M][K] (M = 1..128, one kernel pass per 8 rows; row stride
 may exceed K).
