@@ -123,10 +123,10 @@ def _same_device(index: int, name: str, t: torch.Tensor) -> None:
 
 
 def _ints(t: torch.Tensor, name: str, n: int, index: int) -> int:
-    """Address of a contiguous int32 [n] on the call's device."""
+    """Address of n contiguous int32 on the call's device."""
     if t.dtype is not _I32:
         raise TypeError(f"{name} must be int32")
-    if t.shape != (n,) or not t.is_contiguous():
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous [{n}], got {list(t.shape)}")
     if t.get_device() != index:
         _same_device(index, name, t)
@@ -237,21 +237,29 @@ def paged_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free:
         with _entered(lens, stream):
             return paged_plan(lens, new, table, free, head, block_size, tokens, out)
     index = lens.get_device()
-    n = lens.shape[0]
+    n = lens.numel()
     cols, ld = _table_args(table, n, index)
     sizes = (n + 1, n, tokens, tokens, tokens, 1, 1)
     if out is None:
         if tokens < 0:
             raise ValueError("tokens must not be negative")
-        out = PagedPlan._make(lens.new_empty(2 * n + 3 + 3 * tokens).split_with_sizes(sizes))
-        o = [t.data_ptr() for t in out]
+        whole = lens.new_empty(2 * n + 3 + 3 * tokens)
+        # (views that do not share a version counter: half the time)
+        out = PagedPlan._make(whole.unsafe_split_with_sizes(sizes))
+        o0 = whole.data_ptr()
+        o1 = o0 + 4 * n + 4
+        o2 = o1 + 4 * n
+        o3 = o2 + 4 * tokens
+        o4 = o3 + 4 * tokens
+        o5 = o4 + 4 * tokens
+        o6 = o5 + 4
     else:
-        o = [_ints(t, "out." + name, size, index)
-             for name, t, size in zip(PagedPlan._fields, out, sizes)]
+        o0, o1, o2, o3, o4, o5, o6 = (_ints(t, "out." + name, size, index)
+                                      for name, t, size in zip(PagedPlan._fields, out, sizes))
     a = PlanStruct(_ints(lens, "lens", n, index), _ints(new, "new", n, index), n, block_size,
                    table.data_ptr(), ld, cols, _ints(free, "free", free.numel(), index),
-                   free.numel(), _ints(head, "head", 1, index), tokens, o[0], o[1], o[2], o[3],
-                   o[4], o[5], o[6])
+                   free.numel(), _ints(head, "head", 1, index), tokens, o0, o1, o2, o3, o4, o5,
+                   o6)
     status = (_lib or _load()).nvfp4_paged_plan(a, _raw_stream(index))
     if status:
         _fail(status, "nvfp4_paged_plan")
@@ -311,23 +319,25 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     tokens, heads, dim = shape
     if dim != c.dim or heads % max(c.heads, 1):
         raise ValueError(f"q must be [tokens][heads][{c.dim}], heads a multiple of {c.heads}")
-    n = lens.shape[0]
+    n = lens.numel()
     cols, ld = _table_args(table, n, index)
     if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != shape:
-        raise ValueError(f"out must be {list(shape)}")
-    ldo, ho = _heads(out, "out", index)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
+        ldo, ho = heads * dim, dim
+    else:
+        if out.shape != shape:
+            raise ValueError(f"out must be {list(shape)}")
+        ldo, ho = _heads(out, "out", index)
     st = _raw_stream(index)
     if ws is None:
-        ws = _workspace("attn", paged_attention_workspace_bytes(dim), index, st)
+        ws, ws_at, ws_bytes = _attn_workspace(dim, index, st)
     else:
         _same_device(index, "ws", ws)
+        ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     a = AttnStruct(q.data_ptr(), ldq, hq, out.data_ptr(), ldo, ho, tokens, heads, n,
                    table.data_ptr(), ld, cols, _ints(starts, "starts", n + 1, index),
                    _ints(lens, "lens", n, index), dim ** -0.5 if scale is None else scale)
-    status = (_lib or _load()).nvfp4_paged_attn(a, c, ws.data_ptr(),
-                                                ws.numel() * ws.element_size(), st)
+    status = (_lib or _load()).nvfp4_paged_attn(a, c, ws_at, ws_bytes, st)
     if status:
         _fail(status, "nvfp4_paged_attn")
     if check:
@@ -336,6 +346,18 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
 
 _attn_bytes: dict = {}
+_attn_ready: dict = {}  # (dim, device, stream) -> its cached workspace, address and bytes
+
+
+def _attn_workspace(dim: int, index: int, st: int):
+    capturing = _capturing()
+    found = None if capturing else _attn_ready.get((dim, index, st))
+    if found is None:
+        ws = _workspace("attn", paged_attention_workspace_bytes(dim), index, st)
+        found = ws, ws.data_ptr(), ws.numel()
+        if not capturing:
+            _attn_ready[(dim, index, st)] = found
+    return found
 
 
 def paged_attention_workspace_bytes(dim: int) -> int:
@@ -419,8 +441,10 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if scales.shape != (s,) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous [{s}]")
     if out is None:
-        out = torch.empty_like(y)
-    ldo = _rows(out, "out", m, n, dev)
+        out = torch.empty_like(y) if y.is_contiguous() else y.new_empty((m, n))
+        ldo = n
+    else:
+        ldo = _rows(out, "out", m, n, dev)
     st = _raw_stream(dev)
     if ws is None:
         ws = _workspace("lora", lora_workspace_bytes(m, s, rank, k), dev, st)
