@@ -23,6 +23,7 @@ import torch
 
 KV_BF16, KV_E4M3 = 0, 1
 MAX_REQUESTS = 8192
+MAX_RANK = 128
 
 _lib = None  # the loaded library, set by declare
 
@@ -187,21 +188,29 @@ def _cache_args(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float, v_
                          slot, head, k_scale, v_scale)
 
 
-def _workspace(kind: str, need: int, index: int, st: int) -> torch.Tensor:
-    """The cached workspace of (device, current stream), or, while a graph is captured, one of
-    the graph's own: two graphs never share one."""
-    if _capturing():
-        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-        if kind == "attn":
-            ws[:2048].zero_()  # its words that have to be zero (one per SM, and the error word)
-        return ws
-    ws = _workspaces.get((kind, index, st))
-    if ws is None or ws.numel() < need:
+def _workspace(kind: str, dim: int, index: int, st: int):
+    """(workspace, its address, bytes) for paged_attention of this head dim, or for any lora_add:
+    the cached one of (device, current stream), or, while a graph is captured, one of the
+    graph's own: two graphs never share one."""
+    capturing = _capturing()
+    found = None if capturing else _workspaces.get((kind, dim, index, st))
+    if found is None:
         dev = torch.device("cuda", index)
-        # this cache holds the stream, so that its handle stays its own
-        ws = _nv()._cached_workspace(kind, need, dev, torch.cuda.current_stream(dev))
-        _workspaces[(kind, index, st)] = ws
-    return ws
+        if kind == "attn":
+            need = paged_attention_workspace_bytes(dim)
+        else:
+            need = lora_workspace_bytes(_nv().MAX_ROWS, 1, MAX_RANK, 8)  # 128 KB, the most there is
+        if capturing:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            if kind == "attn":
+                ws[:2048].zero_()  # its words that have to be zero (one per SM, and the error word)
+        else:
+            # this cache holds the stream, so that its handle stays its own
+            ws = _nv()._cached_workspace((kind, dim), need, dev, torch.cuda.current_stream(dev))
+        found = ws, ws.data_ptr(), ws.numel()
+        if not capturing:
+            _workspaces[(kind, dim, index, st)] = found
+    return found
 
 
 _workspaces: dict = {}
@@ -330,7 +339,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         ldo, ho = _heads(out, "out", index)
     st = _raw_stream(index)
     if ws is None:
-        ws, ws_at, ws_bytes = _attn_workspace(dim, index, st)
+        ws, ws_at, ws_bytes = _workspace("attn", dim, index, st)
     else:
         _same_device(index, "ws", ws)
         ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
@@ -346,20 +355,6 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
 
 _attn_bytes: dict = {}
-_attn_ready: dict = {}  # (dim, device, stream) -> its cached workspace, address and bytes
-
-
-def _attn_workspace(dim: int, index: int, st: int):
-    capturing = _capturing()
-    found = None if capturing else _attn_ready.get((dim, index, st))
-    if found is None:
-        ws = _workspace("attn", paged_attention_workspace_bytes(dim), index, st)
-        found = ws, ws.data_ptr(), ws.numel()
-        if not capturing:
-            _attn_ready[(dim, index, st)] = found
-    return found
-
-
 def paged_attention_workspace_bytes(dim: int) -> int:
     """Bytes of a paged_attention workspace for this head dim on the current device."""
     key = (_current_device(), dim)
@@ -384,22 +379,13 @@ def _rows(t: torch.Tensor, name: str, m: int, n: int, index: int) -> int:
     return stride[0] if m > 1 else n
 
 
-_lora_bytes: dict = {}
-
-
 def lora_workspace_bytes(m: int, adapters: int, rank: int, k: int) -> int:
     """Bytes of a lora_add workspace on the current device."""
-    key = (m, adapters, rank, k)
-    need = _lora_bytes.get(key)
-    if need is None:
-        b = ctypes.c_size_t()
-        nv = _nv()
-        nv._check(nv.lib().nvfp4_lora_workspace_bytes(m, adapters, rank, k, ctypes.byref(b)),
-                  "nvfp4_lora_workspace_bytes")
-        if len(_lora_bytes) > 4096:
-            _lora_bytes.clear()
-        need = _lora_bytes[key] = int(b.value)
-    return need
+    b = ctypes.c_size_t()
+    nv = _nv()
+    nv._check(nv.lib().nvfp4_lora_workspace_bytes(m, adapters, rank, k, ctypes.byref(b)),
+              "nvfp4_lora_workspace_bytes")
+    return int(b.value)
 
 
 def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -447,16 +433,16 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
         ldo = _rows(out, "out", m, n, dev)
     st = _raw_stream(dev)
     if ws is None:
-        ws = _workspace("lora", lora_workspace_bytes(m, s, rank, k), dev, st)
+        ws, ws_at, ws_bytes = _workspace("lora", 0, dev, st)
     else:
         _same_device(dev, "ws", ws)
+        ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     l = LoraStruct(a.data_ptr(), sa[0] if s > 1 else rank * k, sa[1] if rank > 1 else k,
                    b.data_ptr(), sb[0] if s > 1 else n * rank, sb[1] if n > 1 else rank,
                    scales.data_ptr(), None if ranks is None else _ints(ranks, "ranks", s, dev),
                    _ints(index, "index", m, dev), s, rank)
     status = (_lib or _load()).nvfp4_lora_add(l, x.data_ptr(), ldx, y.data_ptr(), ldy,
-                                              out.data_ptr(), ldo, m, n, k, ws.data_ptr(),
-                                              ws.numel() * ws.element_size(), st)
+                                              out.data_ptr(), ldo, m, n, k, ws_at, ws_bytes, st)
     if status:
         _fail(status, "nvfp4_lora_add")
     return out
