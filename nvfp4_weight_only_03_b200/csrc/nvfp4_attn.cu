@@ -138,9 +138,17 @@ inline Divisor divisor_of(uint32_t d) {
     }
     return r;
 }
-// a / b, neither negative.  A 64-bit division takes half a microsecond.
-__device__ __noinline__ int64_t div64(int64_t a, int64_t b) {
-    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+// a / b, neither negative.  A 64-bit division takes half a microsecond and a 32-bit one a quarter, and
+// every call waits for three of them, so small ones are approximated in fp32 (off by less than one)
+// and put right.
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((uint64_t)(a | b) >> 22) return div64(a, b);
+    const int x = (int)a, y = (int)b;
+    int q = (int)__fdividef((float)x, (float)y);
+    const int left = x - q * y;
+    q += left >= y;
+    return q - (left < 0);
 }
 
 struct Params {
@@ -157,7 +165,6 @@ struct Params {
     int capacity;      // keys that a table row can hold
     const void* v;     // the cache's values and strides (elements), for what is read without TMA
     int64_t block_stride, slot_stride, head_stride;
-    int min_units;     // fewest units worth a CTA of their own
     // What beginning and ending a row tile costs, in units: Q's rows, the first scores and the epilogue
     // pass without overlap.  The split counts it, or a CTA with many short row tiles would be the
     // last by far.
@@ -307,13 +314,15 @@ struct Ring {
     }
 };
 
+constexpr int kMinUnits = 2;  // fewest units worth a CTA of their own
+
 struct Range {
     int64_t begin, end, total;
     int ctas;
 };
 
 __device__ __forceinline__ int64_t range_begin(int64_t total, int ctas, int c) {
-    return div64(total * c, ctas);
+    return quotient(total * c, ctas);
 }
 
 // This CTA's units and the row tile they start in.  Every thread sums the units of a run of
@@ -324,12 +333,16 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
     if (tid == 0) start->r = -1;  // behind the first __syncthreads at the latest
     const int per = (p.requests + THREADS - 1) / THREADS;
     const int r0 = min(tid * per, p.requests), r1 = min(r0 + per, p.requests);
-    int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) {
-        const Request q = request_of(p, r);
+    int64_t mine = 0, s = 0;
+    Request q;
+    auto weigh = [&](int r) {  // q, and s: the units of one of its heads
+        q = request_of(p, r);
         const int tiles = row_tiles(p, q);
-        int64_t s = 0;
+        s = 0;
         for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + p.tile_cost;
+    };
+    for (int r = r0; r < r1; ++r) {
+        weigh(r);
         mine += s * p.kv_heads;
     }
     int64_t incl = mine;
@@ -349,7 +362,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
     before += incl - mine;
     Range g;
     g.total = total;
-    const int64_t most = div64(total + p.min_units - 1, p.min_units);
+    const int64_t most = (total + kMinUnits - 1) / kMinUnits;
     g.ctas = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
     g.begin = g.end = 0;
     if ((int)blockIdx.x < g.ctas) {
@@ -359,10 +372,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
     if (g.end > g.begin && before <= g.begin && g.begin < before + mine) {
         int64_t at = g.begin - before;
         for (int r = r0; r < r1; ++r) {
-            const Request q = request_of(p, r);
-            const int tiles = row_tiles(p, q);
-            int64_t s = 0;
-            for (int t = 0; t < tiles; ++t) s += units_of<TK>(p, q, t) + p.tile_cost;
+            if (per > 1) weigh(r);
             if (at >= s * p.kv_heads) {
                 at -= s * p.kv_heads;
                 continue;
@@ -370,7 +380,7 @@ __device__ __forceinline__ Range find_range(const Params& p, Cursor<TK>* start, 
             Cursor<TK> c;
             c.r = r;
             c.q = q;
-            c.h = (int)div64(at, s);
+            c.h = (int)quotient(at, s);
             at -= c.h * s;
             c.tile = 0;
             while (at >= units_of<TK>(p, q, c.tile) + p.tile_cost)
@@ -1195,7 +1205,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 // the CTA with unit x (as the ranges count) of this row tile's 0 .. n - 1 from `zero`
                 const int64_t zero = cur.u == 0 ? range.end - cnt : range.begin - cur.u;
                 auto cta_of = [&](int64_t x) {
-                    const int64_t e = div64((x + 1) * range.ctas + range.total - 1, range.total) - 1;
+                    const int64_t e = quotient((x + 1) * range.ctas + range.total - 1, range.total) - 1;
                     return (int)min(max(e, (int64_t)0), (int64_t)range.ctas - 1);
                 };
                 const int owner = cur.u == 0 ? (int)blockIdx.x : cta_of(zero);
@@ -1280,7 +1290,6 @@ int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int 
         }
         ready[dev] = true;
     }
-    p.min_units = 2;
     p.tile_cost = F8 && D == 256 ? 7 : 4;
     const int st = nvfp4_host::launch_behind(nvfp4_attn_kernel<D, F8>, grid, C::kThreads, C::kSmem, 0,
                                              stream, p, mk, mv);
