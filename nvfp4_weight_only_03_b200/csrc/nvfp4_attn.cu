@@ -33,9 +33,9 @@
 // * Measured (B200, calls of a captured graph): 64 requests of up to 8192 keys, 24 heads on 4 of
 //   256, one token each: 167 us, 6.0 TB/s, 93% of the copy rate; one request of 131072 keys: 103 us,
 //   80% (parts of its 4 heads' single row tiles are joined by one CTA each); 16 requests x 8 tokens,
-//   e4m3, 32 heads on 8 of 128: 96 us, 46% (widening V and the one softmax warp that has rows);
-//   2048 tokens over 16384 keys: 680 us, 1140 TFLOP/s, 67% of the matrix rate (shared memory, out
-//   of which Q is read again for every unit).  The least call is some 8 us: lengths, first pages,
+//   e4m3, 32 heads on 8 of 128: 94 us, 47% (widening V and the one softmax warp that has rows);
+//   2048 tokens over 16384 keys: 665 us, 1160 TFLOP/s, 69% of the matrix rate (shared memory, out
+//   of which Q is read again for every unit).  The least call is some 7 us: lengths, first pages,
 //   keys, scores, weights and values follow on one another, each with its latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
