@@ -34,8 +34,8 @@
 //   256, one token each: 167 us, 6.0 TB/s, 93% of the copy rate; one request of 131072 keys: 103 us,
 //   80% (parts of its 4 heads' single row tiles are joined by one CTA each); 16 requests x 8 tokens,
 //   e4m3, 32 heads on 8 of 128: 94 us, 47% (widening V and the one softmax warp that has rows);
-//   2048 tokens over 16384 keys: 665 us, 1160 TFLOP/s, 69% of the matrix rate (shared memory, out
-//   of which Q is read again for every unit).  The least call is some 7 us: lengths, first pages,
+//   2048 tokens over 16384 keys: 665 us, 1160 TFLOP/s, 69% of the matrix rate (the
+//   tensor pipe is busy for half of its cycles: scores, weights and values wait on one another).  The least call is some 7 us: lengths, first pages,
 //   keys, scores, weights and values follow on one another, each with its latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -221,16 +221,16 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Two values as e4m3 codes (the first in the low byte), and back.
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+// Two f16 values as e4m3 codes, and back.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t f16x2) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(f16x2));
     return r;
 }
-__device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
+__device__ __forceinline__ uint32_t e4m3_values(uint32_t codes) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-    return __half22float2(*reinterpret_cast<__half2*>(&h));
+    return h;
 }
 
 // ---- the order of the work ---------------------------------------------------------------
@@ -802,7 +802,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // Q as two e4m3 terms of x = q 2^e, with the row's largest magnitude in [2^7, 2^8): the first
         // is x rounded to its 4 bits, and what that leaves of bf16's 8 bits is at most 8 of its last
         // place, 4 bits again, so the two are exact down to e4m3's smallest step, 2^-9: an error of at
-        // most 2^-10, 2^-17 of the row's largest value.  D / 8 lanes take a row, 16 bytes each; a
+        // most 2^-10, 2^-17 of the row's largest value.  In between x is f16, exact down to 2^-17.  An
+        // infinity makes the row NaN, as its scores would.  D / 8 lanes take a row, 16 bytes each; a
         // warp reads kSome such groups of rows at once, since a row alone is a memory latency and
         // a chain of conversions.  (One warp alone took 45 us for 128 rows at D = 256.)
         auto split_q = [&]() {
@@ -836,27 +837,27 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     uint32_t two = 0;  // largest magnitudes' bits; NaN and infinity lead
 #pragma unroll
                     for (int e = 0; e < 4; ++e) two = __vmaxu2(two, w[e] & 0x7fff7fffu);
-                    uint32_t big = max(two & 0xffffu, two >> 16);
 #pragma unroll
                     for (int d = kLanes / 2; d; d >>= 1)
-                        big = max(big, __shfl_xor_sync(~0u, big, d));
+                        two = __vmaxu2(two, __shfl_xor_sync(~0u, two, d));
+                    const uint32_t big = max(two & 0xffffu, two >> 16);
                     // up: the biased exponent of 2^e.  At most 2^64: a row whose largest value is
-                    // below 2^-57 has scores of zero to fp32 either way.  An infinity times
-                    // 2^e - 2^e is NaN, as e4m3 has none.
+                    // below 2^-57 has scores of zero to fp32 either way.
                     const int up = min(127 + 7 + 127 - (int)(big >> 7), 127 + 64);
                     const float mul = __uint_as_float((uint32_t)up << 23);
-                    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+                    uint32_t hi[2], lo[2];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float a = __uint_as_float(w[e] << 16) * mul;
-                        const float b = __uint_as_float(w[e] & 0xffff0000u) * mul;
-                        const uint32_t h = e4m3_pair(a, b);
-                        const float2 f = e4m3_values(h);
-                        // (a - a is 0, or NaN where a is infinite)
-                        const uint32_t l = e4m3_pair(a - f.x + (a - a), b - f.y + (b - b));
-                        hi[e >> 1] |= h << (e & 1) * 16;
-                        lo[e >> 1] |= l << (e & 1) * 16;
+                        const uint32_t x = pack16(true, __uint_as_float(w[e] << 16) * mul,
+                                                  __uint_as_float(w[e] & 0xffff0000u) * mul);
+                        const uint32_t h = e4m3_pair(x), f = e4m3_values(h);
+                        uint32_t rest;
+                        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(x), "r"(f));
+                        const uint32_t l = e4m3_pair(rest);
+                        hi[e >> 1] = e & 1 ? hi[e >> 1] | h << 16 : h;
+                        lo[e >> 1] = e & 1 ? lo[e >> 1] | l << 16 : l;
                     }
+                    if (big >= 0x7f80u) lo[0] = lo[1] = 0x7f7f7f7fu;
                     if (r < rows) {
                         if (c == 0) sm.q_scale[item & 3][r] = (uint8_t)(254 - up);
                         // 16-byte units turned by the row, as TMA turns K's
