@@ -65,9 +65,6 @@ int launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int
     return NVFP4_ERR_LAUNCH;
 }
 
-// Clears a failed launch's error and turns it into a status.
-inline int launched() { return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH; }
-
 }  // namespace nvfp4_host
 
 #endif

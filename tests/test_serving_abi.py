@@ -12,7 +12,6 @@ from nvfp4_weight_only_03_b200 import build as nvbuild
 from nvfp4_weight_only_03_b200 import serving as sv
 
 NULL, SHAPE, ROWS, ALIGN, ARCH, WORKSPACE, ALIAS = -1, -2, -3, -4, -5, -7, -8
-OK = pytest.param  # (readability of the lists below)
 
 
 @pytest.fixture(scope="module")
