@@ -170,10 +170,11 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
 }
 
 // ------------------------------------------------------------------------------------------
-// Append.  A warp per token and side (K or V); a lane moves pieces of 16 bytes of the cache (8 bf16
-// values, or 16 codes), so loads and stores are whole sectors and the slot is looked up once per
-// row.  HBM bound, 4 bytes of traffic per value (3 with an 8-bit cache).  Measured (B200): 8192 tokens
-// of 4 heads of 256 into an e4m3 cache 12.7 us, 55% of the copy rate; 128 tokens, bf16, 2.5 us.
+// Append.  A warp per token, or per token and side (K or V); a lane moves pieces of 16 bytes of the
+// cache (8 bf16 values, or 16 codes), so loads and stores are whole sectors and the slot is looked up
+// once per row.  HBM bound, 4 bytes of traffic per value (3 with an 8-bit cache).  Measured (B200):
+// 8192 tokens of 4 heads of 256 into an e4m3 cache 10.9 us, 64% of the copy rate; 128 tokens, bf16,
+// 1.9 us.
 //
 // An e4m3 code is e4m3_rn(x / scale) of the fp32 quotient, saturated at 448.  A division per value was
 // the bound (a hundred instructions per eight values).  The quotient is formed from 1 / scale in two
@@ -226,7 +227,7 @@ __device__ __forceinline__ uint2 quantise(uint4 v, float scale, float inverse, f
                       e4m3_pair(q[4], q[5]) | e4m3_pair(q[6], q[7]) << 16);
 }
 
-template <bool F8>
+template <bool F8, int SIDES>  // K and V of a token in one warp, or one of them
 __global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const AppendParams p) {
     constexpr int kPiece = F8 ? 16 : 8;  // values
     const int lane = threadIdx.x & 31;
@@ -235,29 +236,38 @@ __global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const Appe
     const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
     const int64_t me = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t i = me; i < 2 * p.tokens; i += warps) {
-        const int64_t t = i >> 1;
-        const int which = (int)(i & 1);
-        const int32_t slot = p.slots[t];
+    for (int64_t i = me; i < p.tokens * (3 - SIDES); i += warps) {
+        const int64_t t = SIDES == 2 ? i : i >> 1;
+        const int32_t slot = __ldg(p.slots + t);
         const int32_t page = slot / p.block;
         if (slot < 0 || page >= p.blocks) continue;
-        const uint16_t* const src = p.src[which] + t * p.ld[which];
         const int64_t at = page * p.block_stride + (int64_t)(slot - page * p.block) * p.slot_stride;
-        uint8_t* const dst = p.cache[which] + (F8 ? at : 2 * at);
-        const float scale = p.scale[which], inverse = p.inverse[which], rest = p.rest[which];
 #pragma unroll 2
         for (int j = lane; j < pieces; j += 32) {
             const int h = j >> log_per, c = (j - (h << log_per)) * kPiece;
-            const uint4* const from =
-                reinterpret_cast<const uint4*>(src + h * p.head_stride[which] + c);
-            uint8_t* const to = dst + (F8 ? 1 : 2) * (h * p.cache_head_stride + c);
-            if (F8) {
-                const uint4 v = from[0], w = from[1];
-                const uint2 a = quantise(v, scale, inverse, rest);
-                const uint2 b = quantise(w, scale, inverse, rest);
-                *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
-            } else {
-                *reinterpret_cast<uint4*>(to) = from[0];
+            const int64_t to = at + h * p.cache_head_stride + c;
+            uint4 v[SIDES][F8 ? 2 : 1];
+#pragma unroll
+            for (int s = 0; s < SIDES; ++s) {  // (no load waits for a store)
+                const int which = SIDES == 2 ? s : (int)(i & 1);
+                const uint4* const from = reinterpret_cast<const uint4*>(
+                    p.src[which] + t * p.ld[which] + h * p.head_stride[which] + c);
+                v[s][0] = __ldg(from);
+                if (F8) v[s][F8] = __ldg(from + 1);
+            }
+#pragma unroll
+            for (int s = 0; s < SIDES; ++s) {
+                const int which = SIDES == 2 ? s : (int)(i & 1);
+                uint8_t* const dst = p.cache[which] + (F8 ? to : 2 * to);
+                if (F8) {
+                    const float scale = p.scale[which], inverse = p.inverse[which],
+                                rest = p.rest[which];
+                    const uint2 x = quantise(v[s][0], scale, inverse, rest);
+                    const uint2 y = quantise(v[s][F8], scale, inverse, rest);
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(x.x, x.y, y.x, y.y);
+                } else {
+                    *reinterpret_cast<uint4*>(dst) = v[s][0];
+                }
             }
         }
     }
@@ -414,11 +424,17 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     p.heads = c.heads;
     p.dim = c.dim;
     p.block = c.block_size;
-    const int64_t want = (tokens * 2 * 32 + kAppendThreads - 1) / kAppendThreads;  // a warp per row
-    const int grid = (int)(want > 8 * sms ? 8 * sms : want);
+    // Few rows: a warp each.  More than the GPU's warps can be at once: K and V of a token in one, with
+    // twice the loads under way (8192 tokens, e4m3: 10.9 us against 12.7; 128 tokens: 2.6 against 1.9).
+    const int most = 8 * sms;
+    const bool both = tokens * 2 > (int64_t)most * (kAppendThreads / 32);
+    const int64_t want = (tokens * (both ? 1 : 2) * 32 + kAppendThreads - 1) / kAppendThreads;
+    const int grid = (int)(want > most ? most : want);
+    const bool f8 = c.type == NVFP4_KV_E4M3;
     return nvfp4_host::launch_behind(
-        c.type == NVFP4_KV_E4M3 ? nvfp4_append_kernel<true> : nvfp4_append_kernel<false>, grid,
-        kAppendThreads, 0, 0, stream, p);
+        both ? f8 ? nvfp4_append_kernel<true, 2> : nvfp4_append_kernel<false, 2>
+             : f8 ? nvfp4_append_kernel<true, 1> : nvfp4_append_kernel<false, 1>,
+        grid, kAppendThreads, 0, 0, stream, p);
 }
 
 }  // extern "C"

@@ -371,7 +371,8 @@ def test_captured_call_serves_later_lengths():
 @pytest.mark.parametrize("layout", ["nhd", "hnd", "joint"])
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("tokens,heads,dim,block", [(1, 1, 64, 16), (37, 4, 256, 16),
-                                                    (1000, 3, 128, 48)])
+                                                    (1000, 3, 128, 48), (5001, 2, 64, 16),
+                                                    (9600, 5, 128, 32)])
 def test_append(tokens, heads, dim, block, f8, layout):
     g = torch.Generator(device="cuda").manual_seed(tokens)
     blocks = -(-tokens // block) + 2
