@@ -304,6 +304,46 @@ def test_head_groups(heads, kv_heads, dim, f8):
     check_attention(Batch(60, [77, 130, 300, 9], [1, 5, 1, 9], heads, kv_heads, dim, 16, f8))
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_more_requests_than_threads(f8):
+    rng = np.random.default_rng(12)
+    new = [int(x) for x in rng.integers(0, 4, 1300)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 60, 1300))]
+    check_attention(Batch(61, lens, new, 4, 2, 64, 16, f8))
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_offsets_past_32_bits(f8):
+    """Pages whose elements lie past 2^31 (bytes past 2^32): rows written there and read there are
+    those of the same pages of a small cache, bit for bit."""
+    heads, kv_heads, dim, block, n = 8, 4, 256, 16, 100
+    blocks = (2 ** 32 if f8 else 2 ** 31) // (block * kv_heads * dim) + 40
+    g = torch.Generator(device="cuda").manual_seed(90)
+    k, v = (torch.randn((n, kv_heads, dim), generator=g, device="cuda").bfloat16() for _ in "kv")
+    q = torch.randn((9, heads, dim), generator=g, device="cuda").bfloat16()
+    pages = torch.randperm(30, generator=g, device="cuda")[:7].to(torch.int32)
+    dtype = F8 if f8 else torch.bfloat16
+    outs = []
+    for first, total in ((0, 40), (blocks - 30, blocks)):
+        kc, vc = (torch.empty((total, block, kv_heads, dim), dtype=dtype, device="cuda")
+                  for _ in "kv")
+        table = (pages + first).view(1, 7)
+        pos = torch.arange(n, device="cuda")
+        slots = (table[0, pos // block] * block + pos % block).to(torch.int32)
+        nv.kv_append(k, v, kc, vc, slots, 0.02, 0.02)
+        # (a value that is not finite is read by the kernel itself, not by a copy)
+        if f8:
+            vc.view(torch.uint8)[int(table[0, 6]), 1, 0, 5] = 0x7F
+        else:
+            vc[int(table[0, 6]), 1, 0, 5] = float("inf")
+        outs.append(nv.paged_attention(q, kc, vc, table, ints([0, 9]), ints([n]), k_scale=0.02,
+                                       v_scale=0.02))
+        del kc, vc
+    a, b = (o.view(torch.int16) for o in outs)
+    assert torch.equal(a, b)
+    assert not torch.isfinite(outs[0][6:, :2, 5]).any() and torch.isfinite(outs[0][:6]).all()
+
+
 def test_rows_behind_the_last_token_stay():
     b = Batch(12, [40, 50], [3, 1], 8, 2, 128, 16, pad=5)
     out = torch.full_like(b.q, 7.0)
