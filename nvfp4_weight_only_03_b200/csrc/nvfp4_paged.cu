@@ -216,7 +216,9 @@ __device__ __forceinline__ uint2 quantise(uint4 v, float scale, float inverse, f
     for (int i = 0; i < 8; ++i) {
         const float x = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
         const float a = fmaf(x, inverse, x * rest);
-        q[i] = fmaf(fmaf(-a, scale, x), inverse, a);
+        // (sums that are zero are +0: the sign is x's)
+        q[i] = __uint_as_float(__float_as_uint(fmaf(fmaf(-a, scale, x), inverse, a)) |
+                               (__float_as_uint(x) & 0x80000000u));
     }
     if (divide) {
 #pragma unroll

@@ -467,6 +467,20 @@ def test_append_rounds_the_true_quotient():
             assert (same | (torch.isnan(got.float()) & torch.isnan(want.float()))).all()
 
 
+def test_append_keeps_the_sign_of_zero():
+    rows = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    rows[..., 1::2] = -0.0
+    rows[2, :, 8:16] = 1e-30  # (quotients that round to zero, beside values that do not)
+    rows[2, :, 16:24] = -1e-30
+    rows[2, :, 24] = 1.0
+    for scale in (1e-15, 7.3e-5, 0.02, 0.3, 0.7, 1.0, 3.0, 1e15):
+        kc, vc = (torch.zeros((1, 16, 2, 64), dtype=F8, device="cuda") for _ in "kv")
+        nv.kv_append(rows, -rows, kc, vc, ints([0, 1, 2]), scale, scale)
+        for got, x in ((kc, rows), (vc, -rows)):
+            want = torch.signbit(x)
+            assert torch.equal(got.view(torch.uint8)[0, :3] >= 0x80, want), scale
+
+
 # ---------------------------------------------------------------- the plan
 
 
