@@ -181,15 +181,17 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
 // fp32 terms, r and the rest of it, as q = fma(x, r, x * rest), which is off by little more than the
 // rounding itself, so within one place; Markstein's correction (IBM J. Res. Dev. 34, 1990: with r the
 // rounded reciprocal and q within a place, q + r (x - q scale) in two fused steps is the rounded
-// quotient) then makes it exact.  Infinities, NaN, and scales whose products might leave the normal
-// range are divided.
+// quotient) then makes it exact, as long as nothing on the way leaves fp32's range: values of 2^63 scales
+// and more (infinities and NaN among them), and all values at scales below 1e-15 or above 1e15, are
+// divided.
 constexpr int kAppendThreads = 256;
 
 struct AppendParams {
     const uint16_t* src[2];
     int64_t ld[2], head_stride[2];
     uint8_t* cache[2];
-    float scale[2], inverse[2], rest[2];  // 1 / scale = inverse + rest; inverse 0: divide
+    float scale[2], inverse[2], rest[2];  // 1 / scale = inverse + rest
+    uint32_t far[2];  // sets bits 15 and 31 when added to two bf16 exponents that want a division
     const int32_t* slots;
     int64_t tokens, blocks, block_stride, slot_stride, cache_head_stride;
     int heads, dim, block;
@@ -205,12 +207,13 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
 }
 
 // 8 bf16 values -> 8 codes.
-__device__ __forceinline__ uint2 quantise(uint4 v, float scale, float inverse, float rest) {
+__device__ __forceinline__ uint2 quantise(uint4 v, float scale, float inverse, float rest,
+                                          uint32_t far) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;  // bits 15 and 31: an exponent of all ones
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top |= (w[i] & 0x7f807f80u) + 0x00800080u;
-    const bool divide = inverse == 0.f || (top & 0x80008000u);
+    for (int i = 0; i < 4; ++i) top |= (w[i] & 0x7f807f80u) + far;
+    const bool divide = top & 0x80008000u;
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -264,8 +267,9 @@ __global__ void __launch_bounds__(kAppendThreads) nvfp4_append_kernel(const Appe
                 if (F8) {
                     const float scale = p.scale[which], inverse = p.inverse[which],
                                 rest = p.rest[which];
-                    const uint2 x = quantise(v[s][0], scale, inverse, rest);
-                    const uint2 y = quantise(v[s][F8], scale, inverse, rest);
+                    const uint32_t far = p.far[which];
+                    const uint2 x = quantise(v[s][0], scale, inverse, rest, far);
+                    const uint2 y = quantise(v[s][F8], scale, inverse, rest, far);
                     *reinterpret_cast<uint4*>(dst) = make_uint4(x.x, x.y, y.x, y.y);
                 } else {
                     *reinterpret_cast<uint4*>(dst) = v[s][0];
@@ -412,11 +416,17 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     p.cache[1] = static_cast<uint8_t*>(c.v);
     p.scale[0] = c.k_scale;
     p.scale[1] = c.v_scale;
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+        int exponent = 0;  // biased, of the least values that are divided: all of them by default
         if (p.scale[i] >= 1e-15f && p.scale[i] <= 1e15f) {
             p.inverse[i] = 1.f / p.scale[i];
             p.rest[i] = (float)(1.0 / p.scale[i] - p.inverse[i]);
+            int e;  // scale is in [2^(e - 1), 2^e)
+            frexpf(p.scale[i], &e);
+            exponent = 127 + 63 + e;  // 141 to 240: quotients below are less than 2^64
         }
+        p.far[i] = (0x8000u - ((uint32_t)exponent << 7)) * 0x10001u;
+    }
     p.slots = slots;
     p.tokens = tokens;
     p.blocks = c.blocks;

@@ -481,6 +481,40 @@ def test_append_keeps_the_sign_of_zero():
             assert torch.equal(got.view(torch.uint8)[0, :3] >= 0x80, want), scale
 
 
+@pytest.mark.parametrize("tokens", [1024, 5120])
+def test_append_saturates_quotients_that_leave_fp32(tokens):
+    """Every bf16 value, up to the largest of both signs, at scales whose quotients of large values are
+    infinite in fp32: 448 with x's sign, and the fp32 quotient's code below.  (Whole numbers: the codes
+    are equal.)  1024 rows are a warp per side each, 5120 a warp per token."""
+    x = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    rows = x.view(1024, 1, 64).repeat(tokens // 1024, 1, 1)
+    n = rows.shape[0]
+    slots = torch.arange(n, device="cuda", dtype=torch.int32)
+    for scale in (1e-16, 1e-15, 1.1e-15, 1e-10, 7.3e-5, 0.02, 0.3, 0.7, 0.9, 1.0, 3.0, 1e5, 9e14, 1e15,
+                  1e16, 1e-38, 3e38):
+        scale = torch.tensor(scale, dtype=torch.float32)
+        kc, vc = (torch.zeros((n // 16, 16, 1, 64), dtype=F8, device="cuda") for _ in range(2))
+        nv.kv_append(rows.cuda(), (-rows).cuda(), kc, vc, slots, float(scale), float(scale))
+        q = rows.float() / scale
+        for got, q in ((kc, q), (vc, -q)):
+            got = got.view(n, 1, 64).cpu()
+            want = torch.where(torch.isnan(q), q, q.clamp(-448, 448)).to(F8)
+            same = got.view(torch.uint8) == want.view(torch.uint8)
+            nan = torch.isnan(want.float())
+            assert (same | nan).all() and torch.equal(torch.isnan(got.float()), nan), float(scale)
+
+
+def test_attention_over_keys_and_values_past_the_codes_range():
+    # keys and values that saturate are finite to the rows that see them
+    b = Batch(19, [90, 70], [1, 3], 12, 2, 128, 16, True)
+    b.k_scale = b.v_scale = 0.02
+    slots = [int(b.table[r, key // 16]) * 16 + key % 16 for r, key in ((0, 40), (1, 5))]
+    k, v = (torch.randn((2, 2, 128), device="cuda").bfloat16() for _ in "kv")
+    k[0, :, 3], v[0, :, 9], v[1, :, 100] = 7e36, -3.3e38, 1e37
+    nv.kv_append(k, v, b.kc, b.vc, ints(slots), b.k_scale, b.v_scale)
+    check_attention(b)
+
+
 # ---------------------------------------------------------------- the plan
 
 
