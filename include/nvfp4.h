@@ -481,8 +481,10 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
  * with kv head h / (heads / cache->heads), key j at slot j % block_size of page
  * table[r][j / block_size].  Keys whose page is not in 0..blocks-1, or lies beyond table_columns,
  * are not there; a token that sees no key gives zeros.  Rows of o behind the last token stay as
- * they were.  What cache slots hold that a token does not see has no effect on it, whatever it is
- * (keys or values that are infinite or NaN reach the tokens that see them, and no others).
+ * they were.  Where `starts` passes `tokens` (a plan with fewer outputs than its batch has tokens), the
+ * rows that exist are computed, each at its own position.  What cache slots hold that a token does not
+ * see has no effect on it, whatever it is (keys or values that are infinite or NaN reach the tokens that
+ * see them, and no others).
  *   q, o: bf16, head h of token t at q + t*ldq + h*q_head_stride; 16-byte aligned, strides
  *   multiples of 8 and >= dim; o overlaps nothing that the call reads.   heads % cache->heads == 0
  *   scale: > 0 (scale * k_scale a normal fp32 number) */
@@ -496,7 +498,7 @@ typedef struct {
     int32_t requests;         /* 0..NVFP4_MAX_REQUESTS */
     const int32_t* table;     /* [requests][ld_table] */
     int64_t ld_table, table_columns;
-    const int32_t* starts;    /* [requests + 1], ascending; cut to 0..tokens */
+    const int32_t* starts;    /* [requests + 1], ascending; rows outside 0..tokens-1 are left out */
     const int32_t* lens;      /* [requests] */
     float scale;
 } nvfp4_paged_attn_t;

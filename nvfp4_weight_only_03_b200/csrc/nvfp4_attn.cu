@@ -3,7 +3,7 @@
 // launches it as paged_decode_attn ("Blueprint - circuit executor" page for qwen3.8-27b-nvfp4 on
 // GB10, table "Kernels the plan launches").
 //
-//   token i of request r's n new ones: p = len - n + i
+//   token t of request r, starts[r] <= t < starts[r + 1]: p = lens[r] - starts[r + 1] + t
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j),  over the keys j <= p that have a page
 //
 // * Rows: the query heads that share a kv head are rows of one matrix product, row g of a request
@@ -236,15 +236,17 @@ __device__ __forceinline__ uint32_t e4m3_values(uint32_t codes) {
 // ---- the order of the work ---------------------------------------------------------------
 
 struct Request {
-    int token0, n, len;  // first token, new tokens, tokens in the cache (the new ones included)
+    int token0, n, pos;  // first row, rows, position of the first row's token (below 0: sees no key)
 };
 
-// Device data is taken as it is, within bounds: a request outside [0, tokens] is cut to it.
+// Device data is taken as it is, within bounds: a request outside [0, tokens] is cut to it.  What is
+// cut off at its end still counts for the positions: starts[r + 1] is the one behind the last of lens[r].
 __device__ __forceinline__ Request request_of(const Params& p, int r) {
+    const int end = p.starts[r + 1];
     Request q;
     q.token0 = min(max(p.starts[r], 0), p.tokens);
-    q.n = min(max(p.starts[r + 1], q.token0), p.tokens) - q.token0;
-    q.len = max(p.lens[r], 0);
+    q.n = min(max(end, q.token0), p.tokens) - q.token0;
+    q.pos = max(p.lens[r], 0) - (max(end, q.token0) - q.token0);
     return q;
 }
 
@@ -256,12 +258,12 @@ __device__ __forceinline__ int row_tiles(const Params& p, const Request& q) {
 __device__ __forceinline__ int key_end(const Params& p, const Request& q, int tile) {
     const int rows = min((tile + 1) * kRows, q.n * p.group);
     const int last = (int)div_by(rows - 1, p.by_group);
-    return min(max(q.len - q.n + last + 1, 0), p.capacity);
+    return min(max(q.pos + last + 1, 0), p.capacity);
 }
 
 // Keys from this one on are seen by some rows of the row tile only: its first row's position + 1.
 __device__ __forceinline__ int key_open(const Params& p, const Request& q, int tile) {
-    return max(q.len - q.n + (int)div_by(tile * kRows, p.by_group) + 1, 0);
+    return max(q.pos + (int)div_by(tile * kRows, p.by_group) + 1, 0);
 }
 
 template <int TK>
@@ -988,7 +990,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const int tok = (int)div_by(row0 + row, p.by_group);
             const int end = key_end(p, cur.q, cur.tile), open = key_open(p, cur.q, cur.tile);
             // the last key this row sees
-            const int last = mine ? min(cur.q.len - cur.q.n + tok, end - 1) : INT32_MAX;
+            const int last = mine ? min(cur.q.pos + tok, end - 1) : INT32_MAX;
             const int32_t* const table = p.table + cur.r * p.ld_table;
             auto page_at = [&](int j) {  // lane i: the page of 16 keys of the unit
                 const int key = (cur.u + j) * TK + lane * 16;

@@ -313,7 +313,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     q: bfloat16 [tokens][heads][dim]; tokens starts[r] .. starts[r+1]-1 are the last ones of
     request r's lens[r], already in the cache.  Query head h reads kv head h // (heads //
     kv_heads).  scale: of the scores, dim ** -0.5 by default.  out: bfloat16 like q (by default a
-    new one); its rows behind the last token are not written.  ws: a workspace of
+    new one); its rows behind the last token are not written.  A batch of more tokens than q has
+    rows gets those rows, each at its own position.  ws: a workspace of
     paged_attention_workspace_bytes(dim) bytes, zero-filled before its first use; by default
     the cached one of (device, stream), or the graph's own during a capture.  check: synchronise
     and raise if a bounded wait in the kernel gave up."""

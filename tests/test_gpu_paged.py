@@ -344,6 +344,58 @@ def test_offsets_past_32_bits(f8):
     assert not torch.isfinite(outs[0][6:, :2, 5]).any() and torch.isfinite(outs[0][:6]).all()
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("tokens", [1, 4, 5, 20, 37, 54, 56, 57, 60])
+def test_batch_with_more_tokens_than_rows(tokens, f8):
+    """Plan, append and attend where the per-token outputs end inside a request (or before it): the
+    rows that exist are those of the whole batch, at the positions that the plan gives them."""
+    heads, kv_heads, dim, block = 12, 2, 128, 16
+    g = torch.Generator(device="cuda").manual_seed(70)
+    lens, new, blocks = [30, 0, 12], [4, 50, 3], 20
+    t, scale = sum(new), 0.02 if f8 else 1.0
+    free = torch.randperm(blocks, generator=g, device="cuda").to(torch.int32)
+    old = torch.randn((2, sum(lens), kv_heads, dim), generator=g, device="cuda").bfloat16()
+    qkv = torch.randn((t, heads + 2 * kv_heads, dim), generator=g, device="cuda").bfloat16()
+
+    def step(rows):
+        kc, vc = make_cache(g, blocks, block, kv_heads, dim, f8)
+        table = torch.full((3, 6), -1, dtype=torch.int32, device="cuda")
+        before = nv.paged_plan(ints([0] * 3), ints(lens), table, free, ints([0]), block, sum(lens))
+        nv.kv_append(old[0], old[1], kc, vc, before.slots, scale, scale)
+        plan = nv.paged_plan(before.lens, ints(new), table, free, before.head, block, rows)
+        x = torch.cat([qkv, qkv[:3]])[:rows]
+        nv.kv_append(x[:, heads:heads + kv_heads], x[:, heads + kv_heads:], kc, vc, plan.slots,
+                     scale, scale)
+        b = Batch.__new__(Batch)
+        b.lens, b.new, b.f8, b.dim, b.heads, b.kv_heads = plan.lens.tolist(), new, f8, dim, \
+            heads, kv_heads
+        b.kc, b.vc, b.k_scale, b.v_scale, b.table = kc, vc, scale, scale, table
+        b.q, b.tokens, b.starts, b.scale = x[:, :heads], t, plan.starts, dim ** -0.5
+        b.block, b.blocks, b.cols = block, blocks, table.shape[1]
+        return b, plan
+
+    whole, want = step(t)
+    ref, tol = whole.reference()
+    b, plan = step(tokens)
+    n = min(tokens, t)
+    assert plan.starts.tolist() == want.starts.tolist()
+    assert plan.positions[:n].tolist() == want.positions[:n].tolist()
+    out = torch.full_like(b.q, 7.0)
+    got = b.call(out=out)[:n].double()
+    assert torch.isfinite(got).all(), "a row saw a slot that was never written"
+    assert ((got - ref[:n]).abs() <= tol[:n]).all()
+    assert (out[n:] == 7.0).all()
+
+
+def test_starts_that_are_not_in_range():
+    # rows before 0 and behind `tokens` do not exist; those between keep their positions
+    b = Batch(71, [60, 40], [20, 30], 6, 2, 64, 16)
+    ref, tol = b.reference()
+    b.starts = ints([-8, 12, 42])
+    got = b.call(q=b.q[8:40].contiguous())
+    assert ((got.double() - ref[8:40]).abs() <= tol[8:40]).all()
+
+
 def test_rows_behind_the_last_token_stay():
     b = Batch(12, [40, 50], [3, 1], 8, 2, 128, 16, pad=5)
     out = torch.full_like(b.q, 7.0)
