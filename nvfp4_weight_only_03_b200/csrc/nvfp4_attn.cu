@@ -175,7 +175,7 @@ struct Params {
     int join_here;     // rows are few: the last CTA of a cut row tile joins its parts itself
     int32_t* arrived;  // [grid]: parts of CTA i's cut row tile written so far; zero between calls
     Cut* cuts;         // [grid]
-    float2* part_ml;   // [grid][2][128]: maximum (log2 domain) and sum
+    float2* part_ml;   // [grid][2][128]: maximum (of q.k) and sum
     float* part_o;     // [grid][2][D / 4][128][4]: a warp's rows side by side
 };
 
@@ -470,13 +470,13 @@ __device__ __noinline__ void join_rows(const Params& p, int owner, const Cut& cu
 #pragma unroll
             for (int j = 0; j < kSome; ++j) top = fmaxf(top, ml[j].x);
             // (parts that saw no key have a weight of zero and zeros to weigh)
-            const float ref = top == -INFINITY ? 0.f : top, f = exp2_approx(was - ref);
+            const float ref = top == -INFINITY ? 0.f : top, f = exp2_approx((was - ref) * p.c);
             sum *= f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] *= f;
 #pragma unroll
             for (int j = 0; j < kSome; ++j) {
-                const float w = exp2_approx(ml[j].x - ref);
+                const float w = exp2_approx((ml[j].x - ref) * p.c);
                 sum = fmaf(w, ml[j].y, sum);
                 acc[0] = fmaf(w, u[j].x, acc[0]), acc[1] = fmaf(w, u[j].y, acc[1]);
                 acc[2] = fmaf(w, u[j].z, acc[2]), acc[3] = fmaf(w, u[j].w, acc[3]);
@@ -1054,7 +1054,24 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         tmem_st(tmem + lanes + i * 32, o);
                     }
                 }
-                const float mc = m == -INFINITY ? 0.f : m * c;
+                float mc = m == -INFINITY ? 0.f : m * c;
+                // mc's rounding is a factor of all weights of this reference; with large scores it
+                // would be many powers of two, and another one for the next reference
+                if (__any_sync(~0u, mine && fabsf(mc) > 65536.f)) {
+#pragma unroll 1
+                    for (int i = 0; i < kChunks; ++i) {
+                        uint32_t s[32];
+                        tmem_ld(from + i * 32, s);
+                        tmem_wait_ld(s);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            s[e] = __float_as_uint(__uint_as_float(s[e]) -
+                                                   (m == -INFINITY ? 0.f : m));
+                        tmem_st(from + i * 32, s);
+                    }
+                    tmem_wait_st();
+                    mc = 0.f;
+                }
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
                 // a chunk is read while the one before it is worked on
                 uint32_t s[2][32];
@@ -1142,7 +1159,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 
             // ---- O: divided by the sum and written, or left as a part
             bar_sync(9, kSoftmaxWarps * 32);
-            if (F8 && mine) c = p.c * scale_of_q();  // (also if it had no unit)
+            const float unit = F8 && mine ? scale_of_q() : 1.f;
+            c = p.c * unit;  // (also if it had no unit)
             const float most = busy ? sm.row_max[(g - 1) & 1][row] : -INFINITY;  // the last unit's
             sm.row_sum[wg][row] = l > 0.f ? l * exp2_approx((m - most) * c) : l;
             bar_sync(9, kSoftmaxWarps * 32);
@@ -1152,7 +1170,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const int64_t part0 = ((int64_t)blockIdx.x * 2 + which) * kRows;
             const float inv = total == 0.f ? 0.f : p.v_scale / total;
             if (!whole && mine && wg == 0)
-                p.part_ml[part0 + row] = make_float2(most == -INFINITY ? most : most * c, total);
+                p.part_ml[part0 + row] = make_float2(most * unit, total);
             if (busy) {
                 uint16_t* const out =
                     p.o + (int64_t)(cur.q.token0 + tok) * p.ldo +

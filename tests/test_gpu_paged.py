@@ -292,6 +292,40 @@ def test_many_requests_and_long_context(f8):
     check_attention(Batch(11, [3001, 2500], [500, 333], 12, 2, 128, 16, f8))
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("q_scale", [1e4, 1e6, 3e7, 1e9])
+def test_scores_of_any_size_give_finite_rows(q_scale, f8):
+    # (the tolerance says nothing here: an fp32 score is off by more than a power of two)
+    b = Batch(83, [900, 333], [5, 40], 12, 2, 128, 16, f8, q_scale=q_scale)
+    out = b.call()
+    assert torch.isfinite(out).all() and (out.abs() <= 40).all()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("q_scale", [3e2, 1e9, 1e15])
+def test_the_only_large_score_takes_it_all(q_scale, f8):
+    """One key of the context has a large score and all others a score of zero: the row is that key's
+    value, wherever the parts of the work are cut and whatever the score's rounding."""
+    for lens, new in (([900, 333], [5, 40]), ([9000], [1]), ([5000], [300])):
+        b = Batch(84, lens, new, 12, 2, 128, 16, f8)
+        b.q.zero_()
+        b.q[:, :, 3] = q_scale
+        first, want = 0, []
+        for r, (n, m) in enumerate(zip(lens, new)):
+            pos = torch.arange(n, device="cuda")
+            page = b.table[r].long()[pos // 16]
+            k = b.kc.view(torch.uint8) if f8 else b.kc
+            k[page, pos % 16] = 0
+            k[page[7], 7, :, 3] = 0x7E if f8 else 448.0
+            v = b.vc[page[7], 7].view(torch.uint8).view(F8).float() * b.v_scale if f8 else \
+                b.vc[page[7], 7].float()
+            want.append(v.repeat_interleave(6, 0).bfloat16()[None].expand(m, 12, 128))
+        out = b.call()
+        seen = [slice(max(0, 7 - (n - m)), m) for n, m in zip(lens, new)]
+        for w, s, o in zip(want, seen, out.split(new)):
+            assert torch.equal(o[s], w[s])
+
+
 @pytest.mark.parametrize("lens,new", [([6001], [600]), ([2200, 700, 4100], [500, 700, 31])])
 def test_chunks_with_many_units_per_row_tile(lens, new):
     check_attention(Batch(40, lens, new, 24, 4, 256, 32))
