@@ -27,7 +27,10 @@
 //   in memory.  The roles share the instruction cache, so an instruction costs 4 to 10 cycles: uniform
 //   operands, elected lanes and short loops decide the time more than their count of operations.
 // * P is rounded to the MMA's 16-bit type (bf16, or f16 with the e4m3 cache): half a step, 2^-8
-//   (2^-11) of each weight.  With the e4m3 cache K is read by 8-bit MMAs as it lies, q being carried
+//   (2^-11) of each weight.  f16 weights are 2^7 times the formula's, so they reach 2^15 and keep all
+//   their bits down to 2^-21 of the row's reference; below, half a step is 2^-32 of it (without the
+//   factor 2^-25 a key, and the many small weights beside a dominating one were lost).  The sums
+//   carry the factor as well.  With the e4m3 cache K is read by 8-bit MMAs as it lies, q being carried
 //   as two e4m3 terms times a power of two per row (an error of at most 2^-17 of the row's largest).
 //   S, O, maxima and sums are fp32.
 // * Measured (B200, calls of a captured graph): 64 requests of up to 8192 keys, 24 heads on 4 of
@@ -213,6 +216,7 @@ __device__ __forceinline__ void widen_nan(uint32_t w, uint32_t& even, uint32_t& 
         : "r"(x), "r"(0x1c001c00u));  // 2^-8 twice
 }
 constexpr float kWidened = 256.f;
+constexpr float kLift = 7.f;  // f16 weights are stored times 2^kLift
 constexpr uint32_t kWidenedNan = 0x3f80;  // what widen makes of a NaN code, 480 / 256: above all others
 // The larger magnitude of each half (its sign is of no use).
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
@@ -1054,7 +1058,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         tmem_st(tmem + lanes + i * 32, o);
                     }
                 }
-                float mc = m == -INFINITY ? 0.f : m * c;
+                const float lift = F8 ? kLift : 0.f;
+                float mc = (m == -INFINITY ? 0.f : m * c) - lift;
                 // mc's rounding is a factor of all weights of this reference; with large scores it
                 // would be many powers of two, and another one for the next reference
                 if (__any_sync(~0u, mine && fabsf(mc) > 65536.f)) {
@@ -1070,7 +1075,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                         tmem_st(from + i * 32, s);
                     }
                     tmem_wait_st();
-                    mc = 0.f;
+                    mc = -lift;
                 }
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
                 // a chunk is read while the one before it is worked on

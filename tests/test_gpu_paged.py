@@ -326,6 +326,39 @@ def test_the_only_large_score_takes_it_all(q_scale, f8):
             assert torch.equal(o[s], w[s])
 
 
+@pytest.mark.parametrize("at_end", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim,n,new,requests", [
+    (24, 4, 256, 4000, 1, 1), (8, 2, 64, 700, 9, 1), (12, 2, 128, 20000, 2, 1),
+    (24, 4, 256, 1500, 1, 40), (12, 2, 128, 3000, 2, 80)])  # one request: parts with maxima of their own
+@pytest.mark.parametrize("gap", [6.0, 12.0, 17.0, 20.3, 24.6, 25.2, 28.0])
+def test_small_weights_beside_a_sink(gap, heads, kv_heads, dim, n, new, requests, at_end):
+    """e4m3: one key whose score is `gap` powers of two above all others and whose value is zero, so
+    that the result is what the small weights make of theirs.  Weights are stored as f16 times 2^7
+    of the row's reference (a sum of at least 2^7): half the smallest step is 2^-32 of it per key, in
+    place of the 2^-25 that the other tests allow."""
+    b = Batch(80, [n] * requests, [new] * requests, heads, kv_heads, dim, 32, True)
+    pos = torch.arange(n, device="cuda")
+    kk, vv = b.kc.view(torch.uint8), b.vc.view(torch.uint8)
+    sink, most = n - new if at_end else 0, []
+    for r in range(requests):
+        page = b.table[r].long()[pos // 32]
+        kk[page, pos % 32] = 0
+        kk[page[sink], sink % 32, :, 0] = 0x38  # 1.0
+        vv[page, pos % 32] &= 0x7F  # (values of one sign: errors of the weights add up)
+        vv[page[sink], sink % 32] = 0
+        most.append(vv[page, pos % 32].view(F8).double().abs().amax((0, 2)) * b.v_scale)
+    b.q.zero_()
+    b.q[:, :, 0] = gap * np.log(2) / (b.scale * b.k_scale)
+    out = b.call()
+    ref, tol = b.reference()
+    # (the reference's term is n 2^-25 times the largest value of the row's own request and kv head)
+    v = torch.stack(most).repeat_interleave(heads // kv_heads, 1).repeat_interleave(new, 0)[..., None]
+    tol = tol - n * 2.0 ** -25 * v + n * 2.0 ** -32 * v
+    assert (tol > 0).all()
+    assert (ref.abs().amax() > 0) and ((out.double() - ref).abs() <= tol).all(), \
+        ((out.double() - ref).abs() / tol).max().item()
+
+
 @pytest.mark.parametrize("lens,new", [([6001], [600]), ([2200, 700, 4100], [500, 700, 31])])
 def test_chunks_with_many_units_per_row_tile(lens, new):
     check_attention(Batch(40, lens, new, 24, 4, 256, 32))
