@@ -434,6 +434,22 @@ __device__ __noinline__ void add_not_finite(const Params& p, const int32_t* tabl
     }
 }
 
+// A unit's scores in tensor memory, less a lane's `by`.  (Rare, and so out of the way of the code that
+// every unit runs.)
+template <int TK>
+__device__ __noinline__ void subtract_scores(uint32_t at, float by) {
+#pragma unroll 1
+    for (int i = 0; i < TK / 32; ++i) {
+        uint32_t s[32];
+        tmem_ld(at + i * 32, s);
+        tmem_wait_ld(s);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - by);
+        tmem_st(at + i * 32, s);
+    }
+    tmem_wait_st();
+}
+
 // Row `row` (of all the request's) of the cursor's head.
 template <int TK>
 __device__ __forceinline__ const uint16_t* q_row(const Params& p, const Cursor<TK>& cur, int row) {
@@ -1042,7 +1058,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                 bar_arrive(1 + quarter * 2 + wg, 64);
                 if (l > 0.f) l *= exp2_approx((m - now) * c);
                 m = now;
-                if (__any_sync(~0u, rise)) {
+                // the rounding of mc, below, is a factor of all weights of this reference; with large scores
+                // it would be many powers of two, and another one for the next reference
+                const float far = fabsf(m * c);  // (infinite: no key yet)
+                bool large = mine && far > 65536.f && far < INFINITY;
+                const bool rare = __any_sync(~0u, rise || large);
+                if (rare) {
+                    large = __any_sync(~0u, large);
+                    if (large) subtract_scores<TK>(from, m == -INFINITY ? 0.f : m);
+                }
+                if (rare && __any_sync(~0u, rise)) {
                     const float f = rise ? exp2_approx((was - top) * c) : 1.f;
                     wait(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
                     __syncwarp();
@@ -1059,24 +1084,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     }
                 }
                 const float lift = F8 ? kLift : 0.f;
-                float mc = (m == -INFINITY ? 0.f : m * c) - lift;
-                // mc's rounding is a factor of all weights of this reference; with large scores it
-                // would be many powers of two, and another one for the next reference
-                if (__any_sync(~0u, mine && fabsf(mc) > 65536.f)) {
-#pragma unroll 1
-                    for (int i = 0; i < kChunks; ++i) {
-                        uint32_t s[32];
-                        tmem_ld(from + i * 32, s);
-                        tmem_wait_ld(s);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            s[e] = __float_as_uint(__uint_as_float(s[e]) -
-                                                   (m == -INFINITY ? 0.f : m));
-                        tmem_st(from + i * 32, s);
-                    }
-                    tmem_wait_st();
-                    mc = -lift;
-                }
+                const float mc = (m == -INFINITY || large ? 0.f : m * c) - lift;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
                 // a chunk is read while the one before it is worked on
                 uint32_t s[2][32];
@@ -1165,7 +1173,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             // ---- O: divided by the sum and written, or left as a part
             bar_sync(9, kSoftmaxWarps * 32);
             const float unit = F8 && mine ? scale_of_q() : 1.f;
-            c = p.c * unit;  // (also if it had no unit)
+            if (F8) c = p.c * unit;  // (also if it had no unit)
             const float most = busy ? sm.row_max[(g - 1) & 1][row] : -INFINITY;  // the last unit's
             sm.row_sum[wg][row] = l > 0.f ? l * exp2_approx((m - most) * c) : l;
             bar_sync(9, kSoftmaxWarps * 32);
