@@ -1019,6 +1019,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             };
             int page = page_at((g ^ wg) & 1);  // of this warpgroup's first unit; read a turn ahead
             float m = -INFINITY, l = 0.f, c = p.c;
+            // (a row of zeros, or of 2^-57 and less, at a tiny scale: its factor may fall below fp32's
+            // range, and a factor of zero would make a masked score NaN.  Its scores are zero either way.)
+            auto row_factor = [&](float unit) { return fmaxf(p.c * unit, 1.1754944e-38f); };
             auto scale_of_q = [&]() {  // (where scores of the row tile have arrived)
                 return __uint_as_float((uint32_t)sm.q_scale[item & 3][F8 ? row : 0] << 23);
             };
@@ -1154,7 +1157,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     fence_async_smem();
                 }
                 __syncwarp();
-                if (F8 && j < 2 && mine) c = p.c * scale_of_q();  // this warpgroup's first unit
+                if (F8 && j < 2 && mine) c = row_factor(scale_of_q());  // this warpgroup's first unit
                 if (busy) {
                     weigh(j);
                 } else {
@@ -1173,7 +1176,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             // ---- O: divided by the sum and written, or left as a part
             bar_sync(9, kSoftmaxWarps * 32);
             const float unit = F8 && mine ? scale_of_q() : 1.f;
-            if (F8) c = p.c * unit;  // (also if it had no unit)
+            if (F8) c = row_factor(unit);  // (also if it had no unit)
             const float most = busy ? sm.row_max[(g - 1) & 1][row] : -INFINITY;  // the last unit's
             sm.row_sum[wg][row] = l > 0.f ? l * exp2_approx((m - most) * c) : l;
             bar_sync(9, kSoftmaxWarps * 32);

@@ -359,6 +359,17 @@ def test_small_weights_beside_a_sink(gap, heads, kv_heads, dim, n, new, requests
         ((out.double() - ref).abs() / tol).max().item()
 
 
+@pytest.mark.parametrize("n", [40, 5000])
+def test_rows_of_zeros_at_a_tiny_scale(n):
+    # e4m3: a row's own power of two times the scale leaves fp32: all scores are zero, not NaN
+    b = Batch(81, [n, 33], [3, 33], 12, 2, 128, 16, True)
+    b.k_scale = 1e-25
+    b.q[0] = 0
+    b.q[2] *= 1e-30
+    b.q[5:9, 1::2] = 0
+    check_attention(b)
+
+
 @pytest.mark.parametrize("lens,new", [([6001], [600]), ([2200, 700, 4100], [500, 700, 31])])
 def test_chunks_with_many_units_per_row_tile(lens, new):
     check_attention(Batch(40, lens, new, 24, 4, 256, 32))
