@@ -173,7 +173,7 @@ struct Params {
     // last by far.
     int tile_cost;
     float c;           // scale * k_scale * log2(e)
-    float v_scale;
+    float v_scale;     // (1 with a bf16 cache)
     int32_t* error;
     int join_here;     // rows are few: the last CTA of a cut row tile joins its parts itself
     int32_t* arrived;  // [grid]: parts of CTA i's cut row tile written so far; zero between calls
@@ -461,7 +461,7 @@ __device__ __forceinline__ const uint16_t* q_row(const Params& p, const Cursor<T
 // ---- joining the parts of a cut row tile, in their order -------------------------------------
 // Part 0 lies with its CTA's cut at the end, the others with their cuts at the start.  A thread
 // takes 8 columns of a row, its neighbours those of the next rows, as the parts lie.
-template <int D>
+template <int D, bool F8>
 __device__ __noinline__ void join_rows(const Params& p, int owner, const Cut& cut, int item, int step) {
     for (; item < cut.rows * (D / 8); item += step) {
         const int oct = item / cut.rows, row = item - oct * cut.rows;
@@ -504,12 +504,14 @@ __device__ __noinline__ void join_rows(const Params& p, int owner, const Cut& cu
                 acc[6] = fmaf(w, v[j].z, acc[6]), acc[7] = fmaf(w, v[j].w, acc[7]);
             }
         }
-        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+        const float inv = sum == 0.f ? 0.f : (F8 ? kWidened : p.v_scale) / sum;
+        const float last = F8 ? p.v_scale : 1.f;  // (its product with the others may leave fp32's range)
         const int tok = (int)div_by(cut.row0 + row, p.by_group);
         uint4 o;
         uint32_t* const oo = &o.x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) oo[e] = pack16(false, acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        for (int e = 0; e < 4; ++e)
+            oo[e] = pack16(false, acc[2 * e] * inv * last, acc[2 * e + 1] * inv * last);
         *reinterpret_cast<uint4*>(
             p.o + (int64_t)(cut.token0 + tok) * p.ldo +
             (int64_t)(cut.head * p.group + cut.row0 + row - tok * p.group) * p.o_head_stride +
@@ -519,12 +521,12 @@ __device__ __noinline__ void join_rows(const Params& p, int owner, const Cut& cu
 
 constexpr int kJoinThreads = 256;
 
-template <int D>
+template <int D, bool F8>
 __global__ void __launch_bounds__(kJoinThreads) nvfp4_attn_join_kernel(const __grid_constant__ Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Cut cut = p.cuts[blockIdx.y];
     if (cut.parts <= 0) return;
-    join_rows<D>(p, blockIdx.y, cut, blockIdx.x * kJoinThreads + threadIdx.x,
+    join_rows<D, F8>(p, blockIdx.y, cut, blockIdx.x * kJoinThreads + threadIdx.x,
                  gridDim.x * kJoinThreads);
 }
 
@@ -1184,7 +1186,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             const bool whole = cur.u == 0 && cnt == cur.n;
             const int which = cur.u == 0 ? 1 : 0;  // this CTA's cut at its end, or at its start
             const int64_t part0 = ((int64_t)blockIdx.x * 2 + which) * kRows;
-            const float inv = total == 0.f ? 0.f : p.v_scale / total;
+            const float inv = total == 0.f ? 0.f : (F8 ? kWidened : p.v_scale) / total;
+            const float v_scale = F8 ? p.v_scale : 1.f;  // (as in join_rows)
             if (!whole && mine && wg == 0)
                 p.part_ml[part0 + row] = make_float2(most * unit, total);
             if (busy) {
@@ -1213,8 +1216,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
                                 ww[x] = pack16(false,
-                                               __uint_as_float(o[e * 8 + 2 * x]) * inv,
-                                               __uint_as_float(o[e * 8 + 2 * x + 1]) * inv);
+                                               __uint_as_float(o[e * 8 + 2 * x]) * inv * v_scale,
+                                               __uint_as_float(o[e * 8 + 2 * x + 1]) * inv *
+                                                   v_scale);
                             *reinterpret_cast<uint4*>(out + col + e * 8) = w;
                         }
                     } else if (mine) {
@@ -1263,7 +1267,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                     bar_sync(9, kSoftmaxWarps * 32);
                     if (sm.last) {
                         __threadfence();
-                        join_rows<D>(p, owner, cut, tid, kSoftmaxWarps * 32);
+                        join_rows<D, F8>(p, owner, cut, tid, kSoftmaxWarps * 32);
                         if (tid == 0) p.arrived[owner] = 0;
                     }
                 }
@@ -1336,7 +1340,7 @@ int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int 
     const int64_t each = ((int64_t)p.tokens * p.group + p.requests - 1) / p.requests;
     const int rows = each < kRows ? (int)each : kRows;
     return nvfp4_host::launch_behind(
-        nvfp4_attn_join_kernel<D>, dim3((rows * (D / 8) + kJoinThreads - 1) / kJoinThreads, grid),
+        (nvfp4_attn_join_kernel<D, F8>), dim3((rows * (D / 8) + kJoinThreads - 1) / kJoinThreads, grid),
         kJoinThreads, 0, 0, stream, p);
 }
 
@@ -1457,7 +1461,7 @@ int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cac
     const int64_t cap = a.table_columns * kv.block_size;  // (below 2^51)
     p.capacity = (int)(cap > INT32_MAX - 8192 ? INT32_MAX - 8192 : cap);
     p.c = a.scale * (f8 ? kv.k_scale : 1.f) * 1.4426950408889634f;
-    p.v_scale = f8 ? kv.v_scale * kWidened : 1.f;
+    p.v_scale = f8 ? kv.v_scale : 1.f;
     // a factor that left fp32's normal range would turn a masked score of -infinity into NaN
     if (!(p.c >= 1.1754944e-38f) || isinf(p.c)) return NVFP4_ERR_SHAPE;
     uint8_t* const ws = static_cast<uint8_t*>(workspace);

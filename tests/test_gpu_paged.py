@@ -370,6 +370,19 @@ def test_rows_of_zeros_at_a_tiny_scale(n):
     check_attention(b)
 
 
+@pytest.mark.parametrize("n", [40, 5000])
+@pytest.mark.parametrize("v_scale", [3e38, 2e36, 1e-37])
+def test_value_scales_of_the_whole_range(v_scale, n):
+    # results inside bf16's range, whatever factors the kernel forms on the way
+    b = Batch(82, [n, 33], [1, 5], 12, 2, 128, 16, True)
+    b.v_scale = v_scale
+    vv = b.vc.view(torch.uint8)
+    own = vv != 0x7F
+    if v_scale > 1:  # values below 2^-3
+        vv[own] = vv[own] & 0x9F
+    check_attention(b)
+
+
 @pytest.mark.parametrize("lens,new", [([6001], [600]), ([2200, 700, 4100], [500, 700, 31])])
 def test_chunks_with_many_units_per_row_tile(lens, new):
     check_attention(Batch(40, lens, new, 24, 4, 256, 32))
