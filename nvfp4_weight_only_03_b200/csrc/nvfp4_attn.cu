@@ -900,18 +900,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         while (left > 0 && ok) {
             const int cnt = uniform(cur.take(left));
             if (cnt <= 0) break;
-            if (item > 0 && !mbar_wait(&sm.q_free, (item - 1) & 1, stop_v)) ok = false;
-            __syncwarp();
-            if (!__all_sync(~0u, ok)) break;
+            if (item > 0) ok = __all_sync(~0u, mbar_wait(&sm.q_free, (item - 1) & 1, stop_v));
+            if (!ok) break;
             split_q();
             const int end = key_end(p, cur.q, cur.tile), open = key_open(p, cur.q, cur.tile);
             for (int i = 0; i < cnt; ++i) {
                 const int rs = raws.slot, ts = values.slot;
-                if (!mbar_wait(&sm.raw_full[rs], raws.phase, stop_v) ||
-                    !mbar_wait(&empty[NK + ts], values.phase, stop_v)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(~0u, mbar_wait(&sm.raw_full[rs], raws.phase, stop_v) &&
+                                         mbar_wait(&empty[NK + ts], values.phase, stop_v));
+                if (!ok) break;  // (all lanes or none: what follows is for whole warps)
                 const uint8_t* const src = raw + rs * C::kRaw + key * D + piece * 16;
                 uint8_t* const dst = val_ring + ts * C::kVal + key * 128;
                 // piece x of this thread: its key, and its panel

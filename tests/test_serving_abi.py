@@ -2,11 +2,13 @@
 CUDA call, so made-up addresses (far enough apart that only a planted overlap is one) do, and a
 call without fault reports the missing device.  No GPU."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 
-from conftest import cuda_ok
+from conftest import ROOT, cuda_ok
 import nvfp4_weight_only_03_b200 as nv
 from nvfp4_weight_only_03_b200 import build as nvbuild
 from nvfp4_weight_only_03_b200 import serving as sv
@@ -174,6 +176,18 @@ def test_attention_accepts(L):
         assert attn(L, table_columns=0, table=None) == ARCH
         assert attn(L, cache=dict(blocks=0, k=None, v=None)) == ARCH
         assert L.nvfp4_paged_attn_workspace_bytes(128, ctypes.byref(b)) == ARCH
+
+
+def test_attention_roles_leave_their_waits_together():
+    """A bounded wait may give up in some lanes of a warp and not in others (its last tries are apart in
+    time), and what follows it is for whole warps.  So each wait of the attention kernel that ends on
+    `stop` is inside a vote of the warp; the softmax warps', which go on either way, are one lambda."""
+    path = os.path.join(ROOT, "nvfp4_weight_only_03_b200", "csrc", "nvfp4_attn.cu")
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    statements = [s for s in re.split(r"[;{}]", text) if "mbar_wait(" in s and "stop_v" in s]
+    assert len(statements) >= 5
+    alone = [s for s in statements if "__all_sync(~0u, mbar_wait(" not in s]
+    assert [" ".join(s.split()) for s in alone] == ["if (ok && !mbar_wait(b, parity, stop_v)) ok = false"]
 
 
 # ---------------------------------------------------------------- adapters
