@@ -549,6 +549,11 @@ int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const v
                    int64_t ldy, void* out, int64_t ldo, int m, int64_t n, int64_t k,
                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* What nvfp4_lora_add returns for these arguments, the device and the workspace aside, with nothing
+ * enqueued: for programs that enqueue the work that writes y first. */
+int nvfp4_lora_check(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const void* y,
+                     int64_t ldy, void* out, int64_t ldo, int m, int64_t n, int64_t k);
+
 /* The workspace's error word after the work enqueued so far has run (synchronises the
  * stream): 0 if no kernel hit a bounded wait's limit, else a nonzero code -- 2 or 3: a wait on
  * the shared-memory ring (a weight copy that never landed), 4: a chain's dependency wait --

@@ -153,6 +153,11 @@ class Lora:
                  scales: torch.Tensor, ranks: torch.Tensor = None):
         self.a, self.b, self.index, self.scales, self.ranks = a, b, index, scales, ranks
 
+    def behind(self, y: torch.Tensor, x: torch.Tensor):
+        """Checks add(y, x) before the work that writes y is enqueued; what this returns enqueues it
+        behind that work, given the stream."""
+        return _serving.lora_behind(y, x, self.a, self.b, self.index, self.scales, self.ranks)
+
     def add(self, y: torch.Tensor, x: torch.Tensor, stream=None) -> torch.Tensor:
         return lora_add(y, x, self.a, self.b, self.index, self.scales, ranks=self.ranks, out=y,
                         stream=stream)
@@ -361,12 +366,13 @@ def gemv(w: torch.Tensor, s: torch.Tensor, g: float, x: torch.Tensor, y: torch.T
     ws: the workspace; by default the cached one of (x's device, stream).
     check: synchronise after the call and raise if a bounded wait in its kernels gave up.
     lora: adapters of the rows, added to y (lora_add in place: y is rounded before and after);
-    not with a prologue."""
+    not with a prologue.  Refused, where they do not fit, before anything is enqueued."""
     _check_lora(lora, prologue)
     n, k = _weight_args(w, s)
     x, m, ldx = _x_args(x, k, getattr(prologue, "x_dtype", torch.bfloat16))
     pro = None if prologue is None else prologue.struct(m, k)
     y, ldy = _out(y, m, n, x)
+    adapters = None if lora is None else lora.behind(y, x)
     if ws is None:
         ws = wide_workspace(n, k, m, x.device, stream) if (wide_tensor or pro) else \
             workspace(x.device, stream)
@@ -381,8 +387,8 @@ def gemv(w: torch.Tensor, s: torch.Tensor, g: float, x: torch.Tensor, y: torch.T
     _check(st, "nvfp4_gemv")
     if check:
         _check_error(ws, stream, "nvfp4_gemv")
-    if lora is not None:
-        lora.add(y, x, stream)
+    if adapters is not None:
+        adapters(stream)
     return y
 
 
@@ -464,6 +470,7 @@ def gemv_multi(weights, x: torch.Tensor, ys=None, ws: torch.Tensor = None, strea
         result.append(y)
         outs[o].w, outs[o].s, outs[o].global_scale = w.data_ptr(), s.data_ptr(), float(g)
         outs[o].y, outs[o].ldy, outs[o].n = y.data_ptr(), ldy, n
+    adapters = [l.behind(y, x) for y, l in zip(result, lora or ()) if l is not None]
     if ws is None:
         if pro is not None or wide_tensor:
             ws = wide_workspace(max(shapes, key=lambda nk: workspace_bytes_wide(nk[0], k, m))[0],
@@ -481,9 +488,8 @@ def gemv_multi(weights, x: torch.Tensor, ys=None, ws: torch.Tensor = None, strea
     _check(st, "nvfp4_gemv_multi")
     if check:
         _check_error(ws, stream, "nvfp4_gemv_multi")
-    for y, l in zip(result, lora or ()):
-        if l is not None:
-            l.add(y, x, stream)
+    for add in adapters:
+        add(stream)
     return result
 
 

@@ -390,6 +390,39 @@ int check_shape(int m, int adapters, int rank, int64_t k) {
     return NVFP4_OK;
 }
 
+// Everything that a call is refused for but the device and the workspace.
+int check_call(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const void* y, int64_t ldy,
+               void* out, int64_t ldo, int m, int64_t n, int64_t k) {
+    if (!lora) return NVFP4_ERR_NULL;
+    const nvfp4_lora_t& l = *lora;
+    const int st = check_shape(m, l.adapters, l.rank, k);
+    if (st != NVFP4_OK) return st;
+    if (n < 0 || n % 8 || n > (1 << 30) || ldx < k || ldy < n || ldo < n || l.a_ld < k ||
+        l.b_ld < l.rank || l.a_stride < 0 || l.b_stride < 0)
+        return NVFP4_ERR_SHAPE;
+    if (m == 0 || n == 0) return NVFP4_OK;
+    const bool any = l.adapters > 0 && l.rank > 0;
+    if (!y || !out || !l.index || (any && (!l.a || !l.b || !l.scales)) || (any && k && !x))
+        return NVFP4_ERR_NULL;
+    if (misaligned(x, 16) || misaligned(y, 16) || misaligned(out, 16) || misaligned(l.a, 16) ||
+        misaligned(l.b, 16) || misaligned(l.index, 4) || misaligned(l.scales, 4) ||
+        misaligned(l.ranks, 4) || ldx % 8 || ldy % 8 || ldo % 8 || l.a_ld % 8 || l.b_ld % 8 ||
+        l.a_stride % 8 || l.b_stride % 8)
+        return NVFP4_ERR_ALIGN;
+    using nvfp4_host::span;
+    const uint64_t ob = 2 * span(1, 0, 1, 0, m, ldo, n), yb = 2 * span(1, 0, 1, 0, m, ldy, n);
+    // in place is y itself, row for row
+    if (overlaps(out, ob, y, yb) && !(out == y && (ldo == ldy || m == 1))) return NVFP4_ERR_ALIAS;
+    if (overlaps(out, ob, l.index, 4ull * m)) return NVFP4_ERR_ALIAS;
+    if (any && (overlaps(out, ob, x, 2 * span(1, 0, 1, 0, m, ldx, k)) ||
+                overlaps(out, ob, l.a, 2 * span(1, 0, l.adapters, l.a_stride, l.rank, l.a_ld, k)) ||
+                overlaps(out, ob, l.b, 2 * span(1, 0, l.adapters, l.b_stride, n, l.b_ld, l.rank)) ||
+                overlaps(out, ob, l.scales, 4ull * l.adapters) ||
+                overlaps(out, ob, l.ranks, 4ull * l.adapters)))
+        return NVFP4_ERR_ALIAS;
+    return NVFP4_OK;
+}
+
 template <int STEPS>
 int launch_up(const Params& p, int sms, bool after_down, cudaStream_t stream) {
     const int64_t groups = (p.m < p.adapters ? p.m : p.adapters) + 1;
@@ -429,36 +462,19 @@ int nvfp4_lora_workspace_bytes(int m, int adapters, int rank, int64_t k, size_t*
     return NVFP4_OK;
 }
 
+int nvfp4_lora_check(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const void* y,
+                     int64_t ldy, void* out, int64_t ldo, int m, int64_t n, int64_t k) {
+    return check_call(lora, x, ldx, y, ldy, out, ldo, m, n, k);
+}
+
 int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const void* y,
                    int64_t ldy, void* out, int64_t ldo, int m, int64_t n, int64_t k,
                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    if (!lora) return NVFP4_ERR_NULL;
+    int st = check_call(lora, x, ldx, y, ldy, out, ldo, m, n, k);
+    if (st != NVFP4_OK || m == 0 || n == 0) return st;
     const nvfp4_lora_t& l = *lora;
-    int st = check_shape(m, l.adapters, l.rank, k);
-    if (st != NVFP4_OK) return st;
-    if (n < 0 || n % 8 || n > (1 << 30) || ldx < k || ldy < n || ldo < n || l.a_ld < k ||
-        l.b_ld < l.rank || l.a_stride < 0 || l.b_stride < 0)
-        return NVFP4_ERR_SHAPE;
-    if (m == 0 || n == 0) return NVFP4_OK;
     const bool any = l.adapters > 0 && l.rank > 0;
-    if (!y || !out || !l.index || (any && (!l.a || !l.b || !l.scales)) || (any && k && !x))
-        return NVFP4_ERR_NULL;
-    if (misaligned(x, 16) || misaligned(y, 16) || misaligned(out, 16) || misaligned(l.a, 16) ||
-        misaligned(l.b, 16) || misaligned(l.index, 4) || misaligned(l.scales, 4) ||
-        misaligned(l.ranks, 4) || ldx % 8 || ldy % 8 || ldo % 8 || l.a_ld % 8 || l.b_ld % 8 ||
-        l.a_stride % 8 || l.b_stride % 8)
-        return NVFP4_ERR_ALIGN;
-    using nvfp4_host::span;
-    const uint64_t ob = 2 * span(1, 0, 1, 0, m, ldo, n), yb = 2 * span(1, 0, 1, 0, m, ldy, n);
-    // in place is y itself, row for row
-    if (overlaps(out, ob, y, yb) && !(out == y && (ldo == ldy || m == 1))) return NVFP4_ERR_ALIAS;
-    if (overlaps(out, ob, l.index, 4ull * m) || overlaps(out, ob, workspace, t_bytes(m, l.rank)))
-        return NVFP4_ERR_ALIAS;
-    if (any && (overlaps(out, ob, x, 2 * span(1, 0, 1, 0, m, ldx, k)) ||
-                overlaps(out, ob, l.a, 2 * span(1, 0, l.adapters, l.a_stride, l.rank, l.a_ld, k)) ||
-                overlaps(out, ob, l.b, 2 * span(1, 0, l.adapters, l.b_stride, n, l.b_ld, l.rank)) ||
-                overlaps(out, ob, l.scales, 4ull * l.adapters) ||
-                overlaps(out, ob, l.ranks, 4ull * l.adapters)))
+    if (overlaps(out, 2 * nvfp4_host::span(1, 0, 1, 0, m, ldo, n), workspace, t_bytes(m, l.rank)))
         return NVFP4_ERR_ALIAS;
     int dev, sms;
     nvfp4_host::EncodeFn encode;

@@ -74,8 +74,10 @@ def declare(L) -> None:
                                              ctypes.POINTER(sz)]
     L.nvfp4_lora_add.argtypes = [ctypes.POINTER(LoraStruct), _p, _i64, _p, _i64, _p, _i64,
                                  ctypes.c_int, _i64, _i64, _p, sz, _p]
+    L.nvfp4_lora_check.argtypes = L.nvfp4_lora_add.argtypes[:-3]
     for f in (L.nvfp4_paged_plan, L.nvfp4_kv_append, L.nvfp4_paged_attn_workspace_bytes,
-              L.nvfp4_paged_attn, L.nvfp4_lora_workspace_bytes, L.nvfp4_lora_add):
+              L.nvfp4_paged_attn, L.nvfp4_lora_workspace_bytes, L.nvfp4_lora_add,
+              L.nvfp4_lora_check):
         f.restype = ctypes.c_int
     global _lib
     _lib = L
@@ -369,15 +371,19 @@ def paged_attention_workspace_bytes(dim: int) -> int:
     return need
 
 
-def _rows(t: torch.Tensor, name: str, m: int, n: int, index: int) -> int:
+def _rows(t: torch.Tensor, name: str, m: Optional[int], n: int, index: int):
+    """(M, row stride) of a bf16 [M][n] view; M is any if m is None."""
     if t.dtype is not _BF16:
         raise TypeError(f"{name} must be bfloat16")
-    stride = t.stride()
-    if t.shape != (m, n) or (n > 1 and stride[1] != 1):
-        raise ValueError(f"{name} must be [{m}][{n}] with unit inner stride, got {list(t.shape)}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != n or (n > 1 and stride[1] != 1):
+        raise ValueError(f"{name} must be [M][{n}] with unit inner stride, got {list(shape)}")
+    rows = shape[0]
+    if m is not None and rows != m:
+        raise ValueError(f"{name} must have {m} rows, got {rows}")
     if t.get_device() != index:
         _same_device(index, name, t)
-    return stride[0] if m > 1 else n
+    return rows, stride[0] if rows > 1 else n
 
 
 def lora_workspace_bytes(m: int, adapters: int, rank: int, k: int) -> int:
@@ -404,6 +410,31 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if _elsewhere(y, stream):
         with _entered(y, stream):
             return lora_add(y, x, a, b, index, scales, ranks, out, ws)
+    return _lora_enqueue(ws, *_lora_args(y, x, a, b, index, scales, ranks, out))
+
+
+def lora_behind(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                index: torch.Tensor, scales: torch.Tensor, ranks: Optional[torch.Tensor]):
+    """Checks lora_add(y, ..., out=y) before the work that writes y is enqueued, and returns what
+    enqueues it behind that work, given the stream."""
+    if y.get_device() < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    args = _lora_args(y, x, a, b, index, scales, ranks, y)
+    status = (_lib or _load()).nvfp4_lora_check(*args[2:])
+    if status:
+        _fail(status, "nvfp4_lora_add")
+
+    def enqueue(stream) -> None:
+        if _elsewhere(y, stream):
+            with _entered(y, stream):
+                _lora_enqueue(None, *args)
+        else:
+            _lora_enqueue(None, *args)
+    return enqueue
+
+
+def _lora_args(y, x, a, b, index, scales, ranks, out):
+    """out, the device, and the arguments of nvfp4_lora_add up to k."""
     if x.dim() == 1:
         x = x.unsqueeze(0)
     dev = y.get_device()
@@ -413,37 +444,41 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if len(sa) != 3 or len(sb) != 3:
         raise ValueError("a must be [adapters][rank][K] and b [adapters][N][rank]")
     s, rank, k = a.shape
-    n = shape[1]
-    if shape != (s, n, rank):
+    adapters, n, columns = shape
+    if adapters != s or columns != rank:
         raise ValueError(f"b must be [{s}][N][{rank}], got {list(shape)}")
     if (k > 1 and sa[2] != 1) or (rank > 1 and sb[2] != 1):
         raise ValueError("a and b must have unit inner strides")
     if a.get_device() != dev or b.get_device() != dev or scales.get_device() != dev:
         for name, t in (("a", a), ("b", b), ("scales", scales)):
             _same_device(dev, name, t)
-    m = y.shape[0]
-    ldy, ldx = _rows(y, "y", m, n, dev), _rows(x, "x", m, k, dev)
+    m, ldy = _rows(y, "y", None, n, dev)
+    _, ldx = _rows(x, "x", m, k, dev)
     if scales.dtype is not _F32:
         raise TypeError("scales must be float32")
     if scales.shape != (s,) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous [{s}]")
     if out is None:
-        out = torch.empty_like(y) if y.is_contiguous() else y.new_empty((m, n))
+        out = torch.empty_like(y) if ldy == n else y.new_empty((m, n))
         ldo = n
     else:
-        ldo = _rows(out, "out", m, n, dev)
+        ldo = ldy if out is y else _rows(out, "out", m, n, dev)[1]
+    l = LoraStruct(a.data_ptr(), sa[0] if s > 1 else rank * k, sa[1] if rank > 1 else k,
+                   b.data_ptr(), sb[0] if s > 1 else n * rank, sb[1] if n > 1 else rank,
+                   scales.data_ptr(), None if ranks is None else _ints(ranks, "ranks", s, dev),
+                   _ints(index, "index", m, dev), s, rank)
+    return out, dev, l, x.data_ptr(), ldx, y.data_ptr(), ldy, out.data_ptr(), ldo, m, n, k
+
+
+def _lora_enqueue(ws, out, dev, l, x, ldx, y, ldy, to, ldo, m, n, k) -> torch.Tensor:
+    """nvfp4_lora_add on the current device and stream."""
     st = _raw_stream(dev)
     if ws is None:
         ws, ws_at, ws_bytes = _workspace("lora", 0, dev, st)
     else:
         _same_device(dev, "ws", ws)
         ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    l = LoraStruct(a.data_ptr(), sa[0] if s > 1 else rank * k, sa[1] if rank > 1 else k,
-                   b.data_ptr(), sb[0] if s > 1 else n * rank, sb[1] if n > 1 else rank,
-                   scales.data_ptr(), None if ranks is None else _ints(ranks, "ranks", s, dev),
-                   _ints(index, "index", m, dev), s, rank)
-    status = (_lib or _load()).nvfp4_lora_add(l, x.data_ptr(), ldx, y.data_ptr(), ldy,
-                                              out.data_ptr(), ldo, m, n, k, ws_at, ws_bytes, st)
+    status = (_lib or _load()).nvfp4_lora_add(l, x, ldx, y, ldy, to, ldo, m, n, k, ws_at, ws_bytes, st)
     if status:
         _fail(status, "nvfp4_lora_add")
     return out

@@ -172,3 +172,43 @@ def test_another_stream():
     out = nv.lora_add(y, x, a, b, index, scales, stream=stream)
     stream.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("bad", ["rank", "dtype", "b", "index", "scales", "device", "ld", "k"])
+def test_refused_adapters_leave_the_projection_unwritten(bad):
+    """gemv(..., lora=) and gemv_multi(..., lora=) refuse adapters that do not fit before the
+    projection is enqueued: a caller's y stays as it was."""
+    n, k, m = 256, 512, 5
+    W = dev_weight(synth.nvfp4_weight(61, 0, n, k))
+    _, x, a, b, scales = inputs(7, m, n, k, 3, 16)
+    index = ints([0, 2, -1, 1, 0])
+    good = nv.Lora(a, b, index, scales)
+    buf = torch.full((m, n + 4), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    if bad == "rank":
+        lora = nv.Lora(a[:, :12].contiguous(), b[:, :, :12].contiguous(), index, scales)
+    elif bad == "dtype":
+        lora = nv.Lora(a.float(), b, index, scales)
+    elif bad == "b":
+        lora = nv.Lora(a, b[:, :-8], index, scales)
+    elif bad == "index":
+        lora = nv.Lora(a, b, index[:4], scales)
+    elif bad == "scales":
+        lora = nv.Lora(a, b, index, scales[:2])
+    elif bad == "device":
+        lora = nv.Lora(a, b, index.cpu(), scales)
+    elif bad == "ld":  # rows of 8 bytes more than lora_add takes; the projection alone takes them
+        lora, y = good, buf[:, :n]
+    else:
+        lora = nv.Lora(a[:, :, :504], b, index, scales)
+    error = (ValueError, TypeError, nv.Nvfp4Error)
+    with pytest.raises(error):
+        nv.gemv(*W, x, y=y, lora=lora)
+    assert (y == 7.0).all()
+    other = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(error):
+        nv.gemv_multi([W, W], x, ys=[other, y], lora=[good, lora])
+    assert (other == 7.0).all() and (y == 7.0).all()
+    # without the fault the call goes through
+    assert torch.equal(nv.gemv(*W, x, y=other, lora=good),
+                       nv.lora_add(nv.gemv(*W, x), x, a, b, index, scales))

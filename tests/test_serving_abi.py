@@ -222,6 +222,20 @@ def test_lora_refuses(L, kw, status):
     assert lora(L, **kw) == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    ({}, 0), (dict(out=at(6)), 0), (dict(m=0, y=None), 0), (dict(ranks=None), 0), (dict(m=129), ROWS),
+    (dict(rank=12), SHAPE), (dict(k=250), SHAPE), (dict(a=None), NULL), (dict(ldx=260), ALIGN),
+    (dict(out=at(5)), ALIAS),
+])
+def test_lora_check_says_what_the_call_would(L, kw, status):
+    a = dict(dict(x=at(5), ldx=256, y=at(6), ldy=512, out=at(7), ldo=512, m=3, n=512, k=256), **kw)
+    call = [a.pop(i) for i in ("x", "ldx", "y", "ldy", "out", "ldo", "m", "n", "k")]
+    l = sv.LoraStruct(**dict(LORA, **a))
+    assert L.nvfp4_lora_check(ctypes.byref(l), *call) == status
+    if status:
+        assert lora(L, **kw) == status
+
+
 def test_lora_accepts(L):
     assert lora(L, m=0, y=None) == 0 and lora(L, n=0, out=None) == 0
     if not cuda_ok():
