@@ -510,7 +510,8 @@ int nvfp4_paged_attn_workspace_bytes(int dim, size_t* bytes);
 /* workspace: 16-byte aligned, the above bytes, zero-filled before first use; the words that have to
  * be zero are so again after every call that completes.  Its first word is the error word of
  * nvfp4_workspace_error (5..10: a bounded wait gave up and the results are invalid).  Calls that may
- * run at the same time need different workspaces.
+ * run at the same time need different workspaces, and so do calls that two host threads make at the same
+ * time, on one stream too: a call may be two launches, between which no other may use its workspace.
  * Errors: NVFP4_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _WORKSPACE, _ARCH, _LAUNCH. */
 int nvfp4_paged_attn(const nvfp4_paged_attn_t* attn, const nvfp4_kv_cache_t* cache,
                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
@@ -543,7 +544,8 @@ int nvfp4_lora_workspace_bytes(int m, int adapters, int rank, int64_t k, size_t*
 
 /* M = 0..NVFP4_MAX_ROWS rows.  out may be y itself (same leading dimension); otherwise it overlaps
  * nothing that the call reads.  workspace: 16-byte aligned, the above bytes, of any content; it holds no error
- * word (nothing in the call waits).  Calls that may run at the same time need different ones.
+ * word (nothing in the call waits).  Calls that may run at the same time, or be made at the same time by
+ * two host threads, need different ones (a call is two launches).
  * Errors: NVFP4_ERR_NULL, _SHAPE, _ROWS, _ALIGN, _ALIAS, _WORKSPACE, _ARCH, _LAUNCH. */
 int nvfp4_lora_add(const nvfp4_lora_t* lora, const void* x, int64_t ldx, const void* y,
                    int64_t ldy, void* out, int64_t ldo, int m, int64_t n, int64_t k,

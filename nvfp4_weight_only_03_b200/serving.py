@@ -11,12 +11,14 @@ Lengths, tables and indexes stay on the device: no call copies anything to the h
 a captured call serves later lengths.  Every tensor of a call lies on one device, which need not
 be the current one; the call runs on that device's current stream unless `stream` names another,
 on which the inputs must then be ready.  Outputs that a call makes are allocated for the stream
-it runs on.
+it runs on.  Threads may call at the same time, on one stream or several; a workspace that a caller
+passes serves one call at a time, while it is enqueued and while it runs.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -191,9 +193,11 @@ def _cache_args(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float, v_
 
 
 def _workspace(kind: str, dim: int, index: int, st: int):
-    """(workspace, its address, bytes) for paged_attention of this head dim, or for any lora_add:
-    the cached one of (device, current stream), or, while a graph is captured, one of the
-    graph's own: two graphs never share one."""
+    """(workspace, its address, bytes, lock) for paged_attention of this head dim, or for any
+    lora_add: the cached one of (device, current stream), or, while a graph is captured, one of the
+    graph's own: two graphs never share one.  A call holds the lock while it enqueues: it may be two
+    launches that hand data over in the workspace, and another thread's, on the same stream, may not
+    come between them (the library is called without the interpreter's lock)."""
     capturing = _capturing()
     found = None if capturing else _workspaces.get((kind, dim, index, st))
     if found is None:
@@ -201,7 +205,7 @@ def _workspace(kind: str, dim: int, index: int, st: int):
         if kind == "attn":
             need = paged_attention_workspace_bytes(dim)
         else:
-            need = lora_workspace_bytes(_nv().MAX_ROWS, 1, MAX_RANK, 8)  # 128 KB, the most there is
+            need = lora_workspace_bytes(_nv().MAX_ROWS, 1, MAX_RANK, 8)  # 64 KB, the most there is
         if capturing:
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
             if kind == "attn":
@@ -209,13 +213,20 @@ def _workspace(kind: str, dim: int, index: int, st: int):
         else:
             # this cache holds the stream, so that its handle stays its own
             ws = _nv()._cached_workspace((kind, dim), need, dev, torch.cuda.current_stream(dev))
-        found = ws, ws.data_ptr(), ws.numel()
-        if not capturing:
-            _workspaces[(kind, dim, index, st)] = found
+        found = ws, ws.data_ptr(), ws.numel(), threading.Lock()
+        if not capturing:  # (the first thread's, for all)
+            found = _workspaces.setdefault((kind, dim, index, st), found)
     return found
 
 
 _workspaces: dict = {}
+
+
+def _own_workspace(ws: torch.Tensor, index: int):
+    """(address, bytes, lock) of a caller's workspace, which is the caller's to keep to one call at a
+    time."""
+    _same_device(index, "ws", ws)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), contextlib.nullcontext()
 
 
 def _fail(status: int, where: str):
@@ -342,14 +353,14 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         ldo, ho = _heads(out, "out", index)
     st = _raw_stream(index)
     if ws is None:
-        ws, ws_at, ws_bytes = _workspace("attn", dim, index, st)
+        ws, ws_at, ws_bytes, lock = _workspace("attn", dim, index, st)
     else:
-        _same_device(index, "ws", ws)
-        ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        ws_at, ws_bytes, lock = _own_workspace(ws, index)
     a = AttnStruct(q.data_ptr(), ldq, hq, out.data_ptr(), ldo, ho, tokens, heads, n,
                    table.data_ptr(), ld, cols, _ints(starts, "starts", n + 1, index),
                    _ints(lens, "lens", n, index), dim ** -0.5 if scale is None else scale)
-    status = (_lib or _load()).nvfp4_paged_attn(a, c, ws_at, ws_bytes, st)
+    with lock:
+        status = (_lib or _load()).nvfp4_paged_attn(a, c, ws_at, ws_bytes, st)
     if status:
         _fail(status, "nvfp4_paged_attn")
     if check:
@@ -474,11 +485,12 @@ def _lora_enqueue(ws, out, dev, l, x, ldx, y, ldy, to, ldo, m, n, k) -> torch.Te
     """nvfp4_lora_add on the current device and stream."""
     st = _raw_stream(dev)
     if ws is None:
-        ws, ws_at, ws_bytes = _workspace("lora", 0, dev, st)
+        ws, ws_at, ws_bytes, lock = _workspace("lora", 0, dev, st)
     else:
-        _same_device(dev, "ws", ws)
-        ws_at, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    status = (_lib or _load()).nvfp4_lora_add(l, x, ldx, y, ldy, to, ldo, m, n, k, ws_at, ws_bytes, st)
+        ws_at, ws_bytes, lock = _own_workspace(ws, dev)
+    with lock:
+        status = (_lib or _load()).nvfp4_lora_add(l, x, ldx, y, ldy, to, ldo, m, n, k, ws_at, ws_bytes,
+                                                  st)
     if status:
         _fail(status, "nvfp4_lora_add")
     return out

@@ -1,5 +1,7 @@
 """What the binding of the serving operators refuses: types, shapes, strides and devices that do not
 fit, before anything is enqueued."""
+import threading
+
 import pytest
 import torch
 
@@ -155,3 +157,36 @@ def test_lora_into_its_input():
     x = bf(3, 64)
     with pytest.raises(nv.Nvfp4Error):
         lora(x=x, a=bf(2, 8, 64), out=x)
+
+
+def test_threads_on_one_stream():
+    """Threads that call on the same stream at the same time, adapters and attention over different
+    data: each result is that of the call made alone."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF16)
+    jobs = []
+    for i in range(4):
+        k_cache, v_cache = r(150, 16, 2, 64), r(150, 16, 2, 64)
+        table = torch.randperm(150, generator=g, device="cuda").to(torch.int32).view(1, 150)
+        q, n = r(3 + 40 * (i % 2), 8, 64), 2000 + 100 * i
+        starts, lens = ints(0, q.shape[0]), ints(n)
+        y, x, a, b = r(9, 1024), r(9, 512), r(3, 64, 512), r(3, 1024, 64)
+        index, scales = ints(*[(i + m) % 3 for m in range(9)]), torch.ones(3, device="cuda") / 64
+        jobs.append((lambda q=q, k=k_cache, v=v_cache, t=table, s=starts, l=lens:
+                     nv.paged_attention(q, k, v, t, s, l),
+                     lambda y=y, x=x, a=a, b=b, i=index, s=scales: nv.lora_add(y, x, a, b, i, s)))
+    want = [[f() for f in fs] for fs in jobs]
+    same, stream = [], torch.cuda.current_stream()
+
+    def work(fs, ws):
+        with torch.cuda.stream(stream):
+            for _ in range(150):
+                got = [f() for f in fs]
+                same.append(all(torch.equal(o, w) for o, w in zip(got, ws)))
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(same) == 4 * 150 and all(same)

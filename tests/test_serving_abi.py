@@ -4,6 +4,8 @@ call without fault reports the missing device.  No GPU."""
 import ctypes
 import os
 import re
+import threading
+import time
 
 import pytest
 import torch
@@ -267,3 +269,54 @@ def test_binding_wants_cuda_tensors():
     with pytest.raises(ValueError):
         nv.lora_add(y, y, torch.zeros((1, 8, 8), dtype=torch.bfloat16),
                     torch.zeros((1, 8, 8), dtype=torch.bfloat16), i, torch.zeros(1))
+
+
+class _Enqueuer:
+    """Stands in for the library: counts how many calls with one workspace are inside at once."""
+
+    def __init__(self):
+        self.inside, self.most, self.calls = {}, 0, 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            ws = next(a for a in args if isinstance(a, int) and a in self.inside)
+            self.inside[ws] += 1
+            self.most = max(self.most, self.inside[ws])
+            time.sleep(0.002)  # (the interpreter's lock is free meanwhile, as during a library call)
+            self.inside[ws] -= 1
+            self.calls += 1
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("op", ["attention", "lora"])
+def test_threads_do_not_enqueue_into_one_workspace_at_once(monkeypatch, op):
+    """Two threads on one stream: a call's launches stay together, since the next call's would read
+    what they left in the shared workspace."""
+    lib, ws = _Enqueuer(), torch.zeros(1 << 16, dtype=torch.uint8)
+    lib.inside[ws.data_ptr()] = 0
+    monkeypatch.setattr(sv, "_lib", lib)
+    monkeypatch.setattr(sv, "_elsewhere", lambda *_: False)
+    monkeypatch.setattr(sv, "_raw_stream", lambda _: 0)
+    monkeypatch.setattr(sv, "_capturing", lambda: False)
+    monkeypatch.setattr(sv, "_workspaces", {})
+    monkeypatch.setattr(sv, "paged_attention_workspace_bytes", lambda _: ws.numel())
+    monkeypatch.setattr(sv, "lora_workspace_bytes", lambda *_: ws.numel())
+    monkeypatch.setattr(nv, "_cached_workspace", lambda *_: ws)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: None)
+    monkeypatch.setattr(torch, "device", lambda *_: None)
+    i = torch.zeros(2, dtype=torch.int32)
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    if op == "attention":
+        q, c = z(2, 4, 64), [z(3, 16, 2, 64) for _ in "kv"]
+        table = torch.zeros((1, 3), dtype=torch.int32)
+        call = lambda: nv.paged_attention(q, *c, table, i, i[:1])
+    else:
+        y, x, a, b = z(2, 8), z(2, 8), z(1, 8, 8), z(1, 8, 8)
+        call = lambda: nv.lora_add(y, x, a, b, i, torch.zeros(1))
+    threads = [threading.Thread(target=lambda: [call() for _ in range(10)]) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert lib.calls == 40 and lib.most == 1
