@@ -96,10 +96,13 @@ def _nv():
 
 # A call takes tens of microseconds on the device at most, so what it does on the host counts:
 # the usual case (the tensors' device is current, no stream given) asks torch for plain numbers
-# only; any other enters the device and the stream and starts again.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+# only; any other enters the device and the stream and starts again.  (A torch without these, as one
+# built for CPUs, has the public functions, which are slower or raise when they are called.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                     torch.cuda.is_current_stream_capturing)
 _I32, _BF16, _F8, _F32 = torch.int32, torch.bfloat16, torch.float8_e4m3fn, torch.float32
 
 

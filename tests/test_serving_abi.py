@@ -4,6 +4,8 @@ call without fault reports the missing device.  No GPU."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 import threading
 import time
 
@@ -320,3 +322,23 @@ def test_threads_do_not_enqueue_into_one_workspace_at_once(monkeypatch, op):
     for t in threads:
         t.join()
     assert lib.calls == 40 and lib.most == 1
+
+
+def test_import_without_torch_cuda_symbols():
+    """The package imports, and answers what needs no device, with a torch that has no CUDA."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice", "_cuda_isCurrentStreamCapturing"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import nvfp4_weight_only_03_b200 as nv
+assert nv.pack_info(64, 64)["n"] == 64
+i = torch.zeros(2, dtype=torch.int32)
+try:
+    nv.paged_plan(i, i, torch.zeros((2, 3), dtype=torch.int32), i, i[:1], 16, 4)
+except ValueError as e:
+    assert "CUDA device" in str(e)
+else:
+    raise AssertionError("a CPU tensor was taken")
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
