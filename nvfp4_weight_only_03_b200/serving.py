@@ -229,6 +229,8 @@ def _own_workspace(ws: torch.Tensor, index: int):
     """(address, bytes, lock) of a caller's workspace, which is the caller's to keep to one call at a
     time."""
     _same_device(index, "ws", ws)
+    if not ws.is_contiguous():  # (its elements would count for more bytes than lie there in a row)
+        raise ValueError("ws must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size(), contextlib.nullcontext()
 
 

@@ -342,3 +342,12 @@ else:
     raise AssertionError("a CPU tensor was taken")
 """
     subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
+
+
+@pytest.mark.parametrize("ws", [lambda: torch.zeros(1).expand(1 << 20), lambda: torch.zeros(64)[::2],
+                                lambda: torch.zeros((8, 8)).t()])
+def test_workspace_of_a_caller_is_contiguous(ws):
+    # (looked at on the host: a call would write past the elements that are there)
+    with pytest.raises(ValueError):
+        sv._own_workspace(ws(), -1)
+    assert sv._own_workspace(torch.zeros(64), -1)[1] == 256
