@@ -265,6 +265,8 @@ def paged_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free:
             return paged_plan(lens, new, table, free, head, block_size, tokens, out)
     index = lens.get_device()
     n = lens.numel()
+    if not 0 <= block_size < 1 << 31:  # (a C int would take it for another number)
+        raise ValueError("block_size must be in 0..2^31-1")
     cols, ld = _table_args(table, n, index)
     sizes = (n + 1, n, tokens, tokens, tokens, 1, 1)
     if out is None:

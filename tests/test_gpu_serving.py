@@ -119,6 +119,12 @@ def test_plan(bad, error):
         plan(**bad())
 
 
+def test_plan_of_a_block_size_past_32_bits():
+    for block_size in (2 ** 32 + 16, -2 ** 32 + 16, 2 ** 31, -16):
+        with pytest.raises(ValueError):
+            plan(block_size=block_size)
+
+
 def test_plan_in_place():
     p = plan()
     with pytest.raises(nv.Nvfp4Error):
