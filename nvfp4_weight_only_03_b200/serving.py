@@ -336,12 +336,16 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     new one); its rows behind the last token are not written.  A batch of more tokens than q has
     rows gets those rows, each at its own position.  ws: a workspace of
     paged_attention_workspace_bytes(dim) bytes, zero-filled before its first use; by default
-    the cached one of (device, stream), or the graph's own during a capture.  check: synchronise
-    and raise if a bounded wait in the kernel gave up."""
+    the cached one of (device, stream), or the graph's own during a capture, which nobody can look
+    into: pass one to ask workspace_error(ws) after the replays.  check: synchronise and raise if a
+    bounded wait in the kernel gave up (not during a capture)."""
     if _elsewhere(q, stream):
         with _entered(q, stream):
             return paged_attention(q, k_cache, v_cache, table, starts, lens, scale, k_scale,
                                    v_scale, out, ws, None, check)
+    if check and _capturing():
+        raise ValueError("check=True synchronises, which a capture cannot: ask workspace_error(ws) "
+                         "after a replay")
     index = q.get_device()
     c = _cache_args(k_cache, v_cache, k_scale, v_scale, index)
     ldq, hq = _heads(q, "q", index)

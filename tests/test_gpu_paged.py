@@ -548,6 +548,34 @@ def test_captured_call_serves_later_lengths():
         assert ((out.double() - ref).abs() <= tol).all()
 
 
+def test_error_word_of_captured_calls():
+    """Captured calls with a workspace of the caller's: its error word can be asked after the replays, and
+    the words that have to be zero are so again behind each call."""
+    b = Batch(18, [3000, 700], [1, 9], 12, 2, 128, 16)
+    small = Batch(20, [5000], [1], 12, 2, 128, 16)  # (joined in the kernel)
+    ws = torch.zeros(nv.paged_attention_workspace_bytes(128), dtype=torch.uint8, device="cuda")
+    want, want_small = b.call(), small.call()
+    lens, lens_small = ints(b.lens), ints(small.lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [nv.paged_attention(x.q, x.kc, x.vc, x.table, x.starts, n, scale=x.scale, ws=ws)
+                for x, n in ((b, lens), (small, lens_small), (b, lens))]
+        with pytest.raises(ValueError):
+            nv.paged_attention(b.q, b.kc, b.vc, b.table, b.starts, lens, ws=ws, check=True)
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        assert nv.workspace_error(ws) == 0
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want_small)
+        assert torch.equal(outs[2], want)
+        assert int(ws[:1024].count_nonzero()) == 0
+    ws[0] = 7  # what a wait that gave up leaves
+    with pytest.raises(RuntimeError):
+        b.call(ws=ws)
+    assert nv.workspace_error(ws) == 7
+
+
 # ---------------------------------------------------------------- the cache's rows
 
 
