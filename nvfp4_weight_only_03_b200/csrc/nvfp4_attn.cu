@@ -48,6 +48,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "nvfp4.h"
 #include "nvfp4_host.h"
 #include "nvfp4_ptx.h"
@@ -1318,7 +1320,7 @@ template <int D, bool F8>
 int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int grid,
            cudaStream_t stream) {
     using C = Cfg<D, F8>;
-    static bool ready[64];
+    static std::atomic<bool> ready[64];
     if (!ready[dev]) {
         if (cudaFuncSetAttribute(nvfp4_attn_kernel<D, F8>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,

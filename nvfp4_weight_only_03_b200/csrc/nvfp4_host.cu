@@ -1,5 +1,6 @@
-// What the serving operators ask about the current device, looked up once per device.
-#include <string.h>
+// What the serving operators ask about the current device, looked up once per device.  Threads may
+// look at the same time: each finds the same, and what one has stored is complete for the others.
+#include <atomic>
 
 #include "nvfp4_host.h"
 
@@ -7,11 +8,11 @@ namespace nvfp4_host {
 
 namespace {
 struct DeviceInfo {
-    int ok = -1;  // -1 unknown, 0 not a B200, 1 ok
-    int sms = 0;
+    std::atomic<int> ok{-1};  // -1 unknown, 0 not a B200, 1 ok: stored behind the count
+    std::atomic<int> sms{0};
 };
 DeviceInfo g_device[64];
-EncodeFn g_encode = nullptr;
+std::atomic<EncodeFn> g_encode{nullptr};
 }  // namespace
 
 int device(int* dev, int* sms, EncodeFn* encode) {

@@ -351,3 +351,22 @@ def test_workspace_of_a_caller_is_contiguous(ws):
     with pytest.raises(ValueError):
         sv._own_workspace(ws(), -1)
     assert sv._own_workspace(torch.zeros(64), -1)[1] == 256
+
+
+def test_threads_ask_for_the_device_at_once(L):
+    """The first calls of a process may come from many threads: all get the same answer."""
+    code = """
+import ctypes, threading
+import nvfp4_weight_only_03_b200 as nv
+L, got, go = nv.lib(), [], threading.Barrier(16)
+def ask():
+    b = ctypes.c_size_t()
+    go.wait()
+    for _ in range(50):
+        got.append((L.nvfp4_paged_attn_workspace_bytes(128, ctypes.byref(b)), b.value))
+threads = [threading.Thread(target=ask) for _ in range(16)]
+for t in threads: t.start()
+for t in threads: t.join()
+assert len(got) == 800 and len(set(got)) == 1, set(got)
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
