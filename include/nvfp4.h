@@ -394,7 +394,7 @@ int nvfp4_workspace_bytes_wide(int64_t n, int64_t k, int m, size_t* bytes);
  * qwen3.8-27b-nvfp4 on GB10, table "Kernels the plan launches"); the formulas are the standard
  * ones.  Lengths, tables and indexes are device memory, so a captured call serves later values.
  * They are taken within bounds: an index outside its range is skipped as each call says, never
- * followed.  Results are the same in every run.
+ * followed.  Results are the same in every run, but for a slot that nvfp4_kv_append is given twice.
  */
 #define NVFP4_MAX_REQUESTS 8192
 
@@ -465,8 +465,8 @@ int nvfp4_paged_plan(const nvfp4_paged_plan_t* plan, cudaStream_t stream);
 /* New key and value rows into the cache: row t of k and v (bf16, head h at k + t*ldk +
  * h*k_head_stride) goes to slot slots[t], i.e. page slots[t] / block_size; rows whose slot is
  * negative or past the last page are skipped.  An e4m3 cache stores e4m3_rn(x / scale) of the
- * fp32 quotient, saturated at +-448 (NaN stays NaN).  Slots that occur twice leave, value by
- * value, one of their rows.
+ * fp32 quotient, saturated at +-448 (infinite quotients too; NaN stays NaN).  A slot that occurs twice
+ * holds, value by value, one of its rows, not the same in every run.
  *   k, v 16-byte aligned;  strides >= dim and multiples of 8;  the cache overlaps no input, and its
  *   K and V are not one.
  * Errors: NVFP4_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARCH, _LAUNCH. */

@@ -24,8 +24,8 @@
 //   of one unit run under the softmax of another.
 // * Roles: 8 softmax warps, one warp each for the scores' MMAs, the values' MMAs, K, and Q and V; with
 //   an e4m3 cache 4 more that widen V to f16 (exact) and split Q.  All else goes to the MMA as it lies
-//   in memory.  The roles share the instruction cache, so an instruction costs 4 to 10 cycles: uniform
-//   operands, elected lanes and short loops decide the time more than their count of operations.
+//   in memory.  The roles share the instruction cache: uniform operands, elected lanes and short loops
+//   decide the time more than their count of operations.
 // * P is rounded to the MMA's 16-bit type (bf16, or f16 with the e4m3 cache): half a step, 2^-8
 //   (2^-11) of each weight.  f16 weights are 2^7 times the formula's, so they reach 2^15 and keep all
 //   their bits down to 2^-21 of the row's reference; below, half a step is 2^-32 of it (without the
@@ -34,12 +34,12 @@
 //   as two e4m3 terms times a power of two per row (an error of at most 2^-17 of the row's largest).
 //   S, O, maxima and sums are fp32.
 // * Measured (B200, calls of a captured graph): 64 requests of up to 8192 keys, 24 heads on 4 of
-//   256, one token each: 167 us, 6.0 TB/s, 93% of the copy rate; one request of 131072 keys: 103 us,
+//   256, one token each: 166 us, 6.05 TB/s, 94% of the copy rate; one request of 131072 keys: 103 us,
 //   80% (parts of its 4 heads' single row tiles are joined by one CTA each); 16 requests x 8 tokens,
-//   e4m3, 32 heads on 8 of 128: 94 us, 47% (widening V and the one softmax warp that has rows);
-//   2048 tokens over 16384 keys: 665 us, 1160 TFLOP/s, 69% of the matrix rate (the
-//   tensor pipe is busy for half of its cycles: scores, weights and values wait on one another).  The least call is some 7 us: lengths, first pages,
-//   keys, scores, weights and values follow on one another, each with its latency.
+//   e4m3, 32 heads on 8 of 128: 93 us, 48% (widening V and the one softmax warp that has rows);
+//   2048 tokens over 16384 keys: 705 us, 1096 TFLOP/s, 65% of the matrix rate (the tensor pipe is busy
+//   for half of its cycles).  The least call is some 7 us: lengths, first pages, keys, scores, weights
+//   and values follow on one another, each with its latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -125,8 +125,8 @@ struct Cut {
 };
 
 // n / d for 0 <= n < 2^31 by a multiplication with ceil(2^(31 + L) / d), L = ceil(log2 d), whose
-// excess over 2^(31 + L) / d is below 1 and so moves the quotient by less than 2^-L <= 1 / d.  A
-// division is twenty instructions, and the roles of a block share the instruction cache.
+// excess over 2^(31 + L) / d is below 1 and so moves the quotient by less than 2^-L <= 1 / d.  (A
+// division by a variable is a longer sequence, and the roles of a block share the instruction cache.)
 struct Divisor {
     uint32_t mul, shift;
 };
@@ -143,9 +143,8 @@ inline Divisor divisor_of(uint32_t d) {
     }
     return r;
 }
-// a / b, neither negative.  A 64-bit division takes half a microsecond and a 32-bit one a quarter, and
-// every call waits for three of them, so small ones are approximated in fp32 (off by less than one)
-// and put right.
+// a / b, neither negative.  Every call waits for three of these before its first load, so small ones are
+// approximated in fp32 (off by one at most) and put right.
 __device__ __noinline__ int64_t div64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     if ((uint64_t)(a | b) >> 22) return div64(a, b);
@@ -612,8 +611,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // kernel's bound with pages of 16 keys.  A tile is TK / box groups of `box` keys of one page
         // each (lane i knows group i's page and place), and a group is a box per panel.  Keys past the
         // end, and pages that do not exist, are boxes outside the tensor, which arrive as zeros.  One
-        // elected lane issues all of a tile's boxes: a divergent issue, a lane per box, took 95
-        // cycles a box.
+        // elected lane issues all of a tile's boxes: a divergent issue, a lane per box, was slower.
         constexpr int kMost = TK / 16;
         const bool second = warp == kQWarp;
         const int groups = TK / p.box;
@@ -1330,6 +1328,12 @@ int launch(Params p, const CUtensorMap& mk, const CUtensorMap& mv, int dev, int 
         }
         ready[dev] = true;
     }
+    // Times (B200, us) with a cost of 0 / 2 / 4 / 7 / 10 units: 64 decode requests to 2000 keys 65 / 60 / 61
+    // / 61 / 64 (D = 256, bf16), 87 / 63 / 62 / 67 / 70 (128, bf16), 88 / 70 / 66 / 71 / 76 (128, e4m3);
+    // 3 chunks of up to 1024 tokens over 4000 keys 173 / 156 / 144 / 145 / 146 (128, bf16), 245 / 200 /
+    // 166 / 148 / 152 (256, bf16), 263 / 236 / 226 / 212 / 192 (256, e4m3, where Q is split into two
+    // terms first); 2048 over 16384, 256: 754 / 761 / 763 / 791 / 769 in bf16, 706 / 775 / 774 / 756 /
+    // 780 in e4m3.
     p.tile_cost = F8 && D == 256 ? 7 : 4;
     const int st = nvfp4_host::launch_behind(nvfp4_attn_kernel<D, F8>, grid, C::kThreads, C::kSmem, 0,
                                              stream, p, mk, mv);

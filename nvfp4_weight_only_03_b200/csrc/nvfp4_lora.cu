@@ -19,8 +19,8 @@
 // * The second kernel is launched while the first runs and has its groups, its first weights and y
 //   before it waits for T.
 // * Measured (B200, calls of a captured graph): 128 rows over 48 adapters of rank 64, 10240 x 5120:
-//   23.9 us, 3.9 TB/s, 60% of the copy rate (two kernels of 5 and 9 us of traffic, each with its
-//   start and its last wave); one row of rank 16: 5.4 us, latency alone.  One kernel with a cluster
+//   23.8 us, 3.9 TB/s, 60% of the copy rate (two kernels of 5 and 9 us of traffic, each with its
+//   start and its last wave); one row of rank 16: 5.6 us, latency alone.  One kernel with a cluster
 //   per 16 rows of a group for both products took 36.5 and 8.2 us: eight SMs per adapter draw too
 //   little.
 #include <cooperative_groups.h>

@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kPlanThreads) nvfp4_plan_kernel(const PlanPara
 // Append.  A warp per token, or per token and side (K or V); a lane moves pieces of 16 bytes of the
 // cache (8 bf16 values, or 16 codes), so loads and stores are whole sectors and the slot is looked up
 // once per row.  HBM bound, 4 bytes of traffic per value (3 with an 8-bit cache).  Measured (B200):
-// 8192 tokens of 4 heads of 256 into an e4m3 cache 10.9 us, 64% of the copy rate; 128 tokens, bf16,
-// 1.9 us.
+// 8192 tokens of 4 heads of 256 into an e4m3 cache 11.1 us, 63% of the copy rate; 128 tokens, bf16,
+// 1.8 us.
 //
 // An e4m3 code is e4m3_rn(x / scale) of the fp32 quotient, saturated at 448.  A division per value was
 // the bound (a hundred instructions per eight values).  The quotient is formed from 1 / scale in two
@@ -437,7 +437,8 @@ int nvfp4_kv_append(const void* k, int64_t ldk, int64_t k_head_stride, const voi
     p.dim = c.dim;
     p.block = c.block_size;
     // Few rows: a warp each.  More than the GPU's warps can be at once: K and V of a token in one, with
-    // twice the loads under way (8192 tokens, e4m3: 10.9 us against 12.7; 128 tokens: 2.6 against 1.9).
+    // twice the loads under way (e4m3: 8192 tokens 11.1 us against 12.9, 4000 tokens 6.6 against 8.0, 128
+    // tokens 2.5 against 2.1; bf16: 13.1 against 12.5, 8.2 against 7.7, 2.7 against 1.8).
     const int most = 8 * sms;
     const bool both = tokens * 2 > (int64_t)most * (kAppendThreads / 32);
     const int64_t want = (tokens * (both ? 1 : 2) * 32 + kAppendThreads - 1) / kAppendThreads;

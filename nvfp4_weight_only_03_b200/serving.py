@@ -304,7 +304,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     k_cache, v_cache: bfloat16 or float8_e4m3fn [blocks][block_size][heads][dim] (any strides
     with an inner one of 1, the same for both); a float8 cache holds e4m3(x / scale).  slots:
     int32 [tokens], page * block_size + place; rows with a negative slot, or one past the last
-    page, are skipped."""
+    page, are skipped.  No two rows should have one slot: it would hold values of either."""
     if _elsewhere(k, stream):
         with _entered(k, stream):
             return kv_append(k, v, k_cache, v_cache, slots, k_scale, v_scale)
