@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import threading
 from typing import NamedTuple, Optional
 
@@ -231,7 +232,7 @@ def _own_workspace(ws: torch.Tensor, index: int):
     _same_device(index, "ws", ws)
     if not ws.is_contiguous():  # (its elements would count for more bytes than lie there in a row)
         raise ValueError("ws must be contiguous")
-    return ws.data_ptr(), ws.numel() * ws.element_size(), contextlib.nullcontext()
+    return ws.data_ptr(), ws.numel() * ws.element_size(), threading.Lock()
 
 
 def _fail(status: int, where: str):
@@ -370,8 +371,11 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     a = AttnStruct(q.data_ptr(), ldq, hq, out.data_ptr(), ldo, ho, tokens, heads, n,
                    table.data_ptr(), ld, cols, _ints(starts, "starts", n + 1, index),
                    _ints(lens, "lens", n, index), dim ** -0.5 if scale is None else scale)
-    with lock:
+    lock.acquire()
+    try:
         status = (_lib or _load()).nvfp4_paged_attn(a, c, ws_at, ws_bytes, st)
+    finally:
+        lock.release()
     if status:
         _fail(status, "nvfp4_paged_attn")
     if check:
@@ -397,15 +401,18 @@ def _rows(t: torch.Tensor, name: str, m: Optional[int], n: int, index: int):
     """(M, row stride) of a bf16 [M][n] view; M is any if m is None."""
     if t.dtype is not _BF16:
         raise TypeError(f"{name} must be bfloat16")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[1] != n or (n > 1 and stride[1] != 1):
-        raise ValueError(f"{name} must be [M][{n}] with unit inner stride, got {list(shape)}")
-    rows = shape[0]
-    if m is not None and rows != m:
+    stride = t.stride()
+    if len(stride) != 2:
+        raise ValueError(f"{name} must be [M][{n}], got {list(t.shape)}")
+    ld, one = stride
+    rows, columns = t.shape
+    if columns != n or (one != 1 and n > 1):
+        raise ValueError(f"{name} must be [M][{n}] with unit inner stride, got {list(t.shape)}")
+    if rows != m and m is not None:
         raise ValueError(f"{name} must have {m} rows, got {rows}")
     if t.get_device() != index:
         _same_device(index, name, t)
-    return rows, stride[0] if rows > 1 else n
+    return rows, ld if rows > 1 else n
 
 
 def lora_workspace_bytes(m: int, adapters: int, rank: int, k: int) -> int:
@@ -432,7 +439,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if _elsewhere(y, stream):
         with _entered(y, stream):
             return lora_add(y, x, a, b, index, scales, ranks, out, ws)
-    return _lora_enqueue(ws, *_lora_args(y, x, a, b, index, scales, ranks, out))
+    return _lora(y, x, a, b, index, scales, ranks, out, ws, False)
 
 
 def lora_behind(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -441,22 +448,11 @@ def lora_behind(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     enqueues it behind that work, given the stream."""
     if y.get_device() < 0:
         raise ValueError("tensors must be on a CUDA device")
-    args = _lora_args(y, x, a, b, index, scales, ranks, y)
-    status = (_lib or _load()).nvfp4_lora_check(*args[2:])
-    if status:
-        _fail(status, "nvfp4_lora_add")
-
-    def enqueue(stream) -> None:
-        if _elsewhere(y, stream):
-            with _entered(y, stream):
-                _lora_enqueue(None, *args)
-        else:
-            _lora_enqueue(None, *args)
-    return enqueue
+    return _lora(y, x, a, b, index, scales, ranks, y, None, True)
 
 
-def _lora_args(y, x, a, b, index, scales, ranks, out):
-    """out, the device, and the arguments of nvfp4_lora_add up to k."""
+def _lora(y, x, a, b, index, scales, ranks, out, ws, later: bool):
+    """lora_add on the current device and stream; or, later, its checks and what then makes the call."""
     if x.dim() == 1:
         x = x.unsqueeze(0)
     dev = y.get_device()
@@ -489,19 +485,36 @@ def _lora_args(y, x, a, b, index, scales, ranks, out):
                    b.data_ptr(), sb[0] if s > 1 else n * rank, sb[1] if n > 1 else rank,
                    scales.data_ptr(), None if ranks is None else _ints(ranks, "ranks", s, dev),
                    _ints(index, "index", m, dev), s, rank)
-    return out, dev, l, x.data_ptr(), ldx, y.data_ptr(), ldy, out.data_ptr(), ldo, m, n, k
-
-
-def _lora_enqueue(ws, out, dev, l, x, ldx, y, ldy, to, ldo, m, n, k) -> torch.Tensor:
-    """nvfp4_lora_add on the current device and stream."""
+    lib = _lib or _load()
+    if later:
+        args = (l, x.data_ptr(), ldx, y.data_ptr(), ldy, out.data_ptr(), ldo, m, n, k)
+        status = lib.nvfp4_lora_check(*args)
+        if status:
+            _fail(status, "nvfp4_lora_add")
+        return functools.partial(_lora_later, y, dev, args)
     st = _raw_stream(dev)
     if ws is None:
         ws, ws_at, ws_bytes, lock = _workspace("lora", 0, dev, st)
     else:
         ws_at, ws_bytes, lock = _own_workspace(ws, dev)
-    with lock:
-        status = (_lib or _load()).nvfp4_lora_add(l, x, ldx, y, ldy, to, ldo, m, n, k, ws_at, ws_bytes,
-                                                  st)
+    lock.acquire()  # (half the time of a with statement)
+    try:
+        status = lib.nvfp4_lora_add(l, x.data_ptr(), ldx, y.data_ptr(), ldy, out.data_ptr(), ldo, m, n,
+                                    k, ws_at, ws_bytes, st)
+    finally:
+        lock.release()
     if status:
         _fail(status, "nvfp4_lora_add")
     return out
+
+
+def _lora_later(y: torch.Tensor, dev: int, args, stream) -> None:
+    if _elsewhere(y, stream):
+        with _entered(y, stream):
+            return _lora_later(y, dev, args, None)
+    st = _raw_stream(dev)
+    _, ws_at, ws_bytes, lock = _workspace("lora", 0, dev, st)
+    with lock:
+        status = _lib.nvfp4_lora_add(*args, ws_at, ws_bytes, st)
+    if status:
+        _fail(status, "nvfp4_lora_add")
